@@ -349,6 +349,119 @@ moe_status moe_plan_set_forward_events(moe_plan* plan, moe_event_t const* events
  * plan. */
 moe_status moe_plan_set_wait_limit(moe_plan* plan, uint64_t limit_ns);
 
+/* Element type of a tensor argument. */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+/* ---- Routing rules (no counterpart on the pages, whose router is the softmax
+ * top-k of moe_block_route: the scores, bias and groups that other MoE models
+ * route by).
+ *   score         the score s_e of an expert from its logit z_e:
+ *                 MOE_SCORE_SOFTMAX  e^{z_e} / sum over all E of e^z
+ *                 MOE_SCORE_SIGMOID  1 / (1 + e^{-z_e})
+ *   n_groups      the E experts form n_groups groups of E / n_groups consecutive
+ *                 ids; 1: no groups.  1 .. 32, a divisor of E
+ *   top_groups    groups a row may use, 1 .. n_groups; k <= top_groups * E / n_groups
+ *   group_score   MOE_GROUP_MAX: a group's score is its largest key;
+ *                 MOE_GROUP_TOP2: the sum of its two largest (of those that are
+ *                 not masked)
+ *   renormalize   nonzero: a row's k weights are divided by their sum
+ *   scale         finite; multiplies every weight */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct moe_route_rule {
+    int32_t score, n_groups, top_groups, group_score, renormalize;
+    float scale;
+} moe_route_rule;
+
+/* Route rows by their logits under a rule.
+ * The key of expert e is s_e + select_bias[e] (the bias steers the choice and
+ * does not enter the weights).  The top_groups groups with the largest scores
+ * stay (equal scores: the lower group first); of their experts the k with the
+ * largest keys are taken, in that order (equal keys: the lower id first).  The
+ * order is that of the keys' real values, not of their roundings: keys too
+ * close for 32 bits are compared in 64.  Weight j is s of the j-th expert,
+ * divided by the row's sum of k scores with `renormalize`, times `scale`.
+ * Without a bias, scores order as logits do, and the logits are compared.
+ *   A logit of -inf masks its expert: score 0, and it is taken only when the
+ * chosen groups have fewer than k others.  A NaN logit is treated the same and
+ * comes after the masked ones.  A row that is masked throughout gets the
+ * lowest ids of the lowest groups with weight 0.  +inf: a sigmoid of 1; under
+ * the softmax the experts at +inf share the probability evenly.
+ *   logits       [R, E] of `dtype`, rows row_stride elements apart (>= E); E <= 1024
+ *   select_bias  [E] fp32, finite, or NULL
+ *   topk_idx     [R, k] int32 out;  k in 1 .. 32
+ *   topk_w       [R, k] fp32 out
+ *   topk_score   [R, k] fp32 out: the scores s themselves (with
+ *                moe_block_coreset_mass: the masses of the slots), or NULL
+ * Needs no workspace and counts nothing. */
+moe_status moe_route_scored(const moe_route_rule* rule, const void* logits, moe_dtype dtype,
+                            int64_t row_stride, int32_t R, int32_t E, int32_t k,
+                            const float* select_bias, int32_t* topk_idx, float* topk_w,
+                            float* topk_score, moe_stream_t stream);
+
+/* The router's logits alone: those of moe_block_route (fixed order, the bias
+ * added), for moe_route_scored.
+ *   logits  [R, E] fp32 out; other arguments and errors: moe_block_route. */
+moe_status moe_block_logits(const moe_plan* plan, const void* x, int32_t R,
+                            const int32_t* block_offsets, int32_t nb, const float* logit_bias,
+                            float* logits, void* workspace, size_t workspace_bytes,
+                            moe_stream_t stream);
+
+/* ---- 8-bit floating point (e4m3) with one fp32 scale per block of 128 (no
+ * counterpart on the pages, whose 8-bit files are integer codes).
+ * A block of values v with a = max(|v|, 2^-100) has the scale s = a / 448,
+ * rounded once to fp32, and the codes e4m3(448 v / a), halves to even; a code q
+ * stands for q * s.  A block with a NaN has a NaN scale; one with an infinity an
+ * infinite scale: what is computed from either is NaN. */
+
+/* Rows to codes, a scale for each row and block of 128 along it.
+ *   x       [R, K] of `dtype`, rows row_stride elements apart (>= K), aligned to
+ *           its element; any K >= 1 (the last block may be short)
+ *   codes   [R, K] e4m3 bytes out
+ *   scales  [ceil(K / 128), R] fp32 out (block-major) */
+moe_status moe_fp8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, int32_t R,
+                            int32_t K, void* codes, float* scales, moe_stream_t stream);
+
+/* Bytes of device workspace (256-byte aligned; it begins with the status
+ * counters, as in moe_workspace_bytes) of a moe_fp8_gemm; 0 on bad sizes. */
+size_t moe_fp8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K);
+
+/* y = x W^T on codes.
+ *   y[r, n] = sum over blocks b of xs[b, r] * ws[n / 128, b] * sum_{k in b} xq[r, k] wq[n, k]
+ * Products of codes are exact; sums are fp32; y is rounded once.
+ *   xq  [R, K] codes, xs [ceil(K / 128), R] scales (as moe_fp8_quantize writes them)
+ *   wq  [N, K] codes, ws [ceil(N / 128), ceil(K / 128)] scales, one per 128 x 128 block
+ *   y   [R, N] of `dtype` out, rows row_stride elements apart (>= N)
+ * K a multiple of 16, xq and wq 16-byte aligned; R >= 0, N >= 1. */
+moe_status moe_fp8_gemm(const void* xq, const float* xs, int32_t R, const void* wq,
+                        const float* ws, int32_t N, int32_t K, void* y, moe_dtype dtype,
+                        int64_t row_stride, void* workspace, size_t workspace_bytes,
+                        moe_stream_t stream);
+
+/* Expert weights as codes with one fp32 scale per 128 x 128 block (the last
+ * block of either dimension may be short).  Device pointers, codes 16-byte
+ * aligned:
+ *   gate, up [E, I, H]   scales [E, ceil(I / 128), H / 128]
+ *   down     [E, H, I]   scales [E, H / 128, ceil(I / 128)]
+ *   shared_gate, shared_up [Is, H], shared_down [H, Is], their scales likewise
+ *   without the leading dimension */
+typedef struct moe_fp8_weights {
+    const void *gate, *up, *down;
+    const float *gate_scale, *up_scale, *down_scale;
+    const void *shared_gate, *shared_up, *shared_down;
+    const float *shared_gate_scale, *shared_up_scale, *shared_down_scale;
+} moe_fp8_weights;
+
+/* Create a plan whose routed and shared experts are e4m3; w_router is bf16
+ * [E, H] as for moe_plan_create.  Every call works on such a plan as on a bf16
+ * one, with the same routing; the expert FFN of a row x is
+ *   x quantised per block of 128;  g, u = products as in moe_fp8_gemm;
+ *   h = silu(g) * u in fp32, quantised per block of 128;  the down product,
+ * and the outputs are weighted, staged and summed as in moe_block_forward.
+ * Errors as moe_plan_create. */
+moe_status moe_plan_create_fp8(const moe_dims* dims, const void* w_router,
+                               const moe_fp8_weights* weights, moe_plan** out);
+
 /* Copy the MOE_STATUS_WORDS counters to out[] (host); synchronises `stream`. */
 moe_status moe_read_device_status(const void* workspace, moe_stream_t stream, uint32_t* out);
 

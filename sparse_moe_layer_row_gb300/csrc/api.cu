@@ -6,8 +6,10 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 
+#include "fp8.cuh"
 #include "kernels.cuh"
 
 using namespace moe;
@@ -27,6 +29,9 @@ struct moe_plan {
     // these the scales
     int qbits;
     CUtensorMap tm_cg, tm_cu, tm_cd, tm_csg, tm_csu, tm_csd;
+    // e4m3 experts (fp8): tm_wg .. tm_sd map the codes, these are the scales
+    bool fp8;
+    moe_fp8_weights f8;
 };
 
 namespace {
@@ -158,6 +163,13 @@ bool moe::plan_view(const moe_plan* p, PlanView* out) {
     return true;
 }
 
+bool moe::encode_fp8(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2) {
+    const uint64_t d[3] = {d0, d1, d2};
+    const uint32_t box[3] = {128, 128, 1};
+    return encode_plain(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, d2 ? 3 : 2, d, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 moe_status moe::set_error(moe_status s, const char* msg) {
     g_last_error = msg ? msg : "";
     return s;
@@ -178,6 +190,49 @@ cudaError_t mark_event(const moe_plan* p, int i, cudaStream_t st) {
         cap == cudaStreamCaptureStatusActive ? cudaEventRecordExternal : cudaEventRecordDefault);
 }
 
+// The two grouped GEMMs of a plan with e4m3 experts, their inputs and outputs
+// laid over the regions that the bf16 plan uses for the same purpose: in L.h
+// (2 I bytes per pair) the codes of h (I bytes) and then its scales, in L.hs
+// (4 Is bytes per row) the shared expert's.  The codes and scales of x (H and
+// H / 32 bytes per row) are needed until the gate/up GEMM ends, and L.ys (2 H
+// bytes per pair and row) only from then on: they lie there.
+struct Fp8Regions {
+    uint8_t* xq;
+    float* xs;
+};
+Fp8Regions fp8_regions(const moe_plan* p, void* ws, int32_t R) {
+    const Layout L = make_layout(p->d);
+    uint8_t* xq = at<uint8_t>(ws, L.ys);
+    return {xq, reinterpret_cast<float*>(xq + (size_t)R * p->d.H)};   // H % 256 == 0
+}
+
+void fp8_args(const moe_plan* p, const GemmArgs& g, void* ws, int32_t R, bool down, Fp8GemmArgs* a,
+              Fp8Maps* m) {
+    const moe_dims& d = p->d;
+    const Layout L = make_layout(d);
+    const Fp8Regions x = fp8_regions(p, ws, R);
+    a->g = g;
+    a->xq = x.xq;
+    a->xs = x.xs;
+    a->hq = at<uint8_t>(ws, L.h);
+    a->hs = reinterpret_cast<float*>(a->hq + (size_t)L.max_pairs * d.I);      // I, Is % 64 == 0
+    a->shq = at<uint8_t>(ws, L.hs);
+    a->shs = reinterpret_cast<float*>(a->shq + (size_t)d.max_rows * d.Is);
+    a->max_pairs = (int)L.max_pairs;
+    a->max_rows = d.max_rows;
+    a->R = R;
+    a->sc_a = down ? p->f8.down_scale : p->f8.gate_scale;
+    a->sc_b = down ? p->f8.down_scale : p->f8.up_scale;
+    a->sc_sa = down ? p->f8.shared_down_scale : p->f8.shared_gate_scale;
+    a->sc_sb = down ? p->f8.shared_down_scale : p->f8.shared_up_scale;
+    m->w0 = down ? p->tm_wd : p->tm_wg;
+    m->w1 = down ? p->tm_wd : p->tm_wu;
+    m->s0 = down ? p->tm_sd : p->tm_sg;
+    m->s1 = down ? p->tm_sd : p->tm_su;
+    m->a0 = m->w0;   // gate/up gathers its rows itself
+    m->a1 = m->s0;
+}
+
 // The forward's launches after validation: the scatter, the two grouped GEMMs
 // and the combine.  `marked`: event 0 of the plan's forward events was already
 // recorded by the caller.
@@ -194,11 +249,11 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     // rows (few pairs per expert: its CTA-pair units would be mostly empty)
     const bool su = small || p->qbits != 0;
     const bool sd = su || R <= kStreamDownRows;
-    const int nt_gu = su ? kSmallN : kLargeNGU;
-    const int nt_dn = sd ? kSmallN : kLargeNDown;
+    const int nt_gu = p->fp8 ? kFp8Rows : su ? kSmallN : kLargeNGU;
+    const int nt_dn = p->fp8 ? kFp8Rows : sd ? kSmallN : kLargeNDown;
 
     ScatterArgs sa{block_offsets, topk_idx, w_renorm, keep, R, d.H, d.E, d.k, d.I, d.Is, nb, nt_gu, nt_dn,
-                   su ? 64 : 128, sd ? 128 : 256,
+                   p->fp8 ? kFp8GuRows : su ? 64 : 128, p->fp8 ? kFp8DnCols : sd ? 128 : 256,
                    at<int32_t>(workspace, L.prank), at<int32_t>(workspace, L.hist),
                    at<int32_t>(workspace, L.count),
                    at<int32_t>(workspace, L.expert_off), at<int32_t>(workspace, L.misc),
@@ -222,12 +277,13 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     // B rows per TMA box: k_gemm's streaming shape 32 (gate/up: x) and 16 (down:
     // h); k_down_pair a rank's 128
     const uint32_t box_gu = su ? 32 : 128, box_dn = sd ? 16 : 128;
-    bool good = encode_bf16(&gu.b1, x, d.H, (uint64_t)R, 0, box_gu, L2A) &&
+    bool good = p->fp8 ||
+                (encode_bf16(&gu.b1, x, d.H, (uint64_t)R, 0, box_gu, L2A) &&
                 encode_bf16(&gu.bg, x, d.H, (uint64_t)R, 0, 1, L2A) &&
                 encode_bf16(&dn.b0, at<void>(workspace, L.h), (uint64_t)d.I, (uint64_t)L.max_pairs, 0,
                             box_dn, L2A) &&
                 encode_bf16(&dn.b1, at<void>(workspace, L.hs), 2 * (uint64_t)d.Is,
-                            (uint64_t)d.max_rows, 0, box_dn, L2A);
+                            (uint64_t)d.max_rows, 0, box_dn, L2A));
     if (!good) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for an activation tensor");
     GemmArgs ga{at<int4>(workspace, L.units_gu), at<int32_t>(workspace, L.misc) + 1, d.E, d.H, d.I,
                 d.Is, R, static_cast<const __nv_bfloat16*>(x), at<__nv_bfloat16>(workspace, L.h),
@@ -239,21 +295,45 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
                 live ? at<int32_t>(workspace, L.shared_rows) : nullptr, p->wait_ns};
     auto mark = [&](int i) { return mark_event(p, i, st); };
     cudaError_t e = marked ? cudaSuccess : mark(0);
+    Fp8GemmArgs fg{}, fd{};
+    Fp8Maps mg{}, md{};
+    if (p->fp8) {
+        fp8_args(p, ga, workspace, R, false, &fg, &mg);
+        if (!encode_fp8(&md.a0, at<uint8_t>(workspace, L.h), (uint64_t)d.I, (uint64_t)L.max_pairs, 0) ||
+            !encode_fp8(&md.a1, at<uint8_t>(workspace, L.hs), (uint64_t)d.Is, (uint64_t)d.max_rows, 0))
+            return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activation codes");
+        const Fp8Regions rx = fp8_regions(p, workspace, R);
+        if (e == cudaSuccess)
+            e = launch_fp8_quantize(Fp8QuantArgs{x, d.H, R, d.H, rx.xq, rx.xs}, MOE_BF16, p->num_sms, st);
+        if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
+    }
     if (e == cudaSuccess) e = launch_scatter(sa, small, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "scatter launch");
-    if ((e = mark(1)) == cudaSuccess) e = launch_gemm(kGateUp, su, p->qbits, gu, ga, p->num_sms, st);
+    if ((e = mark(1)) == cudaSuccess)
+        e = p->fp8 ? launch_fp8_gemm(kGateUp, mg, fg, p->num_sms, st)
+                   : launch_gemm(kGateUp, su, p->qbits, gu, ga, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "gate/up GEMM launch");
     GemmArgs gd = ga;
     gd.units = at<int4>(workspace, L.units_dn);
     gd.n_units = at<int32_t>(workspace, L.misc) + 2;
-    if ((e = mark(2)) == cudaSuccess) e = launch_gemm(kDown, sd, p->qbits, dn, gd, p->num_sms, st);
+    if ((e = mark(2)) == cudaSuccess) {
+        if (p->fp8) {
+            const CUtensorMap a0 = md.a0, a1 = md.a1;
+            fp8_args(p, gd, workspace, R, true, &fd, &md);
+            md.a0 = a0;
+            md.a1 = a1;
+            e = launch_fp8_gemm(kDown, md, fd, p->num_sms, st);
+        } else {
+            e = launch_gemm(kDown, sd, p->qbits, dn, gd, p->num_sms, st);
+        }
+    }
     if (e != cudaSuccess) return cuda_fail(e, "down GEMM launch");
     CombineArgs ca{at<__half>(workspace, L.ys), at<uint8_t>(workspace, L.ysx),
                    (int)(L.max_pairs + d.max_rows), at<int32_t>(workspace, L.misc) + 4,
                    at<int32_t>(workspace, L.inv), R, d.H, d.k,
                    (int)L.max_pairs, static_cast<__nv_bfloat16*>(y), y_f32,
                    at<uint32_t>(workspace, L.status), live, at<int32_t>(workspace, L.shared_inv)};
-    if ((e = mark(3)) == cudaSuccess) e = launch_combine(ca, p->num_sms, !sd, st);
+    if ((e = mark(3)) == cudaSuccess) e = launch_combine(ca, p->num_sms, !sd && !p->fp8, st);
     if (e == cudaSuccess) e = mark(4);
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
     return ok();
@@ -395,6 +475,59 @@ moe_status moe_plan_create_quantized(const moe_dims* dims, const void* w_router,
     return ok();
 }
 
+moe_status moe_plan_create_fp8(const moe_dims* dims, const void* w_router,
+                               const moe_fp8_weights* w, moe_plan** out) {
+    if (!out) return fail(MOE_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    moe_status s = check_dims(dims);
+    if (s != MOE_OK) return s;
+    if (!w) return fail(MOE_ERR_INVALID_ARG, "fp8 weights are NULL");
+    const void* ws[7] = {w_router, w->gate, w->up, w->down, w->shared_gate, w->shared_up, w->shared_down};
+    const char* names[7] = {"w_router", "gate", "up", "down", "shared_gate", "shared_up", "shared_down"};
+    for (int i = 0; i < 7; ++i)
+        if (!ws[i] || !aligned(ws[i], 16))
+            return fail(MOE_ERR_INVALID_ARG, "%s is NULL or not 16-byte aligned", names[i]);
+    const float* sc[6] = {w->gate_scale, w->up_scale, w->down_scale, w->shared_gate_scale,
+                          w->shared_up_scale, w->shared_down_scale};
+    for (int i = 0; i < 6; ++i)
+        if (!sc[i] || !aligned(sc[i], 4))
+            return fail(MOE_ERR_INVALID_ARG, "%s_scale is NULL or misaligned", names[i + 1]);
+    moe_plan* p = new (std::nothrow) moe_plan();
+    if (!p) return fail(MOE_ERR_CUDA, "out of host memory");
+    p->d = *dims;
+    cudaError_t e = cudaGetDevice(&p->device);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
+    if (e == cudaSuccess) e = fp8_gemm_set_attributes();
+    if (e == cudaSuccess) e = route_tc_set_attributes();
+    if (e != cudaSuccess) {
+        delete p;
+        return cuda_fail(e, "device query");
+    }
+    const moe_dims& d = *dims;
+    p->fp8 = true;
+    p->f8 = *w;
+    p->wr = w_router;
+    p->wg = w->gate; p->wu = w->up; p->wd = w->down;
+    p->sg = w->shared_gate; p->su = w->shared_up; p->sd = w->shared_down;
+    bool good = encode_fp8(&p->tm_wg, w->gate, d.H, d.I, d.E) && encode_fp8(&p->tm_wu, w->up, d.H, d.I, d.E) &&
+                encode_fp8(&p->tm_wd, w->down, d.I, d.H, d.E) &&
+                encode_fp8(&p->tm_sg, w->shared_gate, d.H, d.Is, 0) &&
+                encode_fp8(&p->tm_su, w->shared_up, d.H, d.Is, 0) &&
+                encode_fp8(&p->tm_sd, w->shared_down, d.Is, d.H, 0);
+    p->tc_route = d.E <= 256 && d.E % 16 == 0 && d.k <= 16 && d.H <= 8192;
+    if (good && p->tc_route)
+        good = encode_bf16(&p->tm_wr, w_router, d.H, d.E, 0,
+                           (uint32_t)((d.E > 128 && d.E % 32 == 0) ? d.E / 2 : d.E),
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (!good) {
+        delete p;
+        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for an e4m3 weight tensor");
+    }
+    *out = p;
+    return ok();
+}
+
 void moe_plan_destroy(moe_plan* plan) { delete plan; }
 
 moe_status moe_block_route(const moe_plan* p, const void* x, int32_t R,
@@ -444,6 +577,30 @@ moe_status moe_block_route_probs(const moe_plan* p, const void* x, int32_t R,
                 topk_w, at<uint32_t>(workspace, L.status), topk_p};
     e = launch_route(a, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "route launch");
+    return ok();
+}
+
+moe_status moe_block_logits(const moe_plan* p, const void* x, int32_t R,
+                            const int32_t* block_offsets, int32_t nb, const float* logit_bias,
+                            float* logits, void* workspace, size_t workspace_bytes,
+                            moe_stream_t stream) {
+    moe_status s = check_call(p, R, block_offsets, nb, workspace, workspace_bytes);
+    if (s != MOE_OK) return s;
+    if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x is NULL or not 16-byte aligned");
+    if (!logits || !aligned(logits, 4)) return fail(MOE_ERR_INVALID_ARG, "logits NULL or misaligned");
+    if (logit_bias && !aligned(logit_bias, 4)) return fail(MOE_ERR_INVALID_ARG, "logit_bias misaligned");
+    if (R == 0) return ok();
+    const Layout L = make_layout(p->d);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(at<uint8_t>(workspace, L.route_cnt), 0,
+                                    sizeof(uint32_t) * (size_t)R, st);
+    if (e != cudaSuccess) return cuda_fail(e, "route counters");
+    RouteArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(p->wr),
+                logit_bias, block_offsets, R, p->d.H, p->d.E, p->d.k, nb, logits,
+                at<uint32_t>(workspace, L.route_cnt), nullptr, nullptr,
+                at<uint32_t>(workspace, L.status), nullptr};
+    e = launch_route(a, p->num_sms, st);
+    if (e != cudaSuccess) return cuda_fail(e, "logits launch");
     return ok();
 }
 

@@ -1,0 +1,586 @@
+// Block-scaled e4m3 products on the 5th-generation tensor core (sm_103a): the
+// dense y = x W^T, and the grouped gate/up and down GEMMs of the expert FFN.
+//
+//   y[r, n] = sum over blocks b of 128 along K of
+//             sx[b, r] * sw[n / 128, b] * sum_{k in b} qx[r, k] qw[n, k]
+//
+// The scales of a row and of a weight block differ from block to block along
+// K, so the tensor core may sum one block of K only (four MMAs of K = 32); the
+// eight promotion warps then read that partial sum from TMEM, multiply it by
+// sx * sw and add it to accumulators in registers, in fp32.  Two TMEM buffers
+// let the tensor core work on the next block of K meanwhile.
+//
+// A unit of work is 128 rows (the MMA's M, so a TMEM lane is a row, its scale
+// one number per thread) by 256 weight rows (N):
+//   gate/up  128 gate rows and the 128 up rows of the same intermediate
+//            indices.  h = silu(g) u in fp32 is rounded to e4m3 with one scale
+//            per row and 128 indices (fp8.cuh): a row's 128 values lie in the
+//            two threads of its lane, which exchange their largest magnitude
+//            through shared memory.
+//   down     256 hidden outputs; the pair's weighted output is staged in fp16
+//            with a power-of-two exponent per 32 columns, as k_combine reads it.
+//   dense    256 outputs, stored in bf16, fp16 or fp32.
+//
+// Persistent, one CTA per SM, 512 threads:
+//   warp 0 lane 0   TMA producer: weight tiles (2 x 16 KB) and, but for
+//                   gate/up, the rows' tile (16 KB) into a ring of 4 stages
+//   warp 1          TMEM allocation; lane 0 issues the MMAs
+//   warp 2 lane 0   gate/up: forwarder; when a stage's rows have landed it
+//                   fences them for the async proxy and tells the MMA thread
+//   warps 4..11     promotion and epilogue: lane quadrant warp & 3, columns by
+//                   warpgroup
+//   warps 12..15    gate/up: loaders, gather the unit's rows of x by 16-byte
+//                   cp.async into the swizzled tile
+// Registers are moved from the other warpgroups to the promotion warps, which
+// hold 128 accumulators each.
+// Every wait is bounded: a wait that gives up raises a CTA-wide abort flag and
+// a device status counter, and all roles leave their loops; before the CTA
+// exits its copies and MMAs in flight are waited for (with their own limit),
+// and only then is the TMEM released.
+#include "fp8.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
+constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
+
+constexpr int kStages = 4;
+constexpr int kThreads = 512;
+constexpr int kTile = 128 * 128;                 // 128 rows x 128 codes
+constexpr int kStageBytes = 3 * kTile;           // rows, weights 0, weights 1
+constexpr int kAmaxOff = kStages * kStageBytes;  // uint32 [2 units][2 warpgroups][128 rows]
+constexpr int kBarOff = kAmaxOff + 2 * 2 * 128 * 4;
+constexpr int kSmem = kBarOff + 256 + 1024;
+constexpr int kTmemCols = 512;                   // two buffers of 256 columns
+// registers per thread after the split: the pool is what the CTA was launched
+// with (kThreads x kLaunchRegs), checked on the host before any launch
+constexpr int kLaunchRegs = 128, kFewRegs = 56, kManyRegs = 200;
+static_assert(256 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(8 * (4 * kStages + 6) + 12 <= 256, "barrier region");
+
+// kind::f8f6f4 with e4m3 A and B (format 0), fp32 accumulator, both K-major.
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
+    return 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 32 lanes x 32 columns of TMEM into registers; complete after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// acc[j] += f * v[j], two at a time (fma.rn.f32x2: each half as fmaf).
+__device__ __forceinline__ void promote32(float* acc, const uint32_t (&v)[32], float f) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+        asm("{\n\t.reg .b64 a, b, c;\n\t"
+            "mov.b64 a, {%2, %3};\n\t"
+            "mov.b64 b, {%4, %4};\n\t"
+            "mov.b64 c, {%0, %1};\n\t"
+            "fma.rn.f32x2 c, a, b, c;\n\t"
+            "mov.b64 {%0, %1}, c;\n\t}"
+            : "+f"(acc[j]), "+f"(acc[j + 1])
+            : "r"(v[j]), "r"(v[j + 1]), "f"(f));
+}
+
+__device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bf162_bits(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
+           const __grid_constant__ CUtensorMap tmS0, const __grid_constant__ CUtensorMap tmS1,
+           const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+           Fp8GemmArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (sbase - raw);
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + kBarOff);  // [S] tiles landed
+    uint64_t* rfull = full + kStages;                               // [S] gathered rows landed
+    uint64_t* rready = rfull + kStages;                             // [S] ... and fenced
+    uint64_t* empty = rready + kStages;                             // [S] stage free
+    uint64_t* tfull = empty + kStages;                              // [2] partial sums ready
+    uint64_t* tempty = tfull + 2;                                   // [2] buffer free
+    uint64_t* xbar = tempty + 2;                                    // amax exchange
+    uint64_t* dbar = xbar + 1;                                      // MMA drain
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dbar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* never = abort_flag + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(rfull + s, 128);   // the loader threads' copies
+            mbar_init(rready + s, 1);    // the forwarder
+            mbar_init(empty + s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + i, 1);
+            mbar_init(tempty + i, 256);
+        }
+        mbar_init(xbar, 256);
+        mbar_init(dbar, 1);
+        *abort_flag = 0;
+        *never = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();   // see common.cuh
+    pdl_trigger();
+
+    const int E = a.g.E;
+    const int dense_m = (a.N + 255) / 256;
+    const int nunits = MODE == kDense ? dense_m * ((a.R + kFp8Rows - 1) / kFp8Rows)
+                                      : __ldg(a.g.n_units);
+    const int nact = active_workers(nunits, (int)gridDim.x);   // balanced rounds
+    const int ufirst = (int)blockIdx.x < nact ? (int)blockIdx.x : nunits;
+    // unit u: group, weight tile, first row, rows
+    auto unit = [&](int u) -> int4 {
+        if (MODE != kDense) return __ldg(a.g.units + u);
+        const int c = u / dense_m, m = u - c * dense_m;
+        return make_int4(0, m, c * kFp8Rows, min(kFp8Rows, a.R - c * kFp8Rows));
+    };
+    auto valid = [&](const int4 un) {
+        return MODE == kDense || unit_valid(un, a.g, kFp8Rows, MODE == kDown, kFp8GuRows, kFp8DnCols);
+    };
+    // blocks of 128 along K of a unit of group g
+    auto blocks = [&](int g) {
+        return MODE == kDense ? fp8_blocks(a.K)
+             : MODE == kGateUp ? a.g.H / kFp8Block : fp8_blocks(g == E ? a.g.Is : a.g.I);
+    };
+    auto give_up = [&]() {
+        if (!*abort_flag) { *abort_flag = 1; status_add(a.g.status, MOE_STATUS_WAIT_TIMEOUT, 1); }
+    };
+    const uint64_t kWaitNs = a.g.wait_ns ? a.g.wait_ns : kWaitLimitNs;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------ TMA producer
+            int stage = 0, nfills = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact) {
+                const int4 un = unit(u);
+                if (!valid(un)) continue;
+                const int g = un.x, m = un.y, start = un.z;
+                const bool sh = MODE != kDense && g == E;
+                const int nkb = blocks(g);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sA = sbase + stage * kStageBytes, sW = sA + kTile;
+                    uint64_t* bar = full + stage;
+                    const int kc = kb * kFp8Block;
+                    mbar_expect_tx(bar, (uint32_t)(MODE == kGateUp ? 2 : 3) * kTile);
+                    if (MODE == kGateUp) {
+                        if (sh) {
+                            tma_load_2d(sW, &tmS0, kc, m * 128, bar);
+                            tma_load_2d(sW + kTile, &tmS1, kc, m * 128, bar);
+                        } else {
+                            tma_load_3d(sW, &tmW0, kc, m * 128, g, bar);
+                            tma_load_3d(sW + kTile, &tmW1, kc, m * 128, g, bar);
+                        }
+                    } else if (MODE == kDown) {
+                        for (int i = 0; i < 2; ++i) {
+                            if (sh) tma_load_2d(sW + i * kTile, &tmS0, kc, m * 256 + i * 128, bar);
+                            else tma_load_3d(sW + i * kTile, &tmW0, kc, m * 256 + i * 128, g, bar);
+                        }
+                        tma_load_2d(sA, sh ? &tmA1 : &tmA0, kc, start, bar);
+                    } else {
+                        for (int i = 0; i < 2; ++i)
+                            tma_load_2d(sW + i * kTile, &tmW0, kc, m * 256 + i * 128, bar);
+                        tma_load_2d(sA, &tmA0, kc, start, bar);
+                    }
+                    ++nfills;
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // drain: the last fill of every stage has landed (consumed or not)
+            for (int s = 0; s < kStages; ++s) {
+                if (nfills < kStages && s >= nfills) break;
+                const uint32_t par = s < stage ? phase : (phase ^ 1u);
+                if (!mbar_wait_bounded(full + s, par, never, kDrainLimitNs)) give_up();
+            }
+        } else if (warp == 1 && lane == 0) {
+            // -------------------------------------------------------- MMA issuer
+            const uint32_t idesc = idesc_e4m3_f32(128, 256);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact) {
+                const int4 un = unit(u);
+                if (!valid(un)) {
+                    status_add(a.g.status, MOE_STATUS_BAD_UNIT, 1);
+                    continue;
+                }
+                const int nkb = blocks(un.x);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_bounded(full + stage, phase, abort_flag, kWaitNs) ||
+                        (MODE == kGateUp &&
+                         !mbar_wait_bounded(rready + stage, phase, abort_flag, kWaitNs)) ||
+                        !mbar_wait_bounded(tempty + buf, bphase ^ 1u, abort_flag, kWaitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sA = sbase + stage * kStageBytes, sW = sA + kTile;
+                    const uint32_t d = tmem + (uint32_t)(buf * 256);
+                    // the two weight tiles follow each other: N = 256 rows of 128 bytes
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_e4m3(d, smem_desc_sw128(sA + kk * 32), smem_desc_sw128(sW + kk * 32),
+                                    idesc, kk != 0);
+                    tc_commit(empty + stage);
+                    tc_commit(tfull + buf);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    buf ^= 1;
+                    if (buf == 0) bphase ^= 1u;
+                }
+            }
+            // drain: arrives once every MMA issued above has completed
+            tc_commit(dbar);
+            if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs)) give_up();
+        } else if (MODE == kGateUp && warp == 2 && lane == 0) {
+            // --------------------------------------------------------- forwarder
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact) {
+                const int4 un = unit(u);
+                if (!valid(un)) continue;
+                const int nkb = blocks(un.x);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_bounded(rfull + stage, phase, abort_flag, kWaitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_smem();   // the rows were written by cp.async
+                    mbar_arrive(rready + stage);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (MODE == kGateUp) {
+            // ----------------------------------------------------------- loaders
+            // Row i of the unit is copied by 8 threads, 16 bytes each: chunk c of
+            // row i lands at chunk c ^ (i & 7) (the 128-byte swizzle).  Rows past
+            // the unit's are not loaded: they feed only TMEM lanes never stored.
+            const int lt = threadIdx.x - 384;            // 0..127
+            const int r16 = lt >> 3, ch = lt & 7;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact) {
+                const int4 un = unit(u);
+                if (!valid(un)) continue;
+                const int g = un.x, start = un.z, n = un.w;
+                int row[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = j * 16 + r16;
+                    row[j] = i >= n ? -1
+                           : g != E ? __ldg(a.g.pair_row + start + i)
+                           : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + i) : start + i);
+                }
+                const int nkb = blocks(g);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sA = sbase + stage * kStageBytes;
+                    const uint8_t* col = a.xq + kb * kFp8Block + ch * 16;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int i = j * 16 + r16;
+                        if (row[j] >= 0 && row[j] < a.g.R)
+                            cp_async16(sA + i * 128 + ((ch ^ (i & 7)) << 4), col + (int64_t)row[j] * a.g.H);
+                    }
+                    cp_async_arrive(rfull + stage);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");   // nothing of this thread lands later
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        // ------------------------------------------------ promotion and epilogue
+        const int q = warp & 3;           // TMEM lane quadrant this warp may read
+        const int wg = (warp - 4) >> 2;   // 0 or 1
+        const int t = q * 32 + lane;      // row of the unit
+        // the thread's two groups of 64 columns: gate/up: g and u of the same 64
+        // intermediate indices; else 128 columns in a row
+        const uint32_t col0 = (uint32_t)(MODE == kGateUp ? wg * 64 : wg * 128);
+        const uint32_t col1 = (uint32_t)(MODE == kGateUp ? 128 + wg * 64 : wg * 128 + 64);
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
+        uint32_t* s_amax = reinterpret_cast<uint32_t*>(base + kAmaxOff);
+        int buf = 0, upar = 0;
+        uint32_t bphase = 0, xphase = 0;
+        bool alive = true;
+        for (int u = ufirst; alive && u < nunits; u += nact) {
+            const int4 un = unit(u);
+            if (!valid(un)) continue;
+            const int g = un.x, m = un.y, start = un.z, n = un.w;
+            const bool sh = MODE != kDense && g == E;
+            const int nkb = blocks(g);
+            const int tc = min(t, n - 1);   // rows past the unit's repeat its last
+            // the row's scales (one per block of K, ldx apart) and the weight blocks'
+            const float *px, *pw0, *pw1;
+            int64_t ldx;
+            if (MODE == kGateUp) {
+                int row = sh ? (a.g.shared_rows ? __ldg(a.g.shared_rows + start + tc) : start + tc)
+                             : __ldg(a.g.pair_row + start + tc);
+                row = min(max(row, 0), a.g.R - 1);
+                px = a.xs + row;
+                ldx = a.g.R;
+                const int mb = fp8_blocks(sh ? a.g.Is : a.g.I);
+                const int64_t o = ((int64_t)(sh ? 0 : g) * mb + m) * nkb;
+                pw0 = (sh ? a.sc_sa : a.sc_a) + o;
+                pw1 = (sh ? a.sc_sb : a.sc_b) + o;
+            } else if (MODE == kDown) {
+                px = (sh ? a.shs : a.hs) + start + tc;
+                ldx = sh ? a.max_rows : a.max_pairs;
+                const int hb = a.g.H / kFp8Block;
+                pw0 = pw1 = (sh ? a.sc_sa : a.sc_a) + ((int64_t)(sh ? 0 : g) * hb + 2 * m + wg) * nkb;
+            } else {
+                px = a.xs + start + tc;
+                ldx = a.R;
+                const int nb = fp8_blocks(a.N);
+                pw0 = pw1 = a.sc_a + (int64_t)min(2 * m + wg, nb - 1) * nkb;
+            }
+            float acc[128];
+#pragma unroll
+            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            // h's scales were written by the gate/up kernel: not through the read-only path
+            float sx = __ldcg(px), sw0 = __ldg(pw0), sw1 = __ldg(pw1);
+            for (int kb = 0; kb < nkb; ++kb) {
+                const float f0 = sx * sw0, f1 = sx * sw1;
+                if (kb + 1 < nkb) {   // the next block's scales, while the MMA runs
+                    sx = __ldcg(px + (int64_t)(kb + 1) * ldx);
+                    sw0 = __ldg(pw0 + kb + 1);
+                    sw1 = __ldg(pw1 + kb + 1);
+                }
+                const bool ok = mbar_wait_bounded(tfull + buf, bphase, abort_flag, kWaitNs);
+                if (__any_sync(0xffffffffu, !ok)) { give_up(); alive = false; break; }
+                tc_fence_after();
+                const uint32_t tb = tq + (uint32_t)(buf * 256);
+                uint32_t v[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(tb + (c < 2 ? col0 + 32 * c : col1 + 32 * (c - 2)), v);
+                    tmem_ld_wait();
+                    if (c == 3) {   // the buffer has been read: hand it back
+                        tc_fence_before();
+                        mbar_arrive(tempty + buf);
+                    }
+                    promote32(acc + 32 * c, v, c < 2 ? f0 : f1);
+                }
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1u;
+            }
+            if (!alive) break;
+            if (MODE == kGateUp) {
+                // h of the 64 indices, in place over g
+                uint32_t mx = 0;
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    acc[j] = silu_fast(acc[j]) * acc[64 + j];
+                    mx = max(mx, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
+                }
+                // the row's largest magnitude: the other half is in the other
+                // warpgroup.  Two buffers, taken in turn: a warp can be at most one
+                // exchange ahead of another.
+                uint32_t* am = s_amax + upar * 256;
+                am[wg * 128 + t] = mx;
+                mbar_arrive(xbar);
+                const bool ok = mbar_wait_bounded(xbar, xphase, abort_flag, kWaitNs);
+                if (__any_sync(0xffffffffu, !ok)) { give_up(); alive = false; break; }
+                mx = max(mx, am[(wg ^ 1) * 128 + t]);
+                upar ^= 1;
+                xphase ^= 1u;
+                const float bm = __uint_as_float(fp8_amax_bits(mx));
+                // one more rounding than the quotient of fp8.cuh: h is a sum's rounding away
+                // from its exact value anyway
+                const float inv = __fdiv_rn(448.0f, bm);
+                const int ld = sh ? a.g.Is : a.g.I;
+                const int i0 = m * 128 + wg * 64;   // I, Is are multiples of 64
+                if (t < n) {
+                    const int64_t p = start + t;
+                    if (i0 < ld) {
+                        uint8_t* out = (sh ? a.shq : a.hq) + p * ld + i0;
+#pragma unroll
+                        for (int j = 0; j < 64; j += 16) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = fp8_pair(acc[j + 4 * i] * inv, acc[j + 4 * i + 1] * inv) |
+                                       fp8_pair(acc[j + 4 * i + 2] * inv, acc[j + 4 * i + 3] * inv) << 16;
+                            store16(out + j, w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    if (wg == 0)
+                        (sh ? a.shs : a.hs)[(int64_t)m * (sh ? a.max_rows : a.max_pairs) + p] =
+                            __fdiv_rn(bm, 448.0f);
+                }
+            } else if (MODE == kDown) {
+                const int64_t p = (int64_t)(sh ? a.g.shared_row0 : 0) + start + t;
+                const float w = sh ? 1.0f : __ldg(a.g.pair_w + start + tc);
+                bool big = false;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    // fp16 holds |v| < 65504: a quarter of 32 columns whose largest
+                    // finite magnitude is 2^15 or more is stored as v * 2^-s, s its
+                    // exponent above 2^14 (see gemm.cu)
+                    uint32_t mb = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        acc[c + j] *= w;
+                        const uint32_t ab = __float_as_uint(acc[c + j]) & 0x7FFFFFFFu;
+                        mb = max(mb, ab < 0x7F800000u ? ab : 0u);
+                    }
+                    const int sft = (int)(mb >> 23) - 141;
+                    const uint32_t st = sft > 0 ? (uint32_t)sft : 0u;
+                    if (st) {
+                        big = true;
+                        const float f = __uint_as_float((127u - st) << 23);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[c + j] *= f;
+                    }
+                    if (t < n) {
+                        const int h0 = m * 256 + wg * 128 + c;
+                        __half* out = a.g.ys + p * a.g.H + h0;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            store16(out + j, half2_bits(acc[c + j], acc[c + j + 1]),
+                                    half2_bits(acc[c + j + 2], acc[c + j + 3]),
+                                    half2_bits(acc[c + j + 4], acc[c + j + 5]),
+                                    half2_bits(acc[c + j + 6], acc[c + j + 7]));
+                        a.g.ysx[(int64_t)(h0 >> 5) * a.g.ld_x + p] = (uint8_t)st;
+                    }
+                }
+                if (big && t < n) *a.g.scaled = 1;
+            } else if (t < n) {
+                const int n0 = m * 256 + wg * 128;
+                const int64_t o = (int64_t)(start + t) * a.ldy + n0;
+                if (a.ydtype == MOE_F32) {
+                    float* y = static_cast<float*>(a.y) + o;
+#pragma unroll
+                    for (int j = 0; j < 128; j += 4) {
+                        if (a.y_vec && n0 + j + 4 <= a.N)
+                            store16(y + j, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                                    __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]));
+                        else
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (n0 + j + i < a.N) y[j + i] = acc[j + i];
+                    }
+                } else {
+                    uint16_t* y = static_cast<uint16_t*>(a.y) + o;
+                    const bool bf = a.ydtype == MOE_BF16;
+#pragma unroll
+                    for (int j = 0; j < 128; j += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = bf ? bf162_bits(acc[j + 2 * i], acc[j + 2 * i + 1])
+                                      : half2_bits(acc[j + 2 * i], acc[j + 2 * i + 1]);
+                        if (a.y_vec && n0 + j + 8 <= a.N)
+                            store16(y + j, w[0], w[1], w[2], w[3]);
+                        else
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (n0 + j + i < a.N) y[j + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int MODE>
+static cudaError_t set_attr() {
+    cudaError_t e = cudaFuncSetAttribute(k_fp8_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    // the register split draws on what the CTA is launched with
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, k_fp8_gemm<MODE>)) != cudaSuccess) return e;
+    return fa.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidDeviceFunction;
+}
+
+cudaError_t fp8_gemm_set_attributes() {
+    cudaError_t e = set_attr<kGateUp>();
+    if (e == cudaSuccess) e = set_attr<kDown>();
+    return e == cudaSuccess ? set_attr<kDense>() : e;
+}
+
+cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& m, const Fp8GemmArgs& a, int num_sms,
+                            cudaStream_t st) {
+    auto k = mode == kGateUp ? k_fp8_gemm<kGateUp> : mode == kDown ? k_fp8_gemm<kDown> : k_fp8_gemm<kDense>;
+    return launch_kernel(k, dim3(num_sms), dim3(kThreads), kSmem, st, m.w0, m.w1, m.s0, m.s1, m.a0,
+                         m.a1, a);
+}
+
+}  // namespace moe

@@ -16,7 +16,7 @@ struct RouteArgs {
     int R, H, E, k, nb;
     float* logits;
     uint32_t* cnt;
-    int32_t* topk_idx;
+    int32_t* topk_idx;    // NULL: the finished logits are the output (moe_block_logits)
     float* topk_w;
     uint32_t* status;
     float* topk_p;        // [R, k] probabilities under the full softmax, or NULL

@@ -226,7 +226,27 @@ __device__ __forceinline__ void route_topk_rows(const RouteArgs& a, int r0, int 
     }
 }
 
+// Finish the logits of rows r0..r1-1 in place (moe_block_logits): bias, -0 -> +0.
+__device__ __forceinline__ void finish_rows(const RouteArgs& a, int r0, int r1, int lane) {
+    for (int r = r0; r < r1; ++r) {
+        const float* brow = a.bias ? a.bias + (size_t)find_block(a.off, a.nb, r) * a.E : nullptr;
+        uint32_t nonfinite = 0;
+        for (int e = lane; e < a.E; e += 32) {
+            float* p = a.logits + (size_t)r * a.E + e;
+            const float z = finish_logit(__ldcg(p), brow, e);
+            if (!isfinite(z)) ++nonfinite;
+            *p = z;
+        }
+        nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
+        if (lane == 0) status_add(a.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
+    }
+}
+
 __device__ __forceinline__ void route_topk(const RouteArgs& a, int r0, int r1, int lane) {
+    if (!a.topk_idx) {   // moe_block_logits
+        finish_rows(a, r0, r1, lane);
+        return;
+    }
     const int ne = (a.E + 31) >> 5;
     if (ne <= 1) route_topk_rows<1>(a, r0, r1, lane);
     else if (ne <= 2) route_topk_rows<2>(a, r0, r1, lane);

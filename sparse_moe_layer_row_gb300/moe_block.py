@@ -9,6 +9,7 @@ device) every call raises.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
 
 import torch
@@ -39,6 +40,64 @@ _QFIELDS = ("gate_up", "down", "gate_up_scale", "down_scale", "shared_gate_up", 
 
 class moe_quant_weights(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in _QFIELDS]
+
+
+_F8FIELDS = ("gate", "up", "down", "gate_scale", "up_scale", "down_scale", "shared_gate",
+             "shared_up", "shared_down", "shared_gate_scale", "shared_up_scale",
+             "shared_down_scale")
+
+
+class moe_fp8_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _F8FIELDS]
+
+
+@dataclasses.dataclass
+class Fp8Experts:
+    """Expert weights in e4m3 with one fp32 scale per 128 x 128 block, as
+    moe_fp8_weights holds them."""
+    gate: torch.Tensor            # e4m3 [E, I, H]
+    up: torch.Tensor
+    down: torch.Tensor            # e4m3 [E, H, I]
+    gate_scale: torch.Tensor      # fp32 [E, ceil(I / 128), H / 128]
+    up_scale: torch.Tensor
+    down_scale: torch.Tensor      # fp32 [E, H / 128, ceil(I / 128)]
+    shared_gate: torch.Tensor     # e4m3 [Is, H]
+    shared_up: torch.Tensor
+    shared_down: torch.Tensor     # e4m3 [H, Is]
+    shared_gate_scale: torch.Tensor
+    shared_up_scale: torch.Tensor
+    shared_down_scale: torch.Tensor
+
+
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+@dataclasses.dataclass(frozen=True)
+class RouteRule:
+    """A routing rule (moe_route_rule): scores, expert groups, weights."""
+    score: str = "softmax"        # or "sigmoid"
+    n_groups: int = 1
+    top_groups: int = 1
+    group_score: str = "max"      # or "top2"
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}")
+        if self.group_score not in _GROUP_SCORES:
+            raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}")
+        object.__setattr__(self, "_c", moe_route_rule(
+            _SCORES[self.score], self.n_groups, self.top_groups, _GROUP_SCORES[self.group_score],
+            int(self.renormalize), self.scale))
 
 
 _lib = None
@@ -94,6 +153,21 @@ def load(build_if_missing: bool = False):
                                  P, P, P, sz, P]
     L.moe_block_route_noalloc.restype = ctypes.c_int
     L.moe_block_route_noalloc.argtypes = [P, P, i32, P, i32, P, P, P, P]
+    i64 = ctypes.c_int64
+    L.moe_plan_create_fp8.restype = ctypes.c_int
+    L.moe_plan_create_fp8.argtypes = [ctypes.POINTER(moe_dims), P, ctypes.POINTER(moe_fp8_weights),
+                                      ctypes.POINTER(P)]
+    L.moe_route_scored.restype = ctypes.c_int
+    L.moe_route_scored.argtypes = [ctypes.POINTER(moe_route_rule), P, ctypes.c_int, i64, i32, i32,
+                                   i32, P, P, P, P, P]
+    L.moe_block_logits.restype = ctypes.c_int
+    L.moe_block_logits.argtypes = [P, P, i32, P, i32, P, P, P, sz, P]
+    L.moe_fp8_quantize.restype = ctypes.c_int
+    L.moe_fp8_quantize.argtypes = [P, ctypes.c_int, i64, i32, i32, P, P, P]
+    L.moe_fp8_gemm_workspace_bytes.restype = sz
+    L.moe_fp8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
+    L.moe_fp8_gemm.restype = ctypes.c_int
+    L.moe_fp8_gemm.argtypes = [P, P, i32, P, P, i32, i32, P, ctypes.c_int, i64, P, sz, P]
     L.moe_plan_set_forward_events.restype = ctypes.c_int
     L.moe_plan_set_forward_events.argtypes = [P, P, i32]
     L.moe_plan_set_wait_limit.restype = ctypes.c_int
@@ -132,6 +206,30 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_rows(t: torch.Tensor, name: str, shape=None) -> int:
+    """A matrix of a float type whose rows are contiguous; returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # a single row's stride is never used
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _same_device(*tensors):
+    """The device of the tensors given (None: not given), which must be one."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop()
 
 
 def moe_version() -> int:
@@ -198,6 +296,35 @@ class Plan:
             _check(load().moe_plan_create(ctypes.byref(d), *[_ptr(w) for w in self.weights],
                                           ctypes.byref(h)))
         self.handle = h
+
+    @classmethod
+    def fp8(cls, dims: moe_dims, w_router, q: Fp8Experts):
+        """moe_plan_create_fp8: e4m3 experts with a scale per 128 x 128 block."""
+        d = dims
+        e4m3, f32 = torch.float8_e4m3fn, torch.float32
+        _need(w_router, "w_router", torch.bfloat16, (d.E, d.H))
+        ib, isb, hb = -(-d.I // 128), -(-d.Is // 128), d.H // 128
+        shapes = {"gate": (e4m3, (d.E, d.I, d.H)), "up": (e4m3, (d.E, d.I, d.H)),
+                  "down": (e4m3, (d.E, d.H, d.I)), "gate_scale": (f32, (d.E, ib, hb)),
+                  "up_scale": (f32, (d.E, ib, hb)), "down_scale": (f32, (d.E, hb, ib)),
+                  "shared_gate": (e4m3, (d.Is, d.H)), "shared_up": (e4m3, (d.Is, d.H)),
+                  "shared_down": (e4m3, (d.H, d.Is)), "shared_gate_scale": (f32, (isb, hb)),
+                  "shared_up_scale": (f32, (isb, hb)), "shared_down_scale": (f32, (hb, isb))}
+        tensors = [getattr(q, n) for n in _F8FIELDS]
+        for n, t in zip(_F8FIELDS, tensors):
+            _need(t, n, *shapes[n])
+        self = cls.__new__(cls)
+        self.dims = d
+        self.weights = (w_router, *tensors)
+        self.device = _same_device(w_router, *tensors)
+        self.bits = 8
+        w = moe_fp8_weights(*[t.data_ptr() for t in tensors])
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(load().moe_plan_create_fp8(ctypes.byref(d), _ptr(w_router), ctypes.byref(w),
+                                              ctypes.byref(h)))
+        self.handle = h
+        return self
 
     def close(self):
         if getattr(self, "handle", None) and self.handle.value:
@@ -384,6 +511,86 @@ def moe_block_pass(plan: Plan, x, block_offsets, logit_bias, tau: float, max_exp
                                  _stream(stream)))
 
 
+def moe_block_logits(plan: Plan, x, block_offsets, logit_bias, logits, workspace, stream=None):
+    """The router's logits (fp32 [R, E]) alone, for moe_route_scored."""
+    d = plan.dims
+    R = x.shape[0]
+    nb = block_offsets.shape[0] - 1
+    _need(x, "x", torch.bfloat16, (R, d.H))
+    _need(block_offsets, "block_offsets", torch.int32)
+    if logit_bias is not None:
+        _need(logit_bias, "logit_bias", torch.float32, (nb, d.E))
+    _need(logits, "logits", torch.float32, (R, d.E))
+    _need(workspace, "workspace", torch.uint8)
+    _check(load().moe_block_logits(plan.handle, _ptr(x), R, _ptr(block_offsets), nb,
+                                   _ptr(logit_bias), _ptr(logits), _ptr(workspace),
+                                   workspace.numel(), _stream(stream)))
+
+
+def moe_route_scored(logits, rule: RouteRule, topk_idx, topk_w, select_bias=None, topk_score=None,
+                     stream=None):
+    """Route rows by their logits [R, E] (bf16, fp16 or fp32; rows may be strided) under
+    ``rule``: writes topk_idx (int32 [R, k]), topk_w (fp32 [R, k]) and, when given,
+    topk_score (fp32 [R, k], the chosen experts' scores)."""
+    ld = _need_rows(logits, "logits")
+    R, E = logits.shape
+    _need(topk_idx, "topk_idx", torch.int32)
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must have shape [R, k]")
+    k = topk_idx.shape[1]
+    _need(topk_idx, "topk_idx", torch.int32, (R, k))
+    _need(topk_w, "topk_w", torch.float32, (R, k))
+    if select_bias is not None:
+        _need(select_bias, "select_bias", torch.float32, (E,))
+    if topk_score is not None:
+        _need(topk_score, "topk_score", torch.float32, (R, k))
+    with torch.cuda.device(_same_device(logits, topk_idx, topk_w, select_bias, topk_score)):
+        _check(load().moe_route_scored(ctypes.byref(rule._c), _ptr(logits), _DTYPES[logits.dtype],
+                                       ld, R, E, k, _ptr(select_bias), _ptr(topk_idx),
+                                       _ptr(topk_w), _ptr(topk_score), _stream(stream)))
+
+
+def moe_fp8_quantize(x, codes, scales, stream=None):
+    """Rows x [R, K] (bf16, fp16 or fp32; rows may be strided) to e4m3 ``codes`` [R, K]
+    and fp32 ``scales`` [ceil(K / 128), R], one per row and block of 128."""
+    ld = _need_rows(x, "x")
+    R, K = x.shape
+    _need(codes, "codes", torch.float8_e4m3fn, (R, K))
+    _need(scales, "scales", torch.float32, (-(-K // 128), R))
+    with torch.cuda.device(_same_device(x, codes, scales)):
+        _check(load().moe_fp8_quantize(_ptr(x), _DTYPES[x.dtype], ld, R, K, _ptr(codes),
+                                       _ptr(scales), _stream(stream)))
+
+
+def moe_fp8_gemm_workspace_bytes(R: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_fp8_gemm; raises for sizes it does not take."""
+    n = int(load().moe_fp8_gemm_workspace_bytes(R, N, K))
+    if n == 0:
+        raise MoeError(-1, load().moe_last_error().decode())
+    return n
+
+
+def moe_fp8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
+    """y [R, N] = x W^T on e4m3 codes: xq [R, K] with scales xs [ceil(K / 128), R] (as
+    moe_fp8_quantize writes them), wq [N, K] with a scale per 128 x 128 block
+    (ws [ceil(N / 128), ceil(K / 128)]).  y: bf16, fp16 or fp32, rows may be strided."""
+    ld = _need_rows(y, "y")
+    R, N = y.shape
+    _need(xq, "xq", torch.float8_e4m3fn)
+    if xq.dim() != 2 or xq.shape[0] != R:
+        raise ValueError(f"xq must have shape ({R}, K), got {tuple(xq.shape)}")
+    K = xq.shape[1]
+    kb = -(-K // 128)
+    _need(xs, "xs", torch.float32, (kb, R))
+    _need(wq, "wq", torch.float8_e4m3fn, (N, K))
+    _need(ws, "ws", torch.float32, (-(-N // 128), kb))
+    _need(workspace, "workspace", torch.uint8)
+    with torch.cuda.device(_same_device(xq, xs, wq, ws, y, workspace)):
+        _check(load().moe_fp8_gemm(_ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
+                                   _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(),
+                                   _stream(stream)))
+
+
 def moe_read_device_status(workspace: torch.Tensor, stream=None) -> dict:
     _need(workspace, "workspace", torch.uint8)
     out = (ctypes.c_uint32 * STATUS_WORDS)()
@@ -441,6 +648,17 @@ class MoeBlockLayer:
         self._init_buffers(w_router.device)
         return self
 
+    @classmethod
+    def fp8(cls, w_router, q: Fp8Experts, k: int, max_rows: int, max_blocks: int):
+        """A layer whose experts are e4m3 with a scale per 128 x 128 block
+        (moe_plan_create_fp8)."""
+        E, H = w_router.shape
+        self = cls.__new__(cls)
+        self.dims = moe_dims(H, E, k, q.gate.shape[1], q.shared_gate.shape[0], max_rows, max_blocks)
+        self.plan = Plan.fp8(self.dims, w_router, q)
+        self._init_buffers(w_router.device)
+        return self
+
     def _init_buffers(self, dev):
         E, H, k = self.dims.E, self.dims.H, self.dims.k
         max_rows, max_blocks = self.dims.max_rows, self.dims.max_blocks
@@ -467,6 +685,21 @@ class MoeBlockLayer:
             return idx, w, p
         moe_block_route(self.plan, x, block_offsets, bias, idx, w, self.workspace, stream)
         return idx, w
+
+    def route_scored(self, x, block_offsets, rule: RouteRule, bias=None, select_bias=None,
+                     stream=None):
+        """Routes by ``rule`` on the router's logits (moe_block_logits, then
+        moe_route_scored).  Returns (topk_idx, topk_w, topk_score); topk_score serves as
+        the coreset's ``mass``."""
+        R = x.shape[0]
+        if not hasattr(self, "_logits"):
+            self._logits = torch.empty(self.dims.max_rows, self.dims.E, dtype=torch.float32,
+                                       device=self._topk_w.device)
+            self._topk_s = torch.empty_like(self._topk_w)
+        z, idx, w, sc = self._logits[:R], self._topk_idx[:R], self._topk_w[:R], self._topk_s[:R]
+        moe_block_logits(self.plan, x, block_offsets, bias, z, self.workspace, stream)
+        moe_route_scored(z, rule, idx, w, select_bias=select_bias, topk_score=sc, stream=stream)
+        return idx, w, sc
 
     def coreset(self, block_offsets, topk_idx, topk_w, tau, stream=None, max_experts=0,
                 mass=None):
