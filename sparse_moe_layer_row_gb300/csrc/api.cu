@@ -249,8 +249,10 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     // rows (few pairs per expert: its CTA-pair units would be mostly empty)
     const bool su = small || p->qbits != 0;
     const bool sd = su || R <= kStreamDownRows;
-    const int nt_gu = p->fp8 ? kFp8Rows : su ? kSmallN : kLargeNGU;
-    const int nt_dn = p->fp8 ? kFp8Rows : sd ? kSmallN : kLargeNDown;
+    const bool fs = p->fp8 && R <= kFp8StreamMaxRows;   // e4m3 weights streamed
+    const int nt_fp8 = fs ? kFp8StreamRows : kFp8Rows;
+    const int nt_gu = p->fp8 ? nt_fp8 : su ? kSmallN : kLargeNGU;
+    const int nt_dn = p->fp8 ? nt_fp8 : sd ? kSmallN : kLargeNDown;
 
     ScatterArgs sa{block_offsets, topk_idx, w_renorm, keep, R, d.H, d.E, d.k, d.I, d.Is, nb, nt_gu, nt_dn,
                    p->fp8 ? kFp8GuRows : su ? 64 : 128, p->fp8 ? kFp8DnCols : sd ? 128 : 256,
@@ -310,7 +312,8 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     if (e == cudaSuccess) e = launch_scatter(sa, small, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "scatter launch");
     if ((e = mark(1)) == cudaSuccess)
-        e = p->fp8 ? launch_fp8_gemm(kGateUp, mg, fg, p->num_sms, st)
+        e = fs ? launch_fp8_stream(kGateUp, mg, fg, p->num_sms, st)
+          : p->fp8 ? launch_fp8_gemm(kGateUp, mg, fg, p->num_sms, st)
                    : launch_gemm(kGateUp, su, p->qbits, gu, ga, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "gate/up GEMM launch");
     GemmArgs gd = ga;
@@ -322,7 +325,8 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
             fp8_args(p, gd, workspace, R, true, &fd, &md);
             md.a0 = a0;
             md.a1 = a1;
-            e = launch_fp8_gemm(kDown, md, fd, p->num_sms, st);
+            e = fs ? launch_fp8_stream(kDown, md, fd, p->num_sms, st)
+                   : launch_fp8_gemm(kDown, md, fd, p->num_sms, st);
         } else {
             e = launch_gemm(kDown, sd, p->qbits, dn, gd, p->num_sms, st);
         }
@@ -333,7 +337,7 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
                    at<int32_t>(workspace, L.inv), R, d.H, d.k,
                    (int)L.max_pairs, static_cast<__nv_bfloat16*>(y), y_f32,
                    at<uint32_t>(workspace, L.status), live, at<int32_t>(workspace, L.shared_inv)};
-    if ((e = mark(3)) == cudaSuccess) e = launch_combine(ca, p->num_sms, !sd && !p->fp8, st);
+    if ((e = mark(3)) == cudaSuccess) e = launch_combine(ca, p->num_sms, !sd, st);
     if (e == cudaSuccess) e = mark(4);
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
     return ok();
@@ -499,6 +503,7 @@ moe_status moe_plan_create_fp8(const moe_dims* dims, const void* w_router,
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
     if (e == cudaSuccess) e = fp8_gemm_set_attributes();
+    if (e == cudaSuccess) e = fp8_stream_set_attributes();
     if (e == cudaSuccess) e = route_tc_set_attributes();
     if (e != cudaSuccess) {
         delete p;

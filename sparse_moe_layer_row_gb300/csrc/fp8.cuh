@@ -80,8 +80,28 @@ struct Fp8Maps {
     CUtensorMap s0, s1;   // the shared expert's
     CUtensorMap a0, a1;   // rows: h codes of routed pairs / shared rows; dense: x codes
 };
+// Calls of up to kFp8StreamMaxRows rows take units of up to kFp8StreamRows pairs
+// and the streaming kernels (fp8_stream.cu).
+constexpr int kFp8StreamRows = 32;
+constexpr int kFp8StreamMaxRows = 128;
+cudaError_t fp8_stream_set_attributes();
+cudaError_t launch_fp8_stream(int mode, const Fp8Maps&, const Fp8GemmArgs&, int num_sms, cudaStream_t);
 cudaError_t fp8_gemm_set_attributes();
 cudaError_t launch_fp8_gemm(int mode, const Fp8Maps&, const Fp8GemmArgs&, int num_sms, cudaStream_t);
+
+// The dense product for few rows or little work (fp8_rows.cu).
+struct Fp8RowsArgs {
+    const uint8_t* xq;
+    const float* xs;
+    const uint8_t* wq;
+    const float* ws;
+    int R, N, K;
+    void* y;
+    int64_t ldy;
+    int ydtype;
+};
+bool fp8_rows_applies(int R, int N, int K, int num_sms);
+cudaError_t launch_fp8_rows(const Fp8RowsArgs&, cudaStream_t);
 
 // Tensor map of e4m3 codes, row-major [d2][d1][d0] (rank 2 if d2 == 0), box of
 // 128 x 128 codes in the 128-byte swizzle, zeros outside (implemented in api.cu).

@@ -21,18 +21,22 @@
 //            with a power-of-two exponent per 32 columns, as k_combine reads it.
 //   dense    256 outputs, stored in bf16, fp16 or fp32.
 //
-// Persistent, one CTA per SM, 512 threads:
+// Persistent, one CTA per SM, 384 threads (gate/up: 512):
 //   warp 0 lane 0   TMA producer: weight tiles (2 x 16 KB) and, but for
 //                   gate/up, the rows' tile (16 KB) into a ring of 4 stages
 //   warp 1          TMEM allocation; lane 0 issues the MMAs
-//   warp 2 lane 0   gate/up: forwarder; when a stage's rows have landed it
-//                   fences them for the async proxy and tells the MMA thread
 //   warps 4..11     promotion and epilogue: lane quadrant warp & 3, columns by
 //                   warpgroup
-//   warps 12..15    gate/up: loaders, gather the unit's rows of x by 16-byte
-//                   cp.async into the swizzled tile
+//   loaders         gate/up: warps 12..15, gather the unit's rows of x by
+//                   16-byte cp.async into the swizzled tile (the MMA thread
+//                   fences them for the async proxy); else warps 2, 3.  They
+//                   also copy the block's scales and, with a unit's last block,
+//                   its pair weights, into slots that the promotion warps read;
+//                   all of it arrives on the slot's `rfull` when it lands
 // Registers are moved from the other warpgroups to the promotion warps, which
-// hold 128 accumulators each.
+// hold 128 accumulators each.  A promotion warp whose 32 rows lie past the
+// unit's only passes the buffers on.  Outputs go through 2 KB of shared memory
+// per warp, so that 4 lanes store 64 consecutive bytes of a row.
 // Every wait is bounded: a wait that gives up raises a CTA-wide abort flag and
 // a device status counter, and all roles leave their loops; before the CTA
 // exits its copies and MMAs in flight are waited for (with their own limit),
@@ -47,19 +51,31 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal 
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
 
 constexpr int kStages = 4;
-constexpr int kThreads = 512;
+constexpr int kThreads = 384, kThreadsGU = 512;
 constexpr int kTile = 128 * 128;                 // 128 rows x 128 codes
 constexpr int kStageBytes = 3 * kTile;           // rows, weights 0, weights 1
-constexpr int kAmaxOff = kStages * kStageBytes;  // uint32 [2 units][2 warpgroups][128 rows]
-constexpr int kBarOff = kAmaxOff + 2 * 2 * 128 * 4;
-constexpr int kSmem = kBarOff + 256 + 1024;
+constexpr int kAmaxOff = kStages * kStageBytes;       // uint32 [2 units][2 warpgroups][128 rows]
+constexpr int kStgOff = kAmaxOff + 2 * 2 * 128 * 4;   // 32 rows x 64 bytes per promotion warp
+// Slots of the loaders' scales, one per fill of a stage, in turn, each with its barrier.  The fill kSlots later
+// reuses a slot: it follows the MMA of the fill kSlots - kStages later, which follows the
+// promotion (two TMEM buffers) of the fill kSlots - kStages - 2 later.
+constexpr int kSlots = 8;
+static_assert(kSlots - kStages - 2 > 0 && (kSlots & (kSlots - 1)) == 0, "a slot outlives its promotion and epilogue");
+constexpr int kSxOff = kStgOff + 8 * 2048;            // float [kSlots][128]: row scales
+constexpr int kPwOff = kSxOff + kSlots * 512;         // float [kSlots][128]: pair weights (down)
+constexpr int kSwOff = kPwOff + kSlots * 512;         // float [kSlots][2]: weight block scales
+constexpr int kRowsOff = kSwOff + kSlots * 8;         // int [128]: the loaders' rows of x
+constexpr int kBarOff = kRowsOff + 128 * 4;
+constexpr int kSmem = kBarOff + 256;
 constexpr int kTmemCols = 512;                   // two buffers of 256 columns
 // registers per thread after the split: the pool is what the CTA was launched
 // with (kThreads x kLaunchRegs), checked on the host before any launch
-constexpr int kLaunchRegs = 128, kFewRegs = 56, kManyRegs = 200;
-static_assert(256 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
+constexpr int kLaunchRegsGU = 128, kFewRegsGU = 48, kManyRegsGU = 208;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
+static_assert(256 * kFewRegsGU + 256 * kManyRegsGU <= kThreadsGU * kLaunchRegsGU, "register split");
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
-static_assert(8 * (4 * kStages + 6) + 12 <= 256, "barrier region");
+static_assert(8 * (2 * kStages + kSlots + 6) + 12 <= 256, "barrier region");
 
 // kind::f8f6f4 with e4m3 A and B (format 0), fp32 accumulator, both K-major.
 __device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
@@ -76,22 +92,24 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
+// Arrive on `bar` once this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
 
-// 32 lanes x 32 columns of TMEM into registers; complete after tmem_ld_wait.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 32 lanes x 16 columns of TMEM into registers; complete after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 
@@ -100,9 +118,9 @@ __device__ __forceinline__ void tmem_ld_wait() {
 }
 
 // acc[j] += f * v[j], two at a time (fma.rn.f32x2: each half as fmaf).
-__device__ __forceinline__ void promote32(float* acc, const uint32_t (&v)[32], float f) {
+__device__ __forceinline__ void promote16(float* acc, const uint32_t (&v)[16], float f) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2)
+    for (int j = 0; j < 16; j += 2)
         asm("{\n\t.reg .b64 a, b, c;\n\t"
             "mov.b64 a, {%2, %3};\n\t"
             "mov.b64 b, {%4, %4};\n\t"
@@ -129,19 +147,16 @@ __device__ __forceinline__ uint32_t bf162_bits(float a, float b) {
 }  // namespace
 
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(MODE == kGateUp ? kThreadsGU : kThreads, 1)
 k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
            const __grid_constant__ CUtensorMap tmS0, const __grid_constant__ CUtensorMap tmS1,
            const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
            Fp8GemmArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t sbase = (raw + 1023u) & ~1023u;
-    uint8_t* base = smem_raw + (sbase - raw);
+    extern __shared__ __align__(1024) uint8_t base[];   // swizzle atoms are 1 KB
+    const uint32_t sbase = smem_u32(base);
     uint64_t* full = reinterpret_cast<uint64_t*>(base + kBarOff);  // [S] tiles landed
-    uint64_t* rfull = full + kStages;                               // [S] gathered rows landed
-    uint64_t* rready = rfull + kStages;                             // [S] ... and fenced
-    uint64_t* empty = rready + kStages;                             // [S] stage free
+    uint64_t* rfull = full + kStages;                               // [kSlots] loaders' copies landed
+    uint64_t* empty = rfull + kSlots;                               // [S] stage free
     uint64_t* tfull = empty + kStages;                              // [2] partial sums ready
     uint64_t* tempty = tfull + 2;                                   // [2] buffer free
     uint64_t* xbar = tempty + 2;                                    // amax exchange
@@ -154,13 +169,12 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full + s, 1);
-            mbar_init(rfull + s, 128);   // the loader threads' copies
-            mbar_init(rready + s, 1);    // the forwarder
             mbar_init(empty + s, 1);
         }
+        for (int s = 0; s < kSlots; ++s) mbar_init(rfull + s, MODE == kGateUp ? 128 : 64);   // the loader threads
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + i, 1);
-            mbar_init(tempty + i, 256);
+            mbar_init(tempty + i, 8);   // the promotion warps
         }
         mbar_init(xbar, 256);
         mbar_init(dbar, 1);
@@ -201,8 +215,93 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
     };
     const uint64_t kWaitNs = a.g.wait_ns ? a.g.wait_ns : kWaitLimitNs;
 
+    // The loaders' loop.  Row i of a gate/up unit is copied by 8 threads, 16 bytes
+    // each: chunk c of row i lands at chunk c ^ (i & 7) (the 128-byte swizzle).
+    // Rows past the unit's are not loaded: they feed only TMEM lanes never stored.
+    auto loader = [&]() {
+        constexpr int kLt = MODE == kGateUp ? 128 : 64;
+        const int lt = threadIdx.x - (MODE == kGateUp ? 384 : 64);   // 0 .. kLt - 1
+        const int r16 = lt >> 3, ch = lt & 7;
+        int* s_rows = reinterpret_cast<int*>(base + kRowsOff);
+        const uint32_t dst0 = sbase + r16 * 128 + ((ch ^ (r16 & 7)) << 4);
+        int stage = 0, slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = ufirst; ok && u < nunits; u += nact) {
+            const int4 un = unit(u);
+            if (!valid(un)) continue;
+            const int g = un.x, m = un.y, start = un.z, n = un.w;
+            const bool sh = MODE != kDense && g == E;
+            const int nkb = blocks(g);
+            const float *px, *pw0, *pw1;   // scales: of row lt, of the two weight blocks
+            int64_t ldx;
+            if (MODE == kGateUp) {
+                // the rows are kept in shared memory (the L1 left beside it is too small
+                // for local arrays: 242 -> 1000 us at 8192 rows); a warp copies the rows
+                // that it wrote
+                __syncwarp();
+                int mine = 0;
+                for (int i = r16; i < n; i += 16) {
+                    const int row = !sh ? __ldg(a.g.pair_row + start + i)
+                                  : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + i) : start + i);
+                    s_rows[i] = row >= 0 && row < a.g.R ? row : -1;
+                }
+                if (lt < n)
+                    mine = !sh ? __ldg(a.g.pair_row + start + lt)
+                         : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + lt) : start + lt);
+                __syncwarp();
+                px = a.xs + min(max(mine, 0), a.g.R - 1);
+                ldx = a.g.R;
+                const int mb = fp8_blocks(sh ? a.g.Is : a.g.I);
+                const int64_t o = ((int64_t)(sh ? 0 : g) * mb + m) * nkb;
+                pw0 = (sh ? a.sc_sa : a.sc_a) + o;
+                pw1 = (sh ? a.sc_sb : a.sc_b) + o;
+            } else if (MODE == kDown) {
+                px = (sh ? a.shs : a.hs) + start;
+                ldx = sh ? a.max_rows : a.max_pairs;
+                const int hb = a.g.H / kFp8Block;
+                pw0 = (sh ? a.sc_sa : a.sc_a) + ((int64_t)(sh ? 0 : g) * hb + 2 * m) * nkb;
+                pw1 = pw0 + nkb;
+            } else {
+                px = a.xs + start;
+                ldx = a.R;
+                const int nb = fp8_blocks(a.N);
+                pw0 = a.sc_a + (int64_t)(2 * m) * nkb;
+                pw1 = a.sc_a + (int64_t)min(2 * m + 1, nb - 1) * nkb;
+            }
+            for (int kb = 0; kb < nkb; ++kb) {
+                const bool free_ok = mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitNs);
+                if (__any_sync(0xffffffffu, !free_ok)) {   // the warp leaves together
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                const float* sxk = px + (int64_t)kb * ldx;
+                for (int i = lt; i < n; i += kLt) {
+                    cp_async4(sbase + kSxOff + (slot * 128 + i) * 4, MODE == kGateUp ? sxk : sxk + i);
+                    if (MODE == kDown && kb == nkb - 1 && !sh)
+                        cp_async4(sbase + kPwOff + (slot * 128 + i) * 4, a.g.pair_w + start + i);
+                }
+                if (lt < 2) cp_async4(sbase + kSwOff + (slot * 2 + lt) * 4, (lt ? pw1 : pw0) + kb);
+                if (MODE == kGateUp) {
+                    const uint32_t dst = dst0 + stage * kStageBytes;
+                    const uint8_t* col = a.xq + kb * kFp8Block + ch * 16;
+#pragma unroll 4
+                    for (int i = r16; i < n; i += 16) {
+                        const int row = s_rows[i];
+                        if (row >= 0) cp_async16(dst + (i - r16) * 128, col + (int64_t)row * a.g.H);
+                    }
+                }
+                cp_async_arrive(rfull + slot);
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                slot = (slot + 1) & (kSlots - 1);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");   // nothing of this thread lands later
+    };
+
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MODE == kGateUp ? kFewRegsGU : kFewRegs));
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------------ TMA producer
             int stage = 0, nfills = 0;
@@ -256,8 +355,8 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
         } else if (warp == 1 && lane == 0) {
             // -------------------------------------------------------- MMA issuer
             const uint32_t idesc = idesc_e4m3_f32(128, 256);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
+            int stage = 0, slot = 0, buf = 0;
+            uint32_t phase = 0, rphase = 0, bphase = 0;
             bool ok = true;
             for (int u = ufirst; ok && u < nunits; u += nact) {
                 const int4 un = unit(u);
@@ -269,12 +368,13 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!mbar_wait_bounded(full + stage, phase, abort_flag, kWaitNs) ||
                         (MODE == kGateUp &&
-                         !mbar_wait_bounded(rready + stage, phase, abort_flag, kWaitNs)) ||
+                         !mbar_wait_bounded(rfull + slot, rphase, abort_flag, kWaitNs)) ||
                         !mbar_wait_bounded(tempty + buf, bphase ^ 1u, abort_flag, kWaitNs)) {
                         give_up();
                         ok = false;
                         break;
                     }
+                    if (MODE == kGateUp) fence_proxy_async_smem();   // rows written by cp.async
                     tc_fence_after();
                     const uint32_t sA = sbase + stage * kStageBytes, sW = sA + kTile;
                     const uint32_t d = tmem + (uint32_t)(buf * 256);
@@ -286,6 +386,7 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                     tc_commit(empty + stage);
                     tc_commit(tfull + buf);
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++slot == kSlots) { slot = 0; rphase ^= 1u; }
                     buf ^= 1;
                     if (buf == 0) bphase ^= 1u;
                 }
@@ -293,74 +394,14 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
             // drain: arrives once every MMA issued above has completed
             tc_commit(dbar);
             if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs)) give_up();
-        } else if (MODE == kGateUp && warp == 2 && lane == 0) {
-            // --------------------------------------------------------- forwarder
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int u = ufirst; ok && u < nunits; u += nact) {
-                const int4 un = unit(u);
-                if (!valid(un)) continue;
-                const int nkb = blocks(un.x);
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_bounded(rfull + stage, phase, abort_flag, kWaitNs)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    fence_proxy_async_smem();   // the rows were written by cp.async
-                    mbar_arrive(rready + stage);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
-                }
-            }
+        } else if (MODE != kGateUp && warp >= 2) {
+            loader();
         }
-    } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        if (MODE == kGateUp) {
-            // ----------------------------------------------------------- loaders
-            // Row i of the unit is copied by 8 threads, 16 bytes each: chunk c of
-            // row i lands at chunk c ^ (i & 7) (the 128-byte swizzle).  Rows past
-            // the unit's are not loaded: they feed only TMEM lanes never stored.
-            const int lt = threadIdx.x - 384;            // 0..127
-            const int r16 = lt >> 3, ch = lt & 7;
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int u = ufirst; ok && u < nunits; u += nact) {
-                const int4 un = unit(u);
-                if (!valid(un)) continue;
-                const int g = un.x, start = un.z, n = un.w;
-                int row[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = j * 16 + r16;
-                    row[j] = i >= n ? -1
-                           : g != E ? __ldg(a.g.pair_row + start + i)
-                           : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + i) : start + i);
-                }
-                const int nkb = blocks(g);
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitNs)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sA = sbase + stage * kStageBytes;
-                    const uint8_t* col = a.xq + kb * kFp8Block + ch * 16;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int i = j * 16 + r16;
-                        if (row[j] >= 0 && row[j] < a.g.R)
-                            cp_async16(sA + i * 128 + ((ch ^ (i & 7)) << 4), col + (int64_t)row[j] * a.g.H);
-                    }
-                    cp_async_arrive(rfull + stage);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");   // nothing of this thread lands later
-        }
+    } else if (MODE == kGateUp && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegsGU));
+        loader();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MODE == kGateUp ? kManyRegsGU : kManyRegs));
         // ------------------------------------------------ promotion and epilogue
         const int q = warp & 3;           // TMEM lane quadrant this warp may read
         const int wg = (warp - 4) >> 2;   // 0 or 1
@@ -371,66 +412,51 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
         const uint32_t col1 = (uint32_t)(MODE == kGateUp ? 128 + wg * 64 : wg * 128 + 64);
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
         uint32_t* s_amax = reinterpret_cast<uint32_t*>(base + kAmaxOff);
-        int buf = 0, upar = 0;
-        uint32_t bphase = 0, xphase = 0;
+        uint8_t* stg = base + kStgOff + (warp - 4) * 2048;
+        const float* s_sx = reinterpret_cast<const float*>(base + kSxOff) + t;
+        const float* s_sw = reinterpret_cast<const float*>(base + kSwOff);
+        int buf = 0, upar = 0, slot = 0;
+        uint32_t bphase = 0, xphase = 0, phase = 0;
         bool alive = true;
+        int4 next = ufirst < nunits ? unit(ufirst) : make_int4(0, 0, 0, 0);
         for (int u = ufirst; alive && u < nunits; u += nact) {
-            const int4 un = unit(u);
+            const int4 un = next;
+            if (u + nact < nunits) next = unit(u + nact);   // long before it is needed
             if (!valid(un)) continue;
             const int g = un.x, m = un.y, start = un.z, n = un.w;
             const bool sh = MODE != kDense && g == E;
             const int nkb = blocks(g);
-            const int tc = min(t, n - 1);   // rows past the unit's repeat its last
-            // the row's scales (one per block of K, ldx apart) and the weight blocks'
-            const float *px, *pw0, *pw1;
-            int64_t ldx;
-            if (MODE == kGateUp) {
-                int row = sh ? (a.g.shared_rows ? __ldg(a.g.shared_rows + start + tc) : start + tc)
-                             : __ldg(a.g.pair_row + start + tc);
-                row = min(max(row, 0), a.g.R - 1);
-                px = a.xs + row;
-                ldx = a.g.R;
-                const int mb = fp8_blocks(sh ? a.g.Is : a.g.I);
-                const int64_t o = ((int64_t)(sh ? 0 : g) * mb + m) * nkb;
-                pw0 = (sh ? a.sc_sa : a.sc_a) + o;
-                pw1 = (sh ? a.sc_sb : a.sc_b) + o;
-            } else if (MODE == kDown) {
-                px = (sh ? a.shs : a.hs) + start + tc;
-                ldx = sh ? a.max_rows : a.max_pairs;
-                const int hb = a.g.H / kFp8Block;
-                pw0 = pw1 = (sh ? a.sc_sa : a.sc_a) + ((int64_t)(sh ? 0 : g) * hb + 2 * m + wg) * nkb;
-            } else {
-                px = a.xs + start + tc;
-                ldx = a.R;
-                const int nb = fp8_blocks(a.N);
-                pw0 = pw1 = a.sc_a + (int64_t)min(2 * m + wg, nb - 1) * nkb;
-            }
+            const bool act = q * 32 < n;   // the warp has rows of the unit
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-            // h's scales were written by the gate/up kernel: not through the read-only path
-            float sx = __ldcg(px), sw0 = __ldg(pw0), sw1 = __ldg(pw1);
             for (int kb = 0; kb < nkb; ++kb) {
-                const float f0 = sx * sw0, f1 = sx * sw1;
-                if (kb + 1 < nkb) {   // the next block's scales, while the MMA runs
-                    sx = __ldcg(px + (int64_t)(kb + 1) * ldx);
-                    sw0 = __ldg(pw0 + kb + 1);
-                    sw1 = __ldg(pw1 + kb + 1);
-                }
-                const bool ok = mbar_wait_bounded(tfull + buf, bphase, abort_flag, kWaitNs);
+                // the scales have landed (with or before what the MMA read)
+                bool ok = mbar_wait_bounded(rfull + slot, phase, abort_flag, kWaitNs);
+                const float sx = s_sx[slot * 128];
+                const float f0 = sx * s_sw[slot * 2 + (MODE == kGateUp ? 0 : wg)];
+                const float f1 = sx * s_sw[slot * 2 + (MODE == kGateUp ? 1 : wg)];
+                if (++slot == kSlots) { slot = 0; phase ^= 1u; }
+                ok = ok && mbar_wait_bounded(tfull + buf, bphase, abort_flag, kWaitNs);
                 if (__any_sync(0xffffffffu, !ok)) { give_up(); alive = false; break; }
                 tc_fence_after();
                 const uint32_t tb = tq + (uint32_t)(buf * 256);
-                uint32_t v[32];
+                if (act) {
+                    uint32_t v[2][16];   // the next 16 columns are read while these are added
+                    tmem_ld16_async(tb + col0, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(tb + (c < 2 ? col0 + 32 * c : col1 + 32 * (c - 2)), v);
-                    tmem_ld_wait();
-                    if (c == 3) {   // the buffer has been read: hand it back
-                        tc_fence_before();
-                        mbar_arrive(tempty + buf);
+                    for (int c = 0; c < 8; ++c) {
+                        tmem_ld_wait();
+                        if (c < 7)
+                            tmem_ld16_async(tb + (c < 3 ? col0 + 16 * (c + 1) : col1 + 16 * (c - 3)), v[(c + 1) & 1]);
+                        if (c == 7) {   // the buffer has been read: hand it back
+                            tc_fence_before();
+                            if (lane == 0) mbar_arrive(tempty + buf);
+                        }
+                        promote16(acc + 16 * c, v[c & 1], c < 4 ? f0 : f1);
                     }
-                    promote32(acc + 32 * c, v, c < 2 ? f0 : f1);
+                } else if (lane == 0) {
+                    mbar_arrive(tempty + buf);
                 }
                 buf ^= 1;
                 if (buf == 0) bphase ^= 1u;
@@ -461,93 +487,136 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 const float inv = __fdiv_rn(448.0f, bm);
                 const int ld = sh ? a.g.Is : a.g.I;
                 const int i0 = m * 128 + wg * 64;   // I, Is are multiples of 64
-                if (t < n) {
-                    const int64_t p = start + t;
-                    if (i0 < ld) {
-                        uint8_t* out = (sh ? a.shq : a.hq) + p * ld + i0;
+                if (act && i0 < ld) {
+                    // 64 codes of a row: four 16-byte chunks, swizzled over the row pairs
 #pragma unroll
-                        for (int j = 0; j < 64; j += 16) {
-                            uint32_t w[4];
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = fp8_pair(acc[j + 4 * i] * inv, acc[j + 4 * i + 1] * inv) |
-                                       fp8_pair(acc[j + 4 * i + 2] * inv, acc[j + 4 * i + 3] * inv) << 16;
-                            store16(out + j, w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const float* h = acc + 16 * j + 4 * i;
+                            w[i] = fp8_pair(h[0] * inv, h[1] * inv) | fp8_pair(h[2] * inv, h[3] * inv) << 16;
                         }
+                        store16(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
                     }
-                    if (wg == 0)
-                        (sh ? a.shs : a.hs)[(int64_t)m * (sh ? a.max_rows : a.max_pairs) + p] =
-                            __fdiv_rn(bm, 448.0f);
+                    __syncwarp();
+                    uint8_t* out = (sh ? a.shq : a.hq) + (int64_t)(start + q * 32) * ld + i0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2), ch = lane & 3;
+                        if (q * 32 + r < n)
+                            *reinterpret_cast<uint4*>(out + (int64_t)r * ld + ch * 16) =
+                                *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                    }
+                    __syncwarp();   // the next unit writes here
                 }
+                if (wg == 0 && t < n)
+                    (sh ? a.shs : a.hs)[(int64_t)m * (sh ? a.max_rows : a.max_pairs) + start + t] =
+                        __fdiv_rn(bm, 448.0f);
             } else if (MODE == kDown) {
-                const int64_t p = (int64_t)(sh ? a.g.shared_row0 : 0) + start + t;
-                const float w = sh ? 1.0f : __ldg(a.g.pair_w + start + tc);
+                if (!act) continue;
+                const int64_t p0 = (int64_t)(sh ? a.g.shared_row0 : 0) + start + q * 32;
+                // the slot of the unit's last block
+                const float w = sh ? 1.0f : reinterpret_cast<const float*>(base + kPwOff)[((slot - 1) & (kSlots - 1)) * 128 + t];
+                const int h0 = m * 256 + wg * 128;
                 bool big = false;
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
                     // fp16 holds |v| < 65504: a quarter of 32 columns whose largest
                     // finite magnitude is 2^15 or more is stored as v * 2^-s, s its
                     // exponent above 2^14 (see gemm.cu)
-                    uint32_t mb = 0;
+                    float mx = 0.0f;   // fmaxf skips NaN
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         acc[c + j] *= w;
-                        const uint32_t ab = __float_as_uint(acc[c + j]) & 0x7FFFFFFFu;
-                        mb = max(mb, ab < 0x7F800000u ? ab : 0u);
+                        mx = fmaxf(mx, fabsf(acc[c + j]));
                     }
-                    const int sft = (int)(mb >> 23) - 141;
-                    const uint32_t st = sft > 0 ? (uint32_t)sft : 0u;
-                    if (st) {
-                        big = true;
+                    uint32_t st = 0;
+                    if (mx >= 32768.0f) {
+                        uint32_t mb = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const uint32_t ab = __float_as_uint(acc[c + j]) & 0x7FFFFFFFu;
+                            mb = max(mb, ab < 0x7F800000u ? ab : 0u);
+                        }
+                        const int sft = (int)(mb >> 23) - 141;
+                        st = sft > 0 ? (uint32_t)sft : 0u;
+                        big = big || st != 0;
                         const float f = __uint_as_float((127u - st) << 23);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) acc[c + j] *= f;
                     }
-                    if (t < n) {
-                        const int h0 = m * 256 + wg * 128 + c;
-                        __half* out = a.g.ys + p * a.g.H + h0;
+                    if (t < n) a.g.ysx[(int64_t)((h0 + c) >> 5) * a.g.ld_x + p0 + lane] = (uint8_t)st;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            store16(out + j, half2_bits(acc[c + j], acc[c + j + 1]),
-                                    half2_bits(acc[c + j + 2], acc[c + j + 3]),
-                                    half2_bits(acc[c + j + 4], acc[c + j + 5]),
-                                    half2_bits(acc[c + j + 6], acc[c + j + 7]));
-                        a.g.ysx[(int64_t)(h0 >> 5) * a.g.ld_x + p] = (uint8_t)st;
+                    for (int j = 0; j < 4; ++j) {
+                        const float* v = acc + c + 8 * j;
+                        store16(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), half2_bits(v[0], v[1]),
+                                half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
                     }
+                    __syncwarp();
+                    __half* out = a.g.ys + p0 * a.g.H + h0 + c;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2), ch = lane & 3;
+                        if (q * 32 + r < n)
+                            *reinterpret_cast<uint4*>(out + (int64_t)r * a.g.H + ch * 8) =
+                                *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                    }
+                    __syncwarp();   // written again
                 }
                 if (big && t < n) *a.g.scaled = 1;
-            } else if (t < n) {
-                const int n0 = m * 256 + wg * 128;
-                const int64_t o = (int64_t)(start + t) * a.ldy + n0;
-                if (a.ydtype == MOE_F32) {
-                    float* y = static_cast<float*>(a.y) + o;
+            } else {
+                if (!act) continue;
+                const bool f32 = a.ydtype == MOE_F32, bf = a.ydtype == MOE_BF16;
+                const int es = f32 ? 4 : 2;
+                // 64 bytes of a row at a time: 16 fp32 or 32 16-bit columns
 #pragma unroll
-                    for (int j = 0; j < 128; j += 4) {
-                        if (a.y_vec && n0 + j + 4 <= a.N)
-                            store16(y + j, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
-                                    __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]));
-                        else
+                for (int part = 0; part < 8; ++part) {
+                    if (!f32 && part >= 4) break;
+                    const int n0 = m * 256 + wg * 128 + part * (f32 ? 16 : 32);
+                    if (n0 >= a.N) break;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (n0 + j + i < a.N) y[j + i] = acc[j + i];
-                    }
-                } else {
-                    uint16_t* y = static_cast<uint16_t*>(a.y) + o;
-                    const bool bf = a.ydtype == MOE_BF16;
-#pragma unroll
-                    for (int j = 0; j < 128; j += 8) {
+                    for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = bf ? bf162_bits(acc[j + 2 * i], acc[j + 2 * i + 1])
-                                      : half2_bits(acc[j + 2 * i], acc[j + 2 * i + 1]);
-                        if (a.y_vec && n0 + j + 8 <= a.N)
-                            store16(y + j, w[0], w[1], w[2], w[3]);
-                        else
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (n0 + j + i < a.N) y[j + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                        for (int i = 0; i < 4; ++i) {
+                            if (f32) {
+                                w[i] = __float_as_uint(acc[16 * part + 4 * j + i]);
+                            } else {
+                                const float* v = acc + (32 * part + 8 * j + 2 * i) % 128;
+                                w[i] = bf ? bf162_bits(v[0], v[1]) : half2_bits(v[0], v[1]);
+                            }
+                        }
+                        store16(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
                     }
+                    __syncwarp();
+                    uint8_t* out = static_cast<uint8_t*>(a.y) + ((int64_t)(start + q * 32) * a.ldy + n0) * es;
+                    const int64_t ldb = a.ldy * es;
+                    const int cb = min(64, (a.N - n0) * es);   // bytes of each row
+                    if (a.y_vec) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + (lane >> 2), ch = lane & 3;
+                            const uint8_t* src = stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+                            uint8_t* dst = out + r * ldb + ch * 16;
+                            if (q * 32 + r >= n) continue;
+                            if (ch * 16 + 16 <= cb)
+                                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+                            else
+                                for (int b = 0; ch * 16 + b < cb; b += 2)   // the row's end
+                                    *reinterpret_cast<uint16_t*>(dst + b) = *reinterpret_cast<const uint16_t*>(src + b);
+                        }
+                    } else {   // rows at any element: a row at a time, an element per lane
+                        const int nr = min(32, n - q * 32);
+                        for (int r = 0; r < nr; ++r) {
+                            const int b = lane * es;
+                            if (b >= cb) continue;
+                            const uint8_t* src = stg + r * 64 + (((b >> 4) ^ ((r >> 1) & 3)) << 4) + (b & 15);
+                            if (f32) *reinterpret_cast<uint32_t*>(out + r * ldb + b) = *reinterpret_cast<const uint32_t*>(src);
+                            else *reinterpret_cast<uint16_t*>(out + r * ldb + b) = *reinterpret_cast<const uint16_t*>(src);
+                        }
+                    }
+                    __syncwarp();   // written again
                 }
             }
         }
@@ -567,7 +636,7 @@ static cudaError_t set_attr() {
     // the register split draws on what the CTA is launched with
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, k_fp8_gemm<MODE>)) != cudaSuccess) return e;
-    return fa.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidDeviceFunction;
+    return fa.numRegs == (MODE == kGateUp ? kLaunchRegsGU : kLaunchRegs) ? cudaSuccess : cudaErrorInvalidDeviceFunction;
 }
 
 cudaError_t fp8_gemm_set_attributes() {
@@ -579,7 +648,7 @@ cudaError_t fp8_gemm_set_attributes() {
 cudaError_t launch_fp8_gemm(int mode, const Fp8Maps& m, const Fp8GemmArgs& a, int num_sms,
                             cudaStream_t st) {
     auto k = mode == kGateUp ? k_fp8_gemm<kGateUp> : mode == kDown ? k_fp8_gemm<kDown> : k_fp8_gemm<kDense>;
-    return launch_kernel(k, dim3(num_sms), dim3(kThreads), kSmem, st, m.w0, m.w1, m.s0, m.s1, m.a0,
+    return launch_kernel(k, dim3(num_sms), dim3(mode == kGateUp ? kThreadsGU : kThreads), kSmem, st, m.w0, m.w1, m.s0, m.s1, m.a0,
                          m.a1, a);
 }
 

@@ -1,5 +1,6 @@
 // Host side of the calls that need no plan: moe_route_scored, moe_fp8_quantize
 // and moe_fp8_gemm.  Arguments are checked here, before anything is launched.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cmath>
@@ -31,11 +32,28 @@ moe_status check_dtype(int dt) {
     return MOE_OK;
 }
 
-// SMs of the current device.
-moe_status sm_count(int* n) {
+// SMs of the current device, looked up once per device; with `gemm` the GEMM
+// kernels' attributes are set there too.  A device's entry holds what is done:
+// 0 nothing, else the SM count, plus kAttr once the attributes are set.
+constexpr int kMaxDevices = 64, kAttr = 1 << 20;
+std::atomic<int> g_device[kMaxDevices];
+
+moe_status device_ready(bool gemm, int* sms) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
+    int have = e == cudaSuccess ? g_device[dev].load(std::memory_order_acquire) : 0;
+    if (e == cudaSuccess && !(have & (kAttr - 1))) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        have |= n;
+        if (e == cudaSuccess) g_device[dev].fetch_or(n, std::memory_order_release);
+    }
+    if (e == cudaSuccess && gemm && !(have & kAttr)) {
+        e = fp8_gemm_set_attributes();
+        if (e == cudaSuccess) g_device[dev].fetch_or(kAttr, std::memory_order_release);
+    }
+    *sms = have & (kAttr - 1);
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
 }
 
@@ -84,7 +102,7 @@ moe_status moe_route_scored(const moe_route_rule* rule, const void* logits, moe_
         (topk_score && !aligned(topk_score, 4)))
         return fail(MOE_ERR_INVALID_ARG, "topk_idx/topk_w NULL, or an output misaligned");
     int sms = 0;
-    if ((s = sm_count(&sms)) != MOE_OK) return s;
+    if ((s = device_ready(false, &sms)) != MOE_OK) return s;
     RouteScoredArgs a{logits, row_stride, R, E, k, select_bias, *rule, gs,
                       (uint32_t)(((1u << 20) + gs - 1) / gs), topk_idx, topk_w, topk_score};
     return launched(launch_route_scored(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)),
@@ -103,7 +121,7 @@ moe_status moe_fp8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, 
     if (!codes || !scales || !aligned(scales, 4))
         return fail(MOE_ERR_INVALID_ARG, "codes/scales NULL or misaligned");
     int sms = 0;
-    if ((s = sm_count(&sms)) != MOE_OK) return s;
+    if ((s = device_ready(false, &sms)) != MOE_OK) return s;
     Fp8QuantArgs a{x, row_stride, R, K, static_cast<uint8_t*>(codes), scales};
     return launched(launch_fp8_quantize(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)),
                     "quantise launch");
@@ -138,9 +156,12 @@ moe_status moe_fp8_gemm(const void* xq, const float* xs, int32_t R, const void* 
     if (workspace_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     int sms = 0;
-    if ((s = sm_count(&sms)) != MOE_OK) return s;
-    cudaError_t e = fp8_gemm_set_attributes();
-    if (e != cudaSuccess) return launched(e, "kernel attributes");
+    if ((s = device_ready(true, &sms)) != MOE_OK) return s;
+    if (fp8_rows_applies(R, N, K, sms)) {
+        Fp8RowsArgs ra{static_cast<const uint8_t*>(xq), xs, static_cast<const uint8_t*>(wq), ws, R, N, K, y,
+                       row_stride, dtype};
+        return launched(launch_fp8_rows(ra, reinterpret_cast<cudaStream_t>(stream)), "gemm launch");
+    }
     Fp8Maps m{};
     if (!encode_fp8(&m.w0, wq, (uint64_t)K, (uint64_t)N, 0) || !encode_fp8(&m.a0, xq, (uint64_t)K, (uint64_t)R, 0))
         return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");

@@ -98,6 +98,7 @@ class RouteRule:
         object.__setattr__(self, "_c", moe_route_rule(
             _SCORES[self.score], self.n_groups, self.top_groups, _GROUP_SCORES[self.group_score],
             int(self.renormalize), self.scale))
+        object.__setattr__(self, "_ref", ctypes.byref(self._c))
 
 
 _lib = None
@@ -186,16 +187,23 @@ def _check(rc: int):
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream, device: int | None = None) -> int:
+    """The raw stream of a call: ``stream``, or the current one of ``device``."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if device is None else device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None):
+    # the common case with few attribute reads: a small call costs the GPU less
+    # time than its checks cost the host
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -210,6 +218,9 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
 
 def _need_rows(t: torch.Tensor, name: str, shape=None) -> int:
     """A matrix of a float type whose rows are contiguous; returns the row stride."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES and t.dim() == 2
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return t.shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -224,12 +235,23 @@ def _need_rows(t: torch.Tensor, name: str, shape=None) -> int:
     return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
 
 
-def _same_device(*tensors):
-    """The device of the tensors given (None: not given), which must be one."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+def _same_device(*tensors) -> int:
+    """The index of the tensors' device (None: not given), which must be one."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on different devices: "
+                             f"{sorted({str(t.device) for t in tensors if t is not None})}")
+    return dev
+
+
+def _on(device: int, fn, *args):
+    """Call the library with ``device`` current."""
+    if torch.cuda.current_device() == device:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
 
 
 def moe_version() -> int:
@@ -316,7 +338,8 @@ class Plan:
         self = cls.__new__(cls)
         self.dims = d
         self.weights = (w_router, *tensors)
-        self.device = _same_device(w_router, *tensors)
+        _same_device(w_router, *tensors)
+        self.device = w_router.device
         self.bits = 8
         w = moe_fp8_weights(*[t.data_ptr() for t in tensors])
         h = ctypes.c_void_p()
@@ -534,9 +557,8 @@ def moe_route_scored(logits, rule: RouteRule, topk_idx, topk_w, select_bias=None
     topk_score (fp32 [R, k], the chosen experts' scores)."""
     ld = _need_rows(logits, "logits")
     R, E = logits.shape
-    _need(topk_idx, "topk_idx", torch.int32)
-    if topk_idx.dim() != 2:
-        raise ValueError("topk_idx must have shape [R, k]")
+    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be a tensor of shape [R, k]")
     k = topk_idx.shape[1]
     _need(topk_idx, "topk_idx", torch.int32, (R, k))
     _need(topk_w, "topk_w", torch.float32, (R, k))
@@ -544,10 +566,9 @@ def moe_route_scored(logits, rule: RouteRule, topk_idx, topk_w, select_bias=None
         _need(select_bias, "select_bias", torch.float32, (E,))
     if topk_score is not None:
         _need(topk_score, "topk_score", torch.float32, (R, k))
-    with torch.cuda.device(_same_device(logits, topk_idx, topk_w, select_bias, topk_score)):
-        _check(load().moe_route_scored(ctypes.byref(rule._c), _ptr(logits), _DTYPES[logits.dtype],
-                                       ld, R, E, k, _ptr(select_bias), _ptr(topk_idx),
-                                       _ptr(topk_w), _ptr(topk_score), _stream(stream)))
+    dev = _same_device(logits, topk_idx, topk_w, select_bias, topk_score)
+    _on(dev, load().moe_route_scored, rule._ref, _ptr(logits), _DTYPES[logits.dtype], ld, R, E, k,
+        _ptr(select_bias), _ptr(topk_idx), _ptr(topk_w), _ptr(topk_score), _stream(stream, dev))
 
 
 def moe_fp8_quantize(x, codes, scales, stream=None):
@@ -557,9 +578,9 @@ def moe_fp8_quantize(x, codes, scales, stream=None):
     R, K = x.shape
     _need(codes, "codes", torch.float8_e4m3fn, (R, K))
     _need(scales, "scales", torch.float32, (-(-K // 128), R))
-    with torch.cuda.device(_same_device(x, codes, scales)):
-        _check(load().moe_fp8_quantize(_ptr(x), _DTYPES[x.dtype], ld, R, K, _ptr(codes),
-                                       _ptr(scales), _stream(stream)))
+    dev = _same_device(x, codes, scales)
+    _on(dev, load().moe_fp8_quantize, _ptr(x), _DTYPES[x.dtype], ld, R, K, _ptr(codes),
+        _ptr(scales), _stream(stream, dev))
 
 
 def moe_fp8_gemm_workspace_bytes(R: int, N: int, K: int) -> int:
@@ -585,10 +606,9 @@ def moe_fp8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
     _need(wq, "wq", torch.float8_e4m3fn, (N, K))
     _need(ws, "ws", torch.float32, (-(-N // 128), kb))
     _need(workspace, "workspace", torch.uint8)
-    with torch.cuda.device(_same_device(xq, xs, wq, ws, y, workspace)):
-        _check(load().moe_fp8_gemm(_ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
-                                   _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(),
-                                   _stream(stream)))
+    dev = _same_device(xq, xs, wq, ws, y, workspace)
+    _on(dev, load().moe_fp8_gemm, _ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
+        _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(), _stream(stream, dev))
 
 
 def moe_read_device_status(workspace: torch.Tensor, stream=None) -> dict:
