@@ -306,10 +306,10 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
             return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activation codes");
         const Fp8Regions rx = fp8_regions(p, workspace, R);
         if (e == cudaSuccess)
-            e = launch_fp8_quantize(Fp8QuantArgs{x, d.H, R, d.H, rx.xq, rx.xs}, MOE_BF16, p->num_sms, st);
-        if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
+            e = launch_fp8_front(sa, Fp8QuantArgs{x, d.H, R, d.H, rx.xq, rx.xs}, small, p->num_sms, st);
+    } else if (e == cudaSuccess) {
+        e = launch_scatter(sa, small, p->num_sms, st);
     }
-    if (e == cudaSuccess) e = launch_scatter(sa, small, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "scatter launch");
     if ((e = mark(1)) == cudaSuccess)
         e = fs ? launch_fp8_stream(kGateUp, mg, fg, p->num_sms, st)

@@ -48,6 +48,8 @@ struct Fp8QuantArgs {
     float* scales;        // [ceil(K / 128), R]
 };
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs&, int dtype, int num_sms, cudaStream_t);
+// The scatter and the quantising of bf16 x (rows 16-byte aligned, K a multiple of 8).
+cudaError_t launch_fp8_front(const ScatterArgs&, const Fp8QuantArgs&, bool small, int num_sms, cudaStream_t);
 
 // GEMM modes (kGateUp and kDown as in kernels.cuh).
 constexpr int kDense = 2;

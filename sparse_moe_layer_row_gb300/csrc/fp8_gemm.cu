@@ -23,7 +23,7 @@
 //
 // Persistent, one CTA per SM, 384 threads (gate/up: 512):
 //   warp 0 lane 0   TMA producer: weight tiles (2 x 16 KB) and, but for
-//                   gate/up, the rows' tile (16 KB) into a ring of 4 stages
+//                   gate/up, the rows' tile (16 KB) into a ring of 3 stages
 //   warp 1          TMEM allocation; lane 0 issues the MMAs
 //   warps 4..11     promotion and epilogue: lane quadrant warp & 3, columns by
 //                   warpgroup
@@ -35,8 +35,9 @@
 //                   all of it arrives on the slot's `rfull` when it lands
 // Registers are moved from the other warpgroups to the promotion warps, which
 // hold 128 accumulators each.  A promotion warp whose 32 rows lie past the
-// unit's only passes the buffers on.  Outputs go through 2 KB of shared memory
-// per warp, so that 4 lanes store 64 consecutive bytes of a row.
+// unit's only passes the buffers on.  Outputs are staged in shared memory, a row
+// per lane, and stored 256 consecutive bytes of a row at a time (one bulk copy
+// per row instead: the same time).
 // Every wait is bounded: a wait that gives up raises a CTA-wide abort flag and
 // a device status counter, and all roles leave their loops; before the CTA
 // exits its copies and MMAs in flight are waited for (with their own limit),
@@ -50,18 +51,20 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
 
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kThreads = 384, kThreadsGU = 512;
 constexpr int kTile = 128 * 128;                 // 128 rows x 128 codes
 constexpr int kStageBytes = 3 * kTile;           // rows, weights 0, weights 1
 constexpr int kAmaxOff = kStages * kStageBytes;       // uint32 [2 units][2 warpgroups][128 rows]
-constexpr int kStgOff = kAmaxOff + 2 * 2 * 128 * 4;   // 32 rows x 64 bytes per promotion warp
+constexpr int kStgOff = kAmaxOff + 2 * 2 * 128 * 4;   // per promotion warp: 32 rows of 256 bytes,
+constexpr int kStgRow = 256 + 16;                     // 16 apart, so that 8 lanes' chunks share no bank
+constexpr int kStgWarp = 32 * kStgRow;
 // Slots of the loaders' scales, one per fill of a stage, in turn, each with its barrier.  The fill kSlots later
 // reuses a slot: it follows the MMA of the fill kSlots - kStages later, which follows the
 // promotion (two TMEM buffers) of the fill kSlots - kStages - 2 later.
 constexpr int kSlots = 8;
 static_assert(kSlots - kStages - 2 > 0 && (kSlots & (kSlots - 1)) == 0, "a slot outlives its promotion and epilogue");
-constexpr int kSxOff = kStgOff + 8 * 2048;            // float [kSlots][128]: row scales
+constexpr int kSxOff = kStgOff + 8 * kStgWarp;            // float [kSlots][128]: row scales
 constexpr int kPwOff = kSxOff + kSlots * 512;         // float [kSlots][128]: pair weights (down)
 constexpr int kSwOff = kPwOff + kSlots * 512;         // float [kSlots][2]: weight block scales
 constexpr int kRowsOff = kSwOff + kSlots * 8;         // int [128]: the loaders' rows of x
@@ -71,7 +74,7 @@ constexpr int kTmemCols = 512;                   // two buffers of 256 columns
 // registers per thread after the split: the pool is what the CTA was launched
 // with (kThreads x kLaunchRegs), checked on the host before any launch
 constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
-constexpr int kLaunchRegsGU = 128, kFewRegsGU = 48, kManyRegsGU = 208;
+constexpr int kLaunchRegsGU = 128, kFewRegsGU = 40, kManyRegsGU = 216;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
 static_assert(256 * kFewRegsGU + 256 * kManyRegsGU <= kThreadsGU * kLaunchRegsGU, "register split");
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -133,6 +136,20 @@ __device__ __forceinline__ void promote16(float* acc, const uint32_t (&v)[16], f
 
 __device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+
+// Rows of up to 256 staged bytes to global memory by the warp: 16 lanes a row.
+__device__ __forceinline__ void copy_rows(const uint8_t* stg, uint8_t* out, int64_t ld, int bytes, int rows,
+                                          int lane) {
+    __syncwarp();
+    const int ch = (lane & 15) * 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (r < rows && ch < bytes)
+            *reinterpret_cast<uint4*>(out + r * ld + ch) = *reinterpret_cast<const uint4*>(stg + r * kStgRow + ch);
+    }
+    __syncwarp();   // written again
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
@@ -367,8 +384,7 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 const int nkb = blocks(un.x);
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!mbar_wait_bounded(full + stage, phase, abort_flag, kWaitNs) ||
-                        (MODE == kGateUp &&
-                         !mbar_wait_bounded(rfull + slot, rphase, abort_flag, kWaitNs)) ||
+                        !mbar_wait_bounded(rfull + slot, rphase, abort_flag, kWaitNs) ||
                         !mbar_wait_bounded(tempty + buf, bphase ^ 1u, abort_flag, kWaitNs)) {
                         give_up();
                         ok = false;
@@ -412,11 +428,11 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
         const uint32_t col1 = (uint32_t)(MODE == kGateUp ? 128 + wg * 64 : wg * 128 + 64);
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
         uint32_t* s_amax = reinterpret_cast<uint32_t*>(base + kAmaxOff);
-        uint8_t* stg = base + kStgOff + (warp - 4) * 2048;
-        const float* s_sx = reinterpret_cast<const float*>(base + kSxOff) + t;
-        const float* s_sw = reinterpret_cast<const float*>(base + kSwOff);
+        uint8_t* stg = base + kStgOff + (warp - 4) * kStgWarp;
+        const volatile float* s_sx = reinterpret_cast<const volatile float*>(base + kSxOff) + t;
+        const volatile float* s_sw = reinterpret_cast<const volatile float*>(base + kSwOff);
         int buf = 0, upar = 0, slot = 0;
-        uint32_t bphase = 0, xphase = 0, phase = 0;
+        uint32_t bphase = 0, xphase = 0;
         bool alive = true;
         int4 next = ufirst < nunits ? unit(ufirst) : make_int4(0, 0, 0, 0);
         for (int u = ufirst; alive && u < nunits; u += nact) {
@@ -430,17 +446,19 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            bool ok;
             for (int kb = 0; kb < nkb; ++kb) {
-                // the scales have landed (with or before what the MMA read)
-                bool ok = mbar_wait_bounded(rfull + slot, phase, abort_flag, kWaitNs);
-                const float sx = s_sx[slot * 128];
-                const float f0 = sx * s_sw[slot * 2 + (MODE == kGateUp ? 0 : wg)];
-                const float f1 = sx * s_sw[slot * 2 + (MODE == kGateUp ? 1 : wg)];
-                if (++slot == kSlots) { slot = 0; phase ^= 1u; }
-                ok = ok && mbar_wait_bounded(tfull + buf, bphase, abort_flag, kWaitNs);
+                ok = mbar_wait_bounded(tfull + buf, bphase, abort_flag, kWaitNs);
                 if (__any_sync(0xffffffffu, !ok)) { give_up(); alive = false; break; }
                 tc_fence_after();
                 const uint32_t tb = tq + (uint32_t)(buf * 256);
+                // the block's scales: the MMA thread saw their slot land before it issued
+                // the MMAs that this wait was for (a wait of each warp's own for the slot
+                // took 13 of 88 us at 8192 x 4096 x 2048)
+                const float sx = s_sx[slot * 128];
+                const float f0 = sx * s_sw[slot * 2 + (MODE == kGateUp ? 0 : wg)];
+                const float f1 = sx * s_sw[slot * 2 + (MODE == kGateUp ? 1 : wg)];
+                slot = (slot + 1) & (kSlots - 1);
                 if (act) {
                     uint32_t v[2][16];   // the next 16 columns are read while these are added
                     tmem_ld16_async(tb + col0, v[0]);
@@ -476,7 +494,7 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 uint32_t* am = s_amax + upar * 256;
                 am[wg * 128 + t] = mx;
                 mbar_arrive(xbar);
-                const bool ok = mbar_wait_bounded(xbar, xphase, abort_flag, kWaitNs);
+                ok = mbar_wait_bounded(xbar, xphase, abort_flag, kWaitNs);
                 if (__any_sync(0xffffffffu, !ok)) { give_up(); alive = false; break; }
                 mx = max(mx, am[(wg ^ 1) * 128 + t]);
                 upar ^= 1;
@@ -487,8 +505,8 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 const float inv = __fdiv_rn(448.0f, bm);
                 const int ld = sh ? a.g.Is : a.g.I;
                 const int i0 = m * 128 + wg * 64;   // I, Is are multiples of 64
-                if (act && i0 < ld) {
-                    // 64 codes of a row: four 16-byte chunks, swizzled over the row pairs
+                if (act && i0 < ld) {   // 64 codes of a row, 80 bytes apart
+                        uint8_t* row = stg + lane * 80;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
@@ -497,18 +515,18 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                             const float* h = acc + 16 * j + 4 * i;
                             w[i] = fp8_pair(h[0] * inv, h[1] * inv) | fp8_pair(h[2] * inv, h[3] * inv) << 16;
                         }
-                        store16(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+                        store16(row + 16 * j, w[0], w[1], w[2], w[3]);
                     }
                     __syncwarp();
                     uint8_t* out = (sh ? a.shq : a.hq) + (int64_t)(start + q * 32) * ld + i0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (lane >> 2), ch = lane & 3;
+                        const int r = 8 * i + (lane >> 2), ch = (lane & 3) * 16;
                         if (q * 32 + r < n)
-                            *reinterpret_cast<uint4*>(out + (int64_t)r * ld + ch * 16) =
-                                *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                            *reinterpret_cast<uint4*>(out + (int64_t)r * ld + ch) =
+                                *reinterpret_cast<const uint4*>(stg + r * 80 + ch);
                     }
-                    __syncwarp();   // the next unit writes here
+                    __syncwarp();   // written again
                 }
                 if (wg == 0 && t < n)
                     (sh ? a.shs : a.hs)[(int64_t)m * (sh ? a.max_rows : a.max_pairs) + start + t] =
@@ -519,6 +537,7 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 // the slot of the unit's last block
                 const float w = sh ? 1.0f : reinterpret_cast<const float*>(base + kPwOff)[((slot - 1) & (kSlots - 1)) * 128 + t];
                 const int h0 = m * 256 + wg * 128;
+                uint8_t* row = stg + lane * kStgRow;
                 bool big = false;
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
@@ -550,73 +569,53 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float* v = acc + c + 8 * j;
-                        store16(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), half2_bits(v[0], v[1]),
-                                half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
+                        store16(row + 2 * c + 16 * j, half2_bits(v[0], v[1]), half2_bits(v[2], v[3]),
+                                half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
                     }
-                    __syncwarp();
-                    __half* out = a.g.ys + p0 * a.g.H + h0 + c;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (lane >> 2), ch = lane & 3;
-                        if (q * 32 + r < n)
-                            *reinterpret_cast<uint4*>(out + (int64_t)r * a.g.H + ch * 8) =
-                                *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-                    }
-                    __syncwarp();   // written again
                 }
+                copy_rows(stg, reinterpret_cast<uint8_t*>(a.g.ys + p0 * a.g.H + h0), (int64_t)a.g.H * 2, 256,
+                          n - q * 32, lane);
                 if (big && t < n) *a.g.scaled = 1;
             } else {
                 if (!act) continue;
                 const bool f32 = a.ydtype == MOE_F32, bf = a.ydtype == MOE_BF16;
                 const int es = f32 ? 4 : 2;
-                // 64 bytes of a row at a time: 16 fp32 or 32 16-bit columns
+                uint8_t* row = stg + lane * kStgRow;
+                // 256 bytes of a row at a time: 64 fp32 or 128 16-bit columns
 #pragma unroll
-                for (int part = 0; part < 8; ++part) {
-                    if (!f32 && part >= 4) break;
-                    const int n0 = m * 256 + wg * 128 + part * (f32 ? 16 : 32);
-                    if (n0 >= a.N) break;
+                for (int part = 0; part < 2; ++part) {
+                    const int n0 = m * 256 + wg * 128 + part * 64;
+                    if ((part && !f32) || n0 >= a.N) break;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 16; ++j) {
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (f32) {
-                                w[i] = __float_as_uint(acc[16 * part + 4 * j + i]);
+                                w[i] = __float_as_uint(acc[64 * part + 4 * j + i]);
                             } else {
-                                const float* v = acc + (32 * part + 8 * j + 2 * i) % 128;
+                                const float* v = acc + 8 * j + 2 * i;
                                 w[i] = bf ? bf162_bits(v[0], v[1]) : half2_bits(v[0], v[1]);
                             }
                         }
-                        store16(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+                        store16(row + 16 * j, w[0], w[1], w[2], w[3]);
                     }
-                    __syncwarp();
                     uint8_t* out = static_cast<uint8_t*>(a.y) + ((int64_t)(start + q * 32) * a.ldy + n0) * es;
                     const int64_t ldb = a.ldy * es;
-                    const int cb = min(64, (a.N - n0) * es);   // bytes of each row
-                    if (a.y_vec) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = i * 8 + (lane >> 2), ch = lane & 3;
-                            const uint8_t* src = stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-                            uint8_t* dst = out + r * ldb + ch * 16;
-                            if (q * 32 + r >= n) continue;
-                            if (ch * 16 + 16 <= cb)
-                                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-                            else
-                                for (int b = 0; ch * 16 + b < cb; b += 2)   // the row's end
-                                    *reinterpret_cast<uint16_t*>(dst + b) = *reinterpret_cast<const uint16_t*>(src + b);
-                        }
-                    } else {   // rows at any element: a row at a time, an element per lane
+                    const int cb = min(256, (a.N - n0) * es);   // bytes of each row
+                    if (a.y_vec && cb % 16 == 0) {
+                        copy_rows(stg, out, ldb, cb, n - q * 32, lane);
+                    } else {   // rows at any element: a row at a time, consecutive elements per lane
+                        __syncwarp();
                         const int nr = min(32, n - q * 32);
-                        for (int r = 0; r < nr; ++r) {
-                            const int b = lane * es;
-                            if (b >= cb) continue;
-                            const uint8_t* src = stg + r * 64 + (((b >> 4) ^ ((r >> 1) & 3)) << 4) + (b & 15);
-                            if (f32) *reinterpret_cast<uint32_t*>(out + r * ldb + b) = *reinterpret_cast<const uint32_t*>(src);
-                            else *reinterpret_cast<uint16_t*>(out + r * ldb + b) = *reinterpret_cast<const uint16_t*>(src);
-                        }
+                        for (int r = 0; r < nr; ++r)
+                            for (int b = lane * es; b < cb; b += 32 * es) {
+                                const uint8_t* src = stg + r * kStgRow + b;
+                                if (f32) *reinterpret_cast<uint32_t*>(out + r * ldb + b) = *reinterpret_cast<const uint32_t*>(src);
+                                else *reinterpret_cast<uint16_t*>(out + r * ldb + b) = *reinterpret_cast<const uint16_t*>(src);
+                            }
+                        __syncwarp();   // written again
                     }
-                    __syncwarp();   // written again
                 }
             }
         }

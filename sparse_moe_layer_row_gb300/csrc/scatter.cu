@@ -15,8 +15,6 @@
 
 namespace moe {
 
-constexpr int kScatThreads = 256;
-
 // Large batches: a counting sort of the surviving (row, slot) pairs by expert,
 // in three kernels, all parallel over blocks of rows:
 //   k_scatter_hist   per block: pairs per expert (hist[b][e]) and each pair's
@@ -31,62 +29,10 @@ constexpr int kScatThreads = 256;
 // No copy of x is made: the gate/up GEMM gathers its rows of x itself.
 // A row that names the same expert twice contributes its first slot only
 // (later duplicates are counted as bad ids).
-constexpr int kHistRows = 32;
-
 __global__ void __launch_bounds__(kScatThreads) k_scatter_hist(ScatterArgs a) {
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
-    __shared__ uint8_t s_slot[kHistRows][kMaxExperts];
-    __shared__ int s_run[kMaxExperts];
-    __shared__ int s_dup, s_live;
-    const int b = blockIdx.x, tid = threadIdx.x;
-    const int E = a.E, k = a.k;
-    const int words = (E + 31) >> 5;
-    int r0 = a.off[b], r1 = a.off[b + 1];
-    if (!(0 <= r0 && r0 <= r1 && r1 <= a.R)) r1 = r0 = 0;  // counted by the coreset call
-    for (int e = tid; e < E; e += blockDim.x) s_run[e] = 0;
-    if (tid == 0) { s_dup = 0; s_live = 0; }
-    if (b == 0 && tid == 0) {
-        a.misc[0] = 0;  // ticket of k_scatter_scan (next launch)
-        a.misc[4] = 0;  // no staged output scaled yet (the down GEMM sets it)
-    }
-    for (int c0 = r0; c0 < r1; c0 += kHistRows) {
-        const int nr = min(kHistRows, r1 - c0);
-        __syncthreads();
-        for (int i = tid; i < nr * E; i += blockDim.x) s_slot[i / E][i % E] = 0xFF;
-        __syncthreads();
-        for (int rr = tid; rr < nr; rr += blockDim.x) {
-            const int r = c0 + rr;
-            const bool lv = !a.live || a.live[r] != 0;  // dead rows: no pairs
-            if (lv) atomicAdd(&s_live, 1);
-            int dup = 0;
-            for (int j = 0; j < k; ++j) {
-                const int e = a.topk_idx[(size_t)r * k + j];
-                a.prank[(size_t)r * k + j] = -1;
-                if (!lv || e < 0 || e >= E) continue;
-                if (!((a.keep[(size_t)b * words + (e >> 5)] >> (e & 31)) & 1u)) continue;
-                if (s_slot[rr][e] != 0xFF) { ++dup; continue; }
-                s_slot[rr][e] = (uint8_t)j;
-            }
-            if (dup) atomicAdd(&s_dup, dup);
-        }
-        __syncthreads();
-        for (int e = tid; e < E; e += blockDim.x) {
-            int run = s_run[e];
-            for (int rr = 0; rr < nr; ++rr) {
-                const int j = s_slot[rr][e];
-                if (j == 0xFF) continue;
-                a.prank[(size_t)(c0 + rr) * k + j] = run++;
-            }
-            s_run[e] = run;
-        }
-    }
-    __syncthreads();
-    for (int e = tid; e < E; e += blockDim.x) a.hist[(size_t)b * E + e] = s_run[e];
-    if (tid == 0) {
-        a.live_base[b] = s_live;
-        status_add(a.status, MOE_STATUS_BAD_EXPERT_ID, (uint32_t)s_dup);
-    }
+    scatter_hist(a, blockIdx.x);
 }
 
 constexpr int kScanThreads = 256;
@@ -362,9 +308,12 @@ cudaError_t launch_scatter(const ScatterArgs& a, bool small, int num_sms, cudaSt
     (void)num_sms;
     if (small) return launch_kernel(k_scatter_small, dim3(1), dim3(kSmallThreads), 0, st, a);
     cudaError_t e = launch_kernel(k_scatter_hist, dim3(a.nb), dim3(kScatThreads), 0, st, a);
+    return e == cudaSuccess ? launch_scatter_rest(a, st) : e;
+}
+
+cudaError_t launch_scatter_rest(const ScatterArgs& a, cudaStream_t st) {
     const int scan_ctas = (a.E + kScanThreads / 32 - 1) / (kScanThreads / 32);
-    if (e == cudaSuccess)
-        e = launch_kernel(k_scatter_scan, dim3(scan_ctas), dim3(kScanThreads), 0, st, a);
+    cudaError_t e = launch_kernel(k_scatter_scan, dim3(scan_ctas), dim3(kScanThreads), 0, st, a);
     if (e == cudaSuccess) e = launch_kernel(k_scatter_place, dim3(a.nb), dim3(kScatThreads), 0, st, a);
     return e;
 }

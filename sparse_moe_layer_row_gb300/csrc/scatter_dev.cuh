@@ -1,6 +1,7 @@
-// Device code of the forward bookkeeping of the scatter kernels (scatter.cu):
-// block scans, the GEMM unit lists, and the whole small-call scatter in one
-// CTA.
+// Device code of the forward bookkeeping of the scatter kernels (scatter.cu, and
+// fp8_quant.cu, which runs it beside the quantising of x): block scans, the GEMM
+// unit lists, the whole small-call scatter in one CTA, and the large-batch
+// scatter's first step.
 #pragma once
 
 #include "kernels.cuh"
@@ -177,6 +178,65 @@ __device__ __forceinline__ void scatter_small(const ScatterArgs& a, ScatterSmall
         a.misc[3] = tot_pairs;
         a.misc[4] = 0;  // no staged output scaled yet (the down GEMM sets it)
         status_add(a.status, MOE_STATUS_BAD_EXPERT_ID, (uint32_t)sm.s_dup);
+    }
+}
+
+// Threads of the large-batch scatter's kernels.
+constexpr int kScatThreads = 256;
+constexpr int kHistRows = 32;
+
+// The first kernel of the large-batch scatter, for block b, by the whole CTA.
+__device__ __forceinline__ void scatter_hist(const ScatterArgs& a, int b) {
+    __shared__ uint8_t s_slot[kHistRows][kMaxExperts];
+    __shared__ int s_run[kMaxExperts];
+    __shared__ int s_dup, s_live;
+    const int tid = threadIdx.x;
+    const int E = a.E, k = a.k;
+    const int words = (E + 31) >> 5;
+    int r0 = a.off[b], r1 = a.off[b + 1];
+    if (!(0 <= r0 && r0 <= r1 && r1 <= a.R)) r1 = r0 = 0;  // counted by the coreset call
+    for (int e = tid; e < E; e += blockDim.x) s_run[e] = 0;
+    if (tid == 0) { s_dup = 0; s_live = 0; }
+    if (b == 0 && tid == 0) {
+        a.misc[0] = 0;  // ticket of k_scatter_scan (next launch)
+        a.misc[4] = 0;  // no staged output scaled yet (the down GEMM sets it)
+    }
+    for (int c0 = r0; c0 < r1; c0 += kHistRows) {
+        const int nr = min(kHistRows, r1 - c0);
+        __syncthreads();
+        for (int i = tid; i < nr * E; i += blockDim.x) s_slot[i / E][i % E] = 0xFF;
+        __syncthreads();
+        for (int rr = tid; rr < nr; rr += blockDim.x) {
+            const int r = c0 + rr;
+            const bool lv = !a.live || a.live[r] != 0;  // dead rows: no pairs
+            if (lv) atomicAdd(&s_live, 1);
+            int dup = 0;
+            for (int j = 0; j < k; ++j) {
+                const int e = a.topk_idx[(size_t)r * k + j];
+                a.prank[(size_t)r * k + j] = -1;
+                if (!lv || e < 0 || e >= E) continue;
+                if (!((a.keep[(size_t)b * words + (e >> 5)] >> (e & 31)) & 1u)) continue;
+                if (s_slot[rr][e] != 0xFF) { ++dup; continue; }
+                s_slot[rr][e] = (uint8_t)j;
+            }
+            if (dup) atomicAdd(&s_dup, dup);
+        }
+        __syncthreads();
+        for (int e = tid; e < E; e += blockDim.x) {
+            int run = s_run[e];
+            for (int rr = 0; rr < nr; ++rr) {
+                const int j = s_slot[rr][e];
+                if (j == 0xFF) continue;
+                a.prank[(size_t)(c0 + rr) * k + j] = run++;
+            }
+            s_run[e] = run;
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += blockDim.x) a.hist[(size_t)b * E + e] = s_run[e];
+    if (tid == 0) {
+        a.live_base[b] = s_live;
+        status_add(a.status, MOE_STATUS_BAD_EXPERT_ID, (uint32_t)s_dup);
     }
 }
 
