@@ -2,9 +2,11 @@
 // along the row (the value rule is in fp8.cuh).
 //
 // Reads each input once and writes each code and scale once; bound by HBM.  A
-// half-warp takes one (row, block of 128): eight values per lane, the largest
-// magnitude by four xor steps, eight codes per lane as one 8-byte store; four
-// blocks are loaded before the first is used.
+// warp takes two blocks of 128 of a row, one per half-warp: eight values per lane, the
+// largest magnitude by four xor steps, eight codes per lane as one 8-byte store.
+// Four such tasks are loaded before the first is used, and the arithmetic is kept
+// small (16-bit maxima of the raw words, packed fp32, no index division): at 207
+// instructions per task the issue slots bound it, 17 us for 8192 x 2048.
 #include "fp8.cuh"
 #include "scatter_dev.cuh"
 
@@ -16,88 +18,144 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
-// Eight values of a block of 128 that 16 lanes hold: codes (two per word) and the
-// block's a.  The quotient (7/8 v) / (a / 512) by Markstein's method (IBM J. Res. Dev. 34,
-// 1990): with r the correctly rounded reciprocal of d, q0 = n r and q0 + (n - q0 d) r is
-// the correctly rounded n / d (where it is no subnormal, and those have the code 0).
-// Infinities and NaN, where n - q0 d is NaN, take the division itself.
-__device__ __forceinline__ float block_codes(const float (&v)[8], uint32_t (&q)[4]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+// The largest magnitude of a lane's eight values, as fp32 bits (NaN above infinity above
+// every number): for 16-bit types by 16-bit integer maxima of the raw words.
+__device__ __forceinline__ uint32_t amax_words(const uint4& w) {
+    const uint32_t k = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+    return max(m & 0xFFFFu, m >> 16);
+}
+__device__ __forceinline__ uint32_t f32_bits(uint32_t b, __nv_bfloat16) { return b << 16; }
+__device__ __forceinline__ uint32_t f32_bits(uint32_t b, __half) {
+    const __half h = __ushort_as_half((unsigned short)b);
+    return __float_as_uint(__half2float(h)) & 0x7FFFFFFFu;   // a NaN stays one
+}
+
+// Two values at a time (each half as the scalar operation).
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// n / d by Markstein's method (IBM J. Res. Dev. 34, 1990): with r the correctly rounded
+// reciprocal of d, q0 = n r and q0 + (n - q0 d) r is the correctly rounded quotient
+// (where that is no subnormal; here those have the code 0).
+__device__ __forceinline__ float2 quotient2(float2 n, float d, float r) {
+    const float2 q0 = mul2(n, r);
+    return fma2(fma2(q0, -d, n), r, q0);
+}
+
+// Codes of a lane's eight values of a block (two words) and the block's scale; m: the
+// lane's largest magnitude as fp32 bits.  16 lanes hold the block.
+__device__ __forceinline__ float block_codes(const float2 (&v)[4], uint32_t m, uint32_t (&q)[2]) {
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float am = __uint_as_float(fp8_amax_bits(m));
     const float d = am * (1.0f / 512.0f);
-    float w[8];
+    float2 w[4];
+    float scale;
     if (m < 0x7F800000u) {
-        const float r = __frcp_rn(d);
+        const float r = __frcp_rn(d), r448 = 1.0f / 448.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float n = 0.875f * v[i], q0 = n * r;
-            w[i] = __fmaf_rn(__fmaf_rn(-q0, d, n), r, q0);
-        }
-    } else {
+        for (int i = 0; i < 4; ++i) w[i] = quotient2(mul2(v[i], 0.875f), d, r);
+        scale = am * r448;
+        scale = __fmaf_rn(__fmaf_rn(-scale, 448.0f, am), r448, scale);
+    } else {   // an infinity or a NaN, for which n - q0 d is NaN
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __fdiv_rn(0.875f * v[i], d);
+        for (int i = 0; i < 4; ++i)
+            w[i] = make_float2(__fdiv_rn(0.875f * v[i].x, d), __fdiv_rn(0.875f * v[i].y, d));
+        scale = __fdiv_rn(am, 448.0f);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = fp8_pair(w[2 * i], w[2 * i + 1]);
-    return am;
+    for (int i = 0; i < 2; ++i)
+        q[i] = fp8_pair(w[2 * i].x, w[2 * i].y) | fp8_pair(w[2 * i + 1].x, w[2 * i + 1].y) << 16;
+    return scale;
 }
 
-// The (row, block) tasks first, first + step, ... of this half-warp.  VEC: x rows are
-// 16-byte aligned and K is a multiple of 8.
+// The warp's tasks first, first + step, ...: a row's blocks 2 p and 2 p + 1, a block per
+// half-warp.  VEC: x rows are 16-byte aligned and K is a multiple of 8.
 template <typename T, bool VEC>
-__device__ __forceinline__ void quantize_tasks(const Fp8QuantArgs& a, int64_t first, int64_t step) {
-    constexpr int kFlight = VEC && sizeof(T) == 2 ? 4 : 2;   // blocks loaded before the first is used
-    const int kb = fp8_blocks(a.K);
-    const int hl = threadIdx.x & 15;   // lane of the half-warp
-    const int64_t ntasks = (int64_t)a.R * kb;
-    // both half-warps of a warp run the same number of rounds (the shuffles are warp-wide)
-    for (int64_t t0 = first & ~(int64_t)1; t0 < ntasks; t0 += kFlight * step) {
-        float v[kFlight][8];
-        int row[kFlight], col[kFlight];
+__device__ __forceinline__ void quantize_tasks(const Fp8QuantArgs& a, int first, int step) {
+    constexpr bool kWords = VEC && sizeof(T) == 2;
+    constexpr int kFlight = kWords ? 4 : 2;   // tasks loaded before the first is used
+    const int kb = fp8_blocks(a.K), kp = (kb + 1) >> 1;
+    const int hl = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+    // (row, p) of a task, advanced without division
+    int row = first / kp, p = first - row * kp;
+    const int drow = step / kp, dp = step - drow * kp;
+    while (row < a.R) {
+        uint4 raw[kFlight];
+        float2 v[kFlight][4];
+        int rows[kFlight], ps[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-            const int64_t t = t0 + f * step + (first & 1);
-            const bool on = t < ntasks;
-            row[f] = on ? (int)((uint64_t)t < 0x80000000u ? (uint32_t)t / (uint32_t)kb : t / kb) : -1;
-            const int c0 = on ? (int)(t - (int64_t)row[f] * kb) * kFp8Block + hl * 8 : 0;
-            col[f] = c0;
-            const T* src = static_cast<const T*>(a.x) + (int64_t)max(row[f], 0) * a.ld + c0;
-            if (VEC) {
-                constexpr int kWords = (int)sizeof(T) * 8 / 16;   // 16-byte loads of eight values
-                uint4 w[kWords];
-                const bool in = on && c0 < a.K;   // K is a multiple of 8: all eight or none
-#pragma unroll
-                for (int i = 0; i < kWords; ++i)
-                    w[i] = in ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
-                const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[f][i] = to_f32(e[i]);
+            rows[f] = row;
+            ps[f] = p;
+            const int c0 = (2 * p + half) * kFp8Block + hl * 8;
+            const bool on = row < a.R && c0 < a.K;
+            const T* src = static_cast<const T*>(a.x) + (int64_t)row * a.ld + c0;
+            if (kWords) {
+                raw[f] = on ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
             } else {
+                float e[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[f][i] = on && c0 + i < a.K ? to_f32(src[i]) : 0.0f;
+                for (int i = 0; i < 8; ++i) e[i] = 0.0f;
+                if (VEC) {   // fp32
+                    if (on) {
+                        const float4 lo = __ldg(reinterpret_cast<const float4*>(src));
+                        const float4 hi = __ldg(reinterpret_cast<const float4*>(src) + 1);
+                        e[0] = lo.x; e[1] = lo.y; e[2] = lo.z; e[3] = lo.w;
+                        e[4] = hi.x; e[5] = hi.y; e[6] = hi.z; e[7] = hi.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (row < a.R && c0 + i < a.K) e[i] = to_f32(src[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[f][i] = make_float2(e[2 * i], e[2 * i + 1]);
             }
+            row += drow;
+            p += dp;
+            if (p >= kp) { p -= kp; ++row; }
         }
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-            uint32_t q[4];
-            const float am = block_codes(v[f], q);
-            if (row[f] < 0) continue;
-            const int c0 = col[f];
-            uint8_t* dst = a.codes + (int64_t)row[f] * a.K + c0;
+            uint32_t m = 0, q[2];
+            if constexpr (kWords) {
+                m = f32_bits(amax_words(raw[f]), T());
+                const T* e = reinterpret_cast<const T*>(&raw[f]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[f][i] = make_float2(to_f32(e[2 * i]), to_f32(e[2 * i + 1]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    m = max(m, max(__float_as_uint(v[f][i].x) & 0x7FFFFFFFu, __float_as_uint(v[f][i].y) & 0x7FFFFFFFu));
+            }
+            const float scale = block_codes(v[f], m, q);
+            const int b = 2 * ps[f] + half, c0 = b * kFp8Block + hl * 8;
+            if (rows[f] >= a.R || b >= kb) continue;
+            uint8_t* dst = a.codes + (int64_t)rows[f] * a.K + c0;
             if (VEC) {
-                if (c0 < a.K)
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                if (c0 < a.K) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (c0 + i < a.K) dst[i] = (uint8_t)(q[i >> 1] >> (8 * (i & 1)));
+                    if (c0 + i < a.K) dst[i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
             }
-            if (hl == 0) a.scales[(int64_t)(c0 / kFp8Block) * a.R + row[f]] = __fdiv_rn(am, 448.0f);
+            if (hl == 0) a.scales[(int64_t)b * a.R + rows[f]] = scale;
         }
+        __syncwarp();
     }
 }
 
@@ -105,7 +163,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_fp8_quantize(Fp8QuantArgs a) {
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
-    quantize_tasks<T, VEC>(a, (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), (int64_t)gridDim.x * 16);
+    quantize_tasks<T, VEC>(a, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
 }
 
 // The front of an e4m3 plan's forward: the first step of the scatter (all of it for few
@@ -118,9 +176,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_fp8_front_small(ScatterArgs s
     if (blockIdx.x == 0) {
         scatter_small(s, sm);
     } else {
-        constexpr int kHalves = kSmallThreads / 16;
-        quantize_tasks<__nv_bfloat16, true>(a, (int64_t)(blockIdx.x - 1) * kHalves + (threadIdx.x >> 4),
-                                            (int64_t)(gridDim.x - 1) * kHalves);
+        constexpr int kWarps = kSmallThreads / 32;
+        quantize_tasks<__nv_bfloat16, true>(a, (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5), (gridDim.x - 1) * kWarps);
     }
 }
 __global__ void __launch_bounds__(kScatThreads) k_fp8_front_hist(ScatterArgs s, Fp8QuantArgs a) {
@@ -129,9 +186,9 @@ __global__ void __launch_bounds__(kScatThreads) k_fp8_front_hist(ScatterArgs s, 
     if ((int)blockIdx.x < s.nb) {
         scatter_hist(s, blockIdx.x);
     } else {
-        constexpr int kHalves = kScatThreads / 16;
-        quantize_tasks<__nv_bfloat16, true>(a, (int64_t)((int)blockIdx.x - s.nb) * kHalves + (threadIdx.x >> 4),
-                                            (int64_t)((int)gridDim.x - s.nb) * kHalves);
+        constexpr int kWarps = kScatThreads / 32;
+        quantize_tasks<__nv_bfloat16, true>(a, (blockIdx.x - s.nb) * kWarps + (threadIdx.x >> 5),
+                                            (gridDim.x - s.nb) * kWarps);
     }
 }
 
@@ -140,8 +197,8 @@ cudaError_t launch(const Fp8QuantArgs& a, int num_sms, cudaStream_t st) {
     const bool vec = a.K % 8 == 0 && a.ld * (int64_t)sizeof(T) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-    // few tasks: one per half-warp; many: the SMs' share, several in flight each
-    int64_t blocks = ((int64_t)a.R * fp8_blocks(a.K) + 15) / 16;
+    // few tasks: one per warp; many: the SMs' share, several in flight each
+    int64_t blocks = ((int64_t)a.R * ((fp8_blocks(a.K) + 1) / 2) + 7) / 8;
     if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
     return vec ? launch_kernel(k_fp8_quantize<T, true>, dim3((unsigned)blocks), dim3(256), 0, st, a)
                : launch_kernel(k_fp8_quantize<T, false>, dim3((unsigned)blocks), dim3(256), 0, st, a);
@@ -151,13 +208,13 @@ cudaError_t launch(const Fp8QuantArgs& a, int num_sms, cudaStream_t st) {
 
 cudaError_t launch_fp8_front(const ScatterArgs& s, const Fp8QuantArgs& a, bool small, int num_sms,
                              cudaStream_t st) {
-    const int64_t halves = (int64_t)a.R * fp8_blocks(a.K);
+    const int64_t tasks = (int64_t)a.R * ((fp8_blocks(a.K) + 1) / 2);
     if (small) {
-        int64_t blocks = (halves + kSmallThreads / 16 - 1) / (kSmallThreads / 16);
+        int64_t blocks = (tasks + kSmallThreads / 32 - 1) / (kSmallThreads / 32);
         if (blocks > num_sms) blocks = num_sms;
         return launch_kernel(k_fp8_front_small, dim3((unsigned)(1 + blocks)), dim3(kSmallThreads), 0, st, s, a);
     }
-    int64_t blocks = (halves + kScatThreads / 16 - 1) / (kScatThreads / 16);
+    int64_t blocks = (tasks + kScatThreads / 32 - 1) / (kScatThreads / 32);
     if (blocks > (int64_t)num_sms * 6) blocks = (int64_t)num_sms * 6;
     cudaError_t e = launch_kernel(k_fp8_front_hist, dim3((unsigned)(s.nb + blocks)), dim3(kScatThreads), 0, st, s, a);
     return e == cudaSuccess ? launch_scatter_rest(s, st) : e;
