@@ -249,8 +249,11 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     // rows (few pairs per expert: its CTA-pair units would be mostly empty)
     const bool su = small || p->qbits != 0;
     const bool sd = su || R <= kStreamDownRows;
-    const bool fs = p->fp8 && R <= kFp8StreamMaxRows;   // e4m3 weights streamed
-    const int nt_fp8 = fs ? kFp8StreamRows : kFp8Rows;
+    const int groups = (int64_t)R * d.k < d.E ? R * d.k : d.E;   // routed experts that can have pairs
+    const int gu_units = groups * fp8_blocks(d.I) + fp8_blocks(d.Is);
+    const bool fd8 = p->fp8 && fp8_decodes(R, gu_units, p->num_sms);   // e4m3, a single token
+    const bool fs = p->fp8 && !fd8 && fp8_streams(R, d.E, d.k);        // e4m3, weights streamed
+    const int nt_fp8 = fs || fd8 ? kFp8StreamRows : kFp8Rows;
     const int nt_gu = p->fp8 ? nt_fp8 : su ? kSmallN : kLargeNGU;
     const int nt_dn = p->fp8 ? nt_fp8 : sd ? kSmallN : kLargeNDown;
 
@@ -296,13 +299,20 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
                 (int)L.max_pairs, at<uint32_t>(workspace, L.status),
                 live ? at<int32_t>(workspace, L.shared_rows) : nullptr, p->wait_ns};
     auto mark = [&](int i) { return mark_event(p, i, st); };
+    auto decode = [&](const Fp8GemmArgs& f, bool down) {
+        const auto u8 = [](const void* q) { return static_cast<const uint8_t*>(q); };
+        float* h32 = at<float>(workspace, L.h32);
+        return Fp8DecodeArgs{f, u8(down ? p->wd : p->wg), u8(down ? p->wd : p->wu), u8(down ? p->sd : p->sg),
+                             u8(down ? p->sd : p->su), h32, h32 + (int64_t)R * d.k * d.I};
+    };
     cudaError_t e = marked ? cudaSuccess : mark(0);
     Fp8GemmArgs fg{}, fd{};
     Fp8Maps mg{}, md{};
     if (p->fp8) {
         fp8_args(p, ga, workspace, R, false, &fg, &mg);
-        if (!encode_fp8(&md.a0, at<uint8_t>(workspace, L.h), (uint64_t)d.I, (uint64_t)L.max_pairs, 0) ||
-            !encode_fp8(&md.a1, at<uint8_t>(workspace, L.hs), (uint64_t)d.Is, (uint64_t)d.max_rows, 0))
+        if (!fs && !fd8 &&
+            (!encode_fp8(&md.a0, at<uint8_t>(workspace, L.h), (uint64_t)d.I, (uint64_t)L.max_pairs, 0) ||
+             !encode_fp8(&md.a1, at<uint8_t>(workspace, L.hs), (uint64_t)d.Is, (uint64_t)d.max_rows, 0)))
             return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activation codes");
         const Fp8Regions rx = fp8_regions(p, workspace, R);
         if (e == cudaSuccess)
@@ -312,7 +322,8 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     }
     if (e != cudaSuccess) return cuda_fail(e, "scatter launch");
     if ((e = mark(1)) == cudaSuccess)
-        e = fs ? launch_fp8_stream(kGateUp, mg, fg, p->num_sms, st)
+        e = fd8 ? launch_fp8_decode(kGateUp, decode(fg, false), gu_units, st)
+          : fs ? launch_fp8_stream(kGateUp, mg, fg, p->num_sms, st)
           : p->fp8 ? launch_fp8_gemm(kGateUp, mg, fg, p->num_sms, st)
                    : launch_gemm(kGateUp, su, p->qbits, gu, ga, p->num_sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "gate/up GEMM launch");
@@ -325,7 +336,8 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
             fp8_args(p, gd, workspace, R, true, &fd, &md);
             md.a0 = a0;
             md.a1 = a1;
-            e = fs ? launch_fp8_stream(kDown, md, fd, p->num_sms, st)
+            e = fd8 ? launch_fp8_decode(kDown, decode(fd, true), (groups + 1) * (d.H / kFp8DnCols), st)
+                : fs ? launch_fp8_stream(kDown, md, fd, p->num_sms, st)
                    : launch_fp8_gemm(kDown, md, fd, p->num_sms, st);
         } else {
             e = launch_gemm(kDown, sd, p->qbits, dn, gd, p->num_sms, st);

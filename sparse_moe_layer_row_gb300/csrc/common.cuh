@@ -41,6 +41,7 @@ struct Layout {
     size_t ys;           // fp16 [max_pairs + max_rows, H] staged per-pair and shared outputs
     size_t ysx;          // uint8 [H / 32, max_pairs + max_rows] power-of-two exponent of each
                          // 32-column quarter of a staged row (ys holds value * 2^-exponent)
+    size_t h32;          // fp32: h of calls of up to 8 rows on e4m3 experts, routed pairs then shared rows
     size_t total;
     int64_t max_pairs, max_units_gu, max_units_dn;
 };
@@ -105,6 +106,8 @@ inline Layout make_layout(const moe_dims& d) {
     L.live_base = take(sizeof(int32_t) * (size_t)d.max_blocks);
     L.ys = take(2 * (size_t)(P + R) * (size_t)H);
     L.ysx = take((size_t)(H / 32) * (size_t)(P + R));
+    const size_t few = (size_t)(R < 8 ? R : 8);
+    L.h32 = take(4 * few * (size_t)(d.k * d.I + d.Is));
     L.total = o;
     return L;
 }

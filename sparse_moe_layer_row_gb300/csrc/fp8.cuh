@@ -82,10 +82,13 @@ struct Fp8Maps {
     CUtensorMap s0, s1;   // the shared expert's
     CUtensorMap a0, a1;   // rows: h codes of routed pairs / shared rows; dense: x codes
 };
-// Calls of up to kFp8StreamMaxRows rows take units of up to kFp8StreamRows pairs
-// and the streaming kernels (fp8_stream.cu).
+// Calls with at most kFp8StreamPairs pairs per expert on average take units of up
+// to kFp8StreamRows pairs and the streaming kernels (fp8_stream.cu).  At H = 2048, I =
+// 512, 8 of 256 experts, streaming against the 128-row tiles: 256 rows (8 pairs) 156
+// against 184 us, 384 rows 185 against 188, 512 rows (16 pairs) 220 against 191.
 constexpr int kFp8StreamRows = 32;
-constexpr int kFp8StreamMaxRows = 128;
+constexpr int kFp8StreamPairs = 12;
+inline bool fp8_streams(int64_t rows, int E, int k) { return rows * k <= (int64_t)kFp8StreamPairs * E; }
 cudaError_t fp8_stream_set_attributes();
 cudaError_t launch_fp8_stream(int mode, const Fp8Maps&, const Fp8GemmArgs&, int num_sms, cudaStream_t);
 cudaError_t fp8_gemm_set_attributes();
@@ -104,6 +107,24 @@ struct Fp8RowsArgs {
 };
 bool fp8_rows_applies(int R, int N, int K, int num_sms);
 cudaError_t launch_fp8_rows(const Fp8RowsArgs&, cudaStream_t);
+
+// The expert FFN of up to kFp8DecodeRows rows (fp8_decode.cu), for calls whose gate/up
+// CTAs (kFp8DecodeSub per unit) are resident at once, two per SM: at the sizes above, 1 row
+// (288 CTAs) takes 16.0 us against 20.1 streaming, 2 rows (544) 21.5 against 21.1, 4 rows
+// 32 against 24.
+constexpr int kFp8DecodeRows = 8, kFp8DecodeSub = 8;
+inline bool fp8_decodes(int rows, int gu_units, int num_sms) {
+    return rows <= kFp8DecodeRows && gu_units * kFp8DecodeSub <= 2 * num_sms;
+}
+struct Fp8DecodeArgs {
+    Fp8GemmArgs f;        // units, sizes, pair lists, x codes, scales, staging
+    // weights: gate, up / down, down; the shared expert's
+    const uint8_t *w_a, *w_b, *w_sa, *w_sb;
+    float* h32;           // [pairs, I] h before it is quantised
+    float* sh32;          // [rows, Is]
+};
+// units: a bound on the number in the unit list
+cudaError_t launch_fp8_decode(int mode, const Fp8DecodeArgs&, int units, cudaStream_t);
 
 // Tensor map of e4m3 codes, row-major [d2][d1][d0] (rank 2 if d2 == 0), box of
 // 128 x 128 codes in the 128-byte swizzle, zeros outside (implemented in api.cu).

@@ -120,10 +120,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_fp8_rows(Fp8RowsArgs a) {
     }
 }
 
+// By what the two kernels were measured to take (ns): this one 2300 + CTAs (7 + 0.006 K)
+// with 17 to 32 rows per CTA, the 128 x 256 tiles 4750 + 4 K per round of one tile per
+// SM.  For example (us, this kernel first) 64 x 4096 x 2048: 10.5 and 12.2; 128 x
+// 4096 x 2048: 18.6 and 13.3; 256 x 1024 x 2048: 10.8 and 13.0; 512 x 2048 x 512: 23.7 and
+// 6.8; 77 x 1000 x 1104: 5.5 and 9.1; 32 x 8192 x 8192: 29 and 34; 8 x 8192 x 8192: 11 and 33.
 bool fp8_rows_applies(int R, int N, int K, int num_sms) {
-    (void)K;
+    if (R <= kRowsPerCta) return true;
+    const int64_t ctas = (int64_t)((N + kCols - 1) / kCols) * ((R + kRowsPerCta - 1) / kRowsPerCta);
     const int64_t tiles = (int64_t)((R + 127) / 128) * ((N + 255) / 256);
-    return R <= 32 || tiles * 2 <= num_sms;
+    const int64_t rounds = (tiles + num_sms - 1) / num_sms;
+    return 2300 + ctas * (7000 + 6 * (int64_t)K) / 1000 <= rounds * (4750 + 4 * (int64_t)K);
 }
 
 cudaError_t launch_fp8_rows(const Fp8RowsArgs& a, cudaStream_t st) {

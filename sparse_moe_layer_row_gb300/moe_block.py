@@ -238,7 +238,7 @@ def _need_rows(t: torch.Tensor, name: str, shape=None) -> int:
 def _same_device(*tensors) -> int:
     """The index of the tensors' device (None: not given), which must be one."""
     dev = tensors[0].get_device()
-    for t in tensors:
+    for t in tensors[1:]:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors on different devices: "
                              f"{sorted({str(t.device) for t in tensors if t is not None})}")
@@ -247,8 +247,10 @@ def _same_device(*tensors) -> int:
 
 def _on(device: int, fn, *args):
     """Call the library with ``device`` current."""
-    if torch.cuda.current_device() == device:
-        _check(fn(*args))
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args)
+        if rc:
+            _check(rc)
     else:
         with torch.cuda.device(device):
             _check(fn(*args))

@@ -291,7 +291,7 @@ def pack_bits(kept):
 SHAPES = [dict(), dict(I=64, Is=192), dict(I=320, Is=64, H=512, E=24, k=3), dict(I=192, Is=320, E=40, k=8, block=8)]
 
 
-@pytest.mark.parametrize("R", [1, 2, 31, 32, 33, 130, 300])
+@pytest.mark.parametrize("R", [1, 2, 7, 8, 9, 31, 32, 33, 130, 300])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_experts(shape, R):
     f = Ffn(R, seed=R, **shape)
@@ -309,15 +309,31 @@ def test_experts_full_shape():
     f.check(*f.run())
 
 
-def test_experts_large_outputs():
+@pytest.mark.parametrize("R", [1, 3])
+def test_experts_full_shape_few_rows(R):
+    f = Ffn(R, H=2048, E=256, k=8, I=512, Is=512, seed=R, sigma=0.02, drop=0.0)
+    f.check(*f.run())
+
+
+@pytest.mark.parametrize("R", [1, 6, 40, 300])
+def test_experts_one_expert_takes_all(R):
+    """Every row on the same experts: as many pairs per expert as rows, the others untouched."""
+    f = Ffn(R, E=24, k=2, seed=20 + R, drop=0.0)
+    f.idx[:, 0] = 5
+    f.idx[:, 1] = 23
+    f.check(*f.run())
+
+
+@pytest.mark.parametrize("R", [1, 2, 8, 40, 300])
+def test_experts_large_outputs(R):
     """Outputs beyond fp16's range: the staged exponent."""
-    f = Ffn(40, seed=10, sigma=3.0)
+    f = Ffn(R, seed=10, sigma=3.0)
     y, y32 = f.run()
     assert float(y32.abs().max()) > 65504
     f.check(y, y32)
 
 
-@pytest.mark.parametrize("R", [32, 150])
+@pytest.mark.parametrize("R", [4, 32, 150])
 def test_experts_live_rows(R):
     f = Ffn(R, seed=11)
     full = f.run()
@@ -330,7 +346,7 @@ def test_experts_live_rows(R):
     assert torch.all(y[~live] == 3.0) and torch.all(y32[~live] == 3.0)
 
 
-@pytest.mark.parametrize("R", [32, 200])
+@pytest.mark.parametrize("R", [5, 32, 200])
 def test_experts_repeat_and_row_independence(R):
     """Same call, same bits; a row's output does not depend on the rows beside it."""
     f = Ffn(R, seed=12)
@@ -363,7 +379,7 @@ def test_experts_bad_ids_are_skipped():
     assert torch.all((y32.double() - rr).abs() <= bound + (rr.abs() + bound) * 2.0 ** -24)
 
 
-@pytest.mark.parametrize("R", [32, 300])
+@pytest.mark.parametrize("R", [1, 32, 300])
 def test_pass_equals_the_three_calls(R):
     f = Ffn(R, H=512, E=32, k=4, seed=14)
     L = f.layer
