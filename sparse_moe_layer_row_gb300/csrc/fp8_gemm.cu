@@ -24,7 +24,7 @@
 // Persistent, one CTA per SM, 384 threads (gate/up: 512):
 //   warp 0 lane 0   TMA producer: weight tiles (2 x 16 KB) and, but for
 //                   gate/up, the rows' tile (16 KB) into a ring of 3 stages
-//   warp 1          TMEM allocation; lane 0 issues the MMAs
+//   warp 1          TMEM allocation; issues the MMAs
 //   warps 4..11     promotion and epilogue: lane quadrant warp & 3, columns by
 //                   warpgroup
 //   loaders         gate/up: warps 12..15, gather the unit's rows of x by
@@ -93,6 +93,17 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// One lane of the converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 // Arrive on `bar` once this thread's cp.async copies so far have landed.
@@ -369,38 +380,53 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 const uint32_t par = s < stage ? phase : (phase ^ 1u);
                 if (!mbar_wait_bounded(full + s, par, never, kDrainLimitNs)) give_up();
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer
+            // The whole warp runs the loop, so that its values are uniform, and one
+            // elected lane issues.  This loop is the kernel's pace-maker: with a lone
+            // lane and three waits one after the other it took 1160 clocks per block, of
+            // which the tensor core works 512.
             const uint32_t idesc = idesc_e4m3_f32(128, 256);
+            const bool leader = elect_one();
             int stage = 0, slot = 0, buf = 0;
             uint32_t phase = 0, rphase = 0, bphase = 0;
             bool ok = true;
             for (int u = ufirst; ok && u < nunits; u += nact) {
                 const int4 un = unit(u);
                 if (!valid(un)) {
-                    status_add(a.g.status, MOE_STATUS_BAD_UNIT, 1);
+                    if (lane == 0) status_add(a.g.status, MOE_STATUS_BAD_UNIT, 1);
                     continue;
                 }
                 const int nkb = blocks(un.x);
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_bounded(full + stage, phase, abort_flag, kWaitNs) ||
-                        !mbar_wait_bounded(rfull + slot, rphase, abort_flag, kWaitNs) ||
-                        !mbar_wait_bounded(tempty + buf, bphase ^ 1u, abort_flag, kWaitNs)) {
-                        give_up();
-                        ok = false;
-                        break;
+                    // three tests at once, then the waits for what is not there yet
+                    const bool t0 = mbar_test_wait(full + stage, phase);
+                    const bool t1 = mbar_test_wait(rfull + slot, rphase);
+                    const bool t2 = mbar_test_wait(tempty + buf, bphase ^ 1u);
+                    if (!__all_sync(0xffffffffu, t0 && t1 && t2)) {
+                        const bool got = mbar_wait_bounded(full + stage, phase, abort_flag, kWaitNs) &&
+                                         mbar_wait_bounded(rfull + slot, rphase, abort_flag, kWaitNs) &&
+                                         mbar_wait_bounded(tempty + buf, bphase ^ 1u, abort_flag, kWaitNs);
+                        if (__any_sync(0xffffffffu, !got)) {
+                            if (lane == 0) give_up();
+                            ok = false;
+                            break;
+                        }
                     }
                     if (MODE == kGateUp) fence_proxy_async_smem();   // rows written by cp.async
                     tc_fence_after();
                     const uint32_t sA = sbase + stage * kStageBytes, sW = sA + kTile;
                     const uint32_t d = tmem + (uint32_t)(buf * 256);
-                    // the two weight tiles follow each other: N = 256 rows of 128 bytes
+                    const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sW);
+                    if (leader) {
+                        // the two weight tiles follow each other: N = 256 rows of 128 bytes;
+                        // 32 bytes along K are 2 in the descriptors' address field
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_e4m3(d, smem_desc_sw128(sA + kk * 32), smem_desc_sw128(sW + kk * 32),
-                                    idesc, kk != 0);
-                    tc_commit(empty + stage);
-                    tc_commit(tfull + buf);
+                        for (int kk = 0; kk < 4; ++kk) tc_mma_e4m3(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+                        tc_commit(tfull + buf);
+                        tc_commit(empty + stage);
+                    }
+                    __syncwarp();
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                     if (++slot == kSlots) { slot = 0; rphase ^= 1u; }
                     buf ^= 1;
@@ -408,8 +434,9 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 }
             }
             // drain: arrives once every MMA issued above has completed
-            tc_commit(dbar);
-            if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs)) give_up();
+            if (leader) tc_commit(dbar);
+            __syncwarp();
+            if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs) && lane == 0) give_up();
         } else if (MODE != kGateUp && warp >= 2) {
             loader();
         }
