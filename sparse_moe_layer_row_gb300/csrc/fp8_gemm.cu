@@ -67,14 +67,13 @@ static_assert(kSlots - kStages - 2 > 0 && (kSlots & (kSlots - 1)) == 0, "a slot 
 constexpr int kSxOff = kStgOff + 8 * kStgWarp;            // float [kSlots][128]: row scales
 constexpr int kPwOff = kSxOff + kSlots * 512;         // float [kSlots][128]: pair weights (down)
 constexpr int kSwOff = kPwOff + kSlots * 512;         // float [kSlots][2]: weight block scales
-constexpr int kRowsOff = kSwOff + kSlots * 8;         // int [128]: the loaders' rows of x
-constexpr int kBarOff = kRowsOff + 128 * 4;
+constexpr int kBarOff = kSwOff + kSlots * 8;
 constexpr int kSmem = kBarOff + 256;
 constexpr int kTmemCols = 512;                   // two buffers of 256 columns
 // registers per thread after the split: the pool is what the CTA was launched
 // with (kThreads x kLaunchRegs), checked on the host before any launch
 constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
-constexpr int kLaunchRegsGU = 128, kFewRegsGU = 40, kManyRegsGU = 216;
+constexpr int kLaunchRegsGU = 128, kFewRegsGU = 56, kManyRegsGU = 200;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
 static_assert(256 * kFewRegsGU + 256 * kManyRegsGU <= kThreadsGU * kLaunchRegsGU, "register split");
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -250,7 +249,6 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
         constexpr int kLt = MODE == kGateUp ? 128 : 64;
         const int lt = threadIdx.x - (MODE == kGateUp ? 384 : 64);   // 0 .. kLt - 1
         const int r16 = lt >> 3, ch = lt & 7;
-        int* s_rows = reinterpret_cast<int*>(base + kRowsOff);
         const uint32_t dst0 = sbase + r16 * 128 + ((ch ^ (r16 & 7)) << 4);
         int stage = 0, slot = 0;
         uint32_t phase = 0;
@@ -263,22 +261,17 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
             const int nkb = blocks(g);
             const float *px, *pw0, *pw1;   // scales: of row lt, of the two weight blocks
             int64_t ldx;
+            int row[8];   // gate/up: the rows of x of this thread's chunks, -1: none
             if (MODE == kGateUp) {
-                // the rows are kept in shared memory (the L1 left beside it is too small
-                // for local arrays: 242 -> 1000 us at 8192 rows); a warp copies the rows
-                // that it wrote
-                __syncwarp();
-                int mine = 0;
-                for (int i = r16; i < n; i += 16) {
-                    const int row = !sh ? __ldg(a.g.pair_row + start + i)
-                                  : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + i) : start + i);
-                    s_rows[i] = row >= 0 && row < a.g.R ? row : -1;
-                }
-                if (lt < n)
-                    mine = !sh ? __ldg(a.g.pair_row + start + lt)
-                         : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + lt) : start + lt);
-                __syncwarp();
-                px = a.xs + min(max(mine, 0), a.g.R - 1);
+                auto row_of = [&](int i) {
+                    if (i >= n) return -1;
+                    const int r = !sh ? __ldg(a.g.pair_row + start + i)
+                                : (a.g.shared_rows ? __ldg(a.g.shared_rows + start + i) : start + i);
+                    return r < a.g.R ? r : -1;
+                };
+#pragma unroll
+                for (int j = 0; j < 8; ++j) row[j] = row_of(16 * j + r16);
+                px = a.xs + max(row_of(lt), 0);
                 ldx = a.g.R;
                 const int mb = fp8_blocks(sh ? a.g.Is : a.g.I);
                 const int64_t o = ((int64_t)(sh ? 0 : g) * mb + m) * nkb;
@@ -314,11 +307,9 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                 if (MODE == kGateUp) {
                     const uint32_t dst = dst0 + stage * kStageBytes;
                     const uint8_t* col = a.xq + kb * kFp8Block + ch * 16;
-#pragma unroll 4
-                    for (int i = r16; i < n; i += 16) {
-                        const int row = s_rows[i];
-                        if (row >= 0) cp_async16(dst + (i - r16) * 128, col + (int64_t)row * a.g.H);
-                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (row[j] >= 0) cp_async16(dst + j * 2048, col + (int64_t)row[j] * a.g.H);
                 }
                 cp_async_arrive(rfull + slot);
                 if (++stage == kStages) { stage = 0; phase ^= 1u; }
