@@ -386,3 +386,38 @@ def quantize_experts(T: "Tensors", bits: int) -> QuantExperts:
         one(w) for w in (T.w_gate, T.w_up, T.w_down, T.ws_gate, T.ws_up, T.ws_down)]
     return QuantExperts(bits, interleave_gate_up(gq, uq, -2), dq, interleave_gate_up(gd, ud, -1), dd,
                         interleave_gate_up(sgq, suq, -2), sdq, interleave_gate_up(sgd, sud, -1), sdd)
+
+
+# --------------------------------------------------------------------------- e4m3 experts
+#
+# Synthetic e4m3 weights with one fp32 scale per 128 x 128 block
+# (moe_fp8_weights) from the synthetic bf16 layer, by rounding to nearest.
+
+FP8_BLOCK = 128
+
+
+def quantize_blocks_e4m3(w: torch.Tensor):
+    """Weights [..., N, K] -> (e4m3 codes of the same shape, fp32 scales
+    [..., ceil(N / 128), ceil(K / 128)]): scale = max|w| / 448 per block (at least
+    2^-100 / 448), code = w / scale rounded to nearest."""
+    *lead, N, K = w.shape
+    nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
+    p = torch.nn.functional.pad(w.float(), (0, kb * FP8_BLOCK - K, 0, nb * FP8_BLOCK - N))
+    p = p.view(*lead, nb, FP8_BLOCK, kb, FP8_BLOCK)
+    s = p.abs().amax(dim=(-3, -1)).clamp_min(2.0 ** -100) / 448.0
+    q = (p / s[..., :, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    q = q.view(*lead, nb * FP8_BLOCK, kb * FP8_BLOCK)[..., :N, :K]
+    return q.contiguous(), s.contiguous()
+
+
+def fp8_experts(T: Tensors, chunk: int = 32):
+    """The e4m3 weights of a bf16 layer's experts, for Plan.fp8 / MoeBlockLayer.fp8
+    (``chunk`` experts are converted at a time)."""
+    from .moe_block import Fp8Experts
+
+    def many(w):
+        parts = [quantize_blocks_e4m3(w[i:i + chunk]) for i in range(0, w.shape[0], chunk)]
+        return torch.cat([q for q, _ in parts]), torch.cat([s for _, s in parts])
+    (g, gs), (u, us), (d, ds) = many(T.w_gate), many(T.w_up), many(T.w_down)
+    (sg, sgs), (su, sus), (sd, sds) = (quantize_blocks_e4m3(w) for w in (T.ws_gate, T.ws_up, T.ws_down))
+    return Fp8Experts(g, u, d, gs, us, ds, sg, su, sd, sgs, sus, sds)

@@ -157,6 +157,27 @@ def test_binding_refuses_cpu_and_misfit_tensors():
         mb.moe_fp8_quantize([1.0], z, z)
 
 
+def test_synthetic_e4m3_experts():
+    """quantize_blocks_e4m3: shapes, the scale of each block, values within half a code's
+    step of the weights (2^-4 of the value, or of the least normal code)."""
+    from sparse_moe_layer_row_gb300 import workloads as W
+    w = torch.randn(3, 200, 300)
+    w[1, :128, :128] = 0.0
+    q, s = W.quantize_blocks_e4m3(w)
+    assert q.shape == w.shape and s.shape == (3, 2, 3) and q.dtype == torch.float8_e4m3fn
+    assert s[1, 0, 0] == torch.tensor(2.0 ** -100) / 448.0
+    assert s[0, 1, 2] == w[0, 128:, 256:].abs().max() / 448.0
+    v = F.weight_values(q, s)
+    step = s.repeat_interleave(128, -2)[..., :200, :].repeat_interleave(128, -1)[..., :300].double() * 2.0 ** -6
+    assert torch.all((v - w.double()).abs() <= 2.0 ** -4 * torch.maximum(w.abs().double(), step) * (1 + 1e-6))
+    T = W.make_tensors(W.TINY)
+    e = W.fp8_experts(T, chunk=5)
+    assert e.gate.shape == (16, 128, 256) and e.gate_scale.shape == (16, 1, 2)
+    assert e.down.shape == (16, 256, 128) and e.shared_down_scale.shape == (2, 1)
+    one, os_ = W.quantize_blocks_e4m3(T.w_up[7])
+    assert torch.equal(e.up[7].view(torch.uint8), one.view(torch.uint8)) and torch.equal(e.up_scale[7], os_)
+
+
 # ---- the references that the GPU tests compare with
 
 def test_reference_rounding_matches_the_type():

@@ -438,3 +438,18 @@ def test_wait_limit_aborts_and_recovers(R):
     after = f.run()
     assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
     assert not any(f.layer.status().values())
+
+
+@pytest.mark.parametrize("args", [["--tiny"], ["--tiny", "--rows", "1"], ["--rows", "40"]], ids=str)
+def test_example(args):
+    """The example layer: its e4m3 experts stay near the bf16 ones.  A rounding to e4m3 is off
+    by up to 2^-4 of a value, its mean square by (2^-4)^2 / 3; x, h and the three weights are
+    rounded, so that independent errors add up to sqrt(5 / 3) 2^-4 = 0.08 of the norm at most."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "scored_fp8_layer.py")
+    spec = importlib.util.spec_from_file_location("scored_fp8_layer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    assert 0 < ex.main(args + ["--passes", "2"]) < 0.08
