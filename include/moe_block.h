@@ -399,8 +399,11 @@ moe_status moe_route_scored(const moe_route_rule* rule, const void* logits, moe_
                             const float* select_bias, int32_t* topk_idx, float* topk_w,
                             float* topk_score, moe_stream_t stream);
 
-/* The router's logits alone: those of moe_block_route (fixed order, the bias
- * added), for moe_route_scored.
+/* The router's logits alone, the bias added, for moe_route_scored: fp32 sums of
+ * exact products.  Up to 255 rows (and for shapes that the tensor-core router does
+ * not take: E > 256, E % 16, k > 16 or H > 8192) in the fixed order of
+ * moe_block_route, bit for bit its logits; from 256 rows on as the tensor cores
+ * sum them.
  *   logits  [R, E] fp32 out; other arguments and errors: moe_block_route. */
 moe_status moe_block_logits(const moe_plan* plan, const void* x, int32_t R,
                             const int32_t* block_offsets, int32_t nb, const float* logit_bias,

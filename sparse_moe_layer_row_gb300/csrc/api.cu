@@ -609,8 +609,21 @@ moe_status moe_block_logits(const moe_plan* p, const void* x, int32_t R,
     if (R == 0) return ok();
     const Layout L = make_layout(p->d);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(at<uint8_t>(workspace, L.route_cnt), 0,
-                                    sizeof(uint32_t) * (size_t)R, st);
+    cudaError_t e;
+    if (p->tc_route && R >= kTcRouteMinRows) {
+        CUtensorMap tm_x;
+        if (!encode_bf16(&tm_x, x, p->d.H, (uint64_t)R, 0, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+            return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for x");
+        RouteTcArgs ta{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(p->wr),
+                       logit_bias, block_offsets, R, p->d.H, p->d.E, p->d.k, nb,
+                       at<float>(workspace, L.wnorm), at<float>(workspace, L.logits), nullptr, nullptr,
+                       at<uint32_t>(workspace, L.status), p->wait_ns,
+                       route_tc_parts(R, p->d.E, p->d.H, logit_rows(p->d.max_rows), p->num_sms)};
+        e = launch_logits_tc(ta, tm_x, p->tm_wr, logits, p->num_sms, st);
+        if (e != cudaSuccess) return cuda_fail(e, "logits launch");
+        return ok();
+    }
+    e = cudaMemsetAsync(at<uint8_t>(workspace, L.route_cnt), 0, sizeof(uint32_t) * (size_t)R, st);
     if (e != cudaSuccess) return cuda_fail(e, "route counters");
     RouteArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(p->wr),
                 logit_bias, block_offsets, R, p->d.H, p->d.E, p->d.k, nb, logits,

@@ -139,6 +139,9 @@ cudaError_t launch_route(const RouteArgs&, int num_sms, cudaStream_t);
 cudaError_t route_tc_set_attributes();
 cudaError_t launch_route_tc(const RouteTcArgs&, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
                             int num_sms, cudaStream_t);
+// The screen's logits as an output (bias added) instead of a top-k.
+cudaError_t launch_logits_tc(const RouteTcArgs&, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                             float* out, int num_sms, cudaStream_t);
 int route_tc_parts(int R, int E, int H, int64_t cap_rows, int num_sms);
 cudaError_t launch_coreset(const CoresetArgs&, cudaStream_t);
 cudaError_t launch_scatter(const ScatterArgs&, bool small, int num_sms, cudaStream_t);

@@ -523,6 +523,36 @@ __global__ void __launch_bounds__(256, 2) k_route_exact(RouteTcArgs a) {
     }
 }
 
+// moe_block_logits for large batches: the screen's logits themselves, their K parts added
+// in part order, with the bias; one warp per row.  8192 rows x 256 experts: 19.5 us with
+// the screen, against some 600 in the fixed order of the SIMT router.
+__global__ void __launch_bounds__(256) k_logits_sum(RouteTcArgs a, float* out) {
+    pdl_wait();  // see common.cuh: nothing global is touched before
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int nwarps = (gridDim.x * blockDim.x) >> 5;
+    for (int r = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; r < a.R; r += nwarps) {
+        const float* brow = a.bias ? a.bias + (size_t)find_block(a.off, a.nb, r) * a.E : nullptr;
+        uint32_t nonfinite = 0;
+        for (int e = lane * 4; e < a.E; e += 128) {   // E % 16 == 0
+            float4 z = __ldcg(reinterpret_cast<const float4*>(a.logits + (size_t)r * a.E + e));
+            for (int p = 1; p < a.nk; ++p) {
+                const float4 q = __ldcg(reinterpret_cast<const float4*>(a.logits + ((size_t)p * a.R + r) * a.E + e));
+                z.x += q.x; z.y += q.y; z.z += q.z; z.w += q.w;
+            }
+            const float v[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = finish_logit(v[i], brow, e + i);
+                if (!isfinite(f)) ++nonfinite;
+                out[(size_t)r * a.E + e + i] = f;
+            }
+        }
+        nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
+        if (lane == 0) status_add(a.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
+    }
+}
+
 cudaError_t route_tc_set_attributes() {
     cudaError_t e = cudaFuncSetAttribute(k_route_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          TcCfg::kSmem);
@@ -544,15 +574,27 @@ int route_tc_parts(int R, int E, int H, int64_t cap_rows, int num_sms) {
     return nk;
 }
 
-cudaError_t launch_route_tc(const RouteTcArgs& a, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
-                            int num_sms, cudaStream_t st) {
-    cudaError_t e = launch_kernel(k_route_norms, dim3((unsigned)((a.E + 7) / 8)), dim3(256), 0, st, a);
+static cudaError_t launch_screen(const RouteTcArgs& a, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                                 int num_sms, cudaStream_t st) {
     const int ntiles = (a.R + 127) / 128;
     const int nsplit = (a.E > 128 && a.E % 32 == 0) ? 2 : 1;
     const int nunits = ntiles * a.nk * nsplit;
     const int grid = nunits < num_sms ? nunits : num_sms;
-    if (e == cudaSuccess)
-        e = launch_kernel(k_route_tc, dim3(grid), dim3(192), TcCfg::kSmem, st, tm_x, tm_w, a, nsplit);
+    return launch_kernel(k_route_tc, dim3(grid), dim3(192), TcCfg::kSmem, st, tm_x, tm_w, a, nsplit);
+}
+
+cudaError_t launch_logits_tc(const RouteTcArgs& a, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                             float* out, int num_sms, cudaStream_t st) {
+    cudaError_t e = launch_screen(a, tm_x, tm_w, num_sms, st);
+    long blocks = ((long)a.R + 7) / 8;
+    if (blocks > (long)num_sms * 8) blocks = (long)num_sms * 8;
+    return e == cudaSuccess ? launch_kernel(k_logits_sum, dim3((unsigned)blocks), dim3(256), 0, st, a, out) : e;
+}
+
+cudaError_t launch_route_tc(const RouteTcArgs& a, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                            int num_sms, cudaStream_t st) {
+    cudaError_t e = launch_kernel(k_route_norms, dim3((unsigned)((a.E + 7) / 8)), dim3(256), 0, st, a);
+    if (e == cudaSuccess) e = launch_screen(a, tm_x, tm_w, num_sms, st);
     const long ntiles_ex = (a.R + kExRows - 1) / kExRows;
     const long eb = ntiles_ex < (long)num_sms * 2 ? ntiles_ex : (long)num_sms * 2;
     if (e == cudaSuccess)

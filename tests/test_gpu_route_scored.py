@@ -184,13 +184,40 @@ def test_graph_capture():
     assert np.array_equal(idx.cpu().numpy(), ref[0]) and np.array_equal(w.cpu().double().numpy(), ref[1])
 
 
-@pytest.mark.parametrize("w", [W.TINY, W.BLOCKS16_ZIPF], ids=lambda w: w.name)
-def test_layer_route_scored(w):
-    """A plan's logits order as moe_block_route does (fixed order, biased), and routing by
-    the softmax rule over the chosen gives its weights."""
+def layer_of(w):
     T = W.make_tensors(w, device="cuda")
-    layer = mb.MoeBlockLayer(T.w_router, T.w_gate, T.w_up, T.w_down, T.ws_gate, T.ws_up, T.ws_down,
-                             k=w.k, max_rows=w.R, max_blocks=w.nb)
+    return T, mb.MoeBlockLayer(T.w_router, T.w_gate, T.w_up, T.w_down, T.ws_gate, T.ws_up, T.ws_down,
+                               k=w.k, max_rows=w.R, max_blocks=w.nb)
+
+
+@pytest.mark.parametrize("w", [W.TINY, W.BLOCKS16_ZIPF, W.BY_NAME["rows2048-b32-tau0.9"]], ids=lambda w: w.name)
+def test_block_logits(w):
+    """The logits against 64 bits.  H products, exact in fp32, are added in fp32: each addition
+    a whole step 2^-23 of the sum of magnitudes at most (a tensor core may truncate), and the
+    bias half a step."""
+    T, layer = layer_of(w)
+    z = torch.full((w.R, w.E), float("nan"), device="cuda")
+    mb.moe_block_logits(layer.plan, T.x, T.block_offsets, T.bias, z, layer.workspace)
+    torch.cuda.synchronize()
+    x, wr = T.x.double(), T.w_router.double()
+    ref, mag = x @ wr.t(), x.abs() @ wr.abs().t()
+    if T.bias is not None:
+        block = torch.searchsorted(T.block_offsets, torch.arange(w.R, device="cuda"), right=True) - 1
+        ref = ref + T.bias.double()[block]
+    assert torch.all((z.double() - ref).abs() <= w.H * F.STEP * mag + ref.abs() * 2.0 ** -24)
+    assert layer.status()["nonfinite_logits"] == 0
+    T.x[3, 7] = float("nan")
+    mb.moe_block_logits(layer.plan, T.x, T.block_offsets, T.bias, z, layer.workspace)
+    torch.cuda.synchronize()
+    assert torch.isnan(z[3]).all() and torch.isfinite(z[:3]).all() and torch.isfinite(z[4:]).all()
+    assert layer.status()["nonfinite_logits"] == w.E
+
+
+@pytest.mark.parametrize("w", [W.TINY, W.BLOCK32], ids=lambda w: w.name)
+def test_layer_route_scored(w):
+    """A plan's logits of up to 255 rows order as moe_block_route does (fixed order), and
+    routing by the softmax rule over the chosen gives its weights."""
+    T, layer = layer_of(w)
     idx0, w0 = (t.clone() for t in layer.route(T.x, T.block_offsets, T.bias))
     idx, wt, sc = layer.route_scored(T.x, T.block_offsets, mb.RouteRule(), bias=T.bias)
     torch.cuda.synchronize()
