@@ -13,6 +13,9 @@
 //            multiplies: the four lanes of a pair hold its block of 128.  The same
 //            formula on the same h as the other paths.  Weights and unit list do
 //            not depend on the gate/up kernel: they are loaded before the wait for it.
+//
+// One row of the 2048 x 512 layer with 8 of 256 experts takes 15.7 us with its front and
+// combine, four dependent launches of some 4 us each; its 25.8 MB would take 3.9.
 #include "fp8.cuh"
 
 namespace moe {

@@ -1,12 +1,13 @@
 // moe_fp8_quantize: rows -> e4m3 codes and one fp32 scale per block of 128
 // along the row (the value rule is in fp8.cuh).
 //
-// Reads each input once and writes each code and scale once; bound by HBM.  A
-// warp takes two blocks of 128 of a row, one per half-warp: eight values per lane, the
+// Reads each input once and writes each code and scale once.  8192 x 2048 bf16 takes
+// 12.2 us (4.2 TB/s; 7.6 us at the measured copy rate): the issue slots (0.67 per
+// clock) bound it beside HBM.  A warp takes two blocks of 128 of a row, one per half-warp: eight values per lane, the
 // largest magnitude by four xor steps, eight codes per lane as one 8-byte store.
 // Four such tasks are loaded before the first is used, and the arithmetic is kept
 // small (16-bit maxima of the raw words, packed fp32, no index division): at 207
-// instructions per task the issue slots bound it, 17 us for 8192 x 2048.
+// instructions per task the same rows took 17.3 us.
 #include "fp8.cuh"
 #include "scatter_dev.cuh"
 

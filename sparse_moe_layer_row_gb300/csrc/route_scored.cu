@@ -13,6 +13,10 @@
 //     takes this GPU 62 clocks), and what is closer still with 64-bit scores.
 //     With bounds near 1e-6 and neighbouring keys some 1e-2 apart the first
 //     happens to about one row in a thousand.
+//
+// 8192 rows of 256 experts in 8 groups take 13.9 us: the issue slots bound them (0.59
+// per clock), and the rows that 32 bits leave open end last.  Taking the k best one
+// by one, with 64-bit scores for every unsure row, took 42.
 #include <cfloat>
 
 #include "route_common.cuh"
