@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_fp8_rows(Fp8RowsArgs a) {
 // 6.8; 77 x 1000 x 1104: 5.5 and 9.1; 32 x 8192 x 8192: 29 and 34; 8 x 8192 x 8192: 11 and 33.
 bool fp8_rows_applies(int R, int N, int K, int num_sms) {
     if (R <= kRowsPerCta) return true;
+    if (R > 65535 * kRowsPerCta) return false;   // the grid's y: row tiles
     const int64_t ctas = (int64_t)((N + kCols - 1) / kCols) * ((R + kRowsPerCta - 1) / kRowsPerCta);
     const int64_t tiles = (int64_t)((R + 127) / 128) * ((N + 255) / 256);
     const int64_t rounds = (tiles + num_sms - 1) / num_sms;

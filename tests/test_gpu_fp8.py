@@ -155,6 +155,13 @@ def test_gemm_row_counts(R):
     assert_gemm(gemm(*ops, dtype=torch.float32), ref, bound)
 
 
+def test_gemm_few_outputs_of_very_many_rows():
+    """More row tiles than a grid has in y, with too few outputs to fill a tile."""
+    ops = operands(65535 * 32 + 5, 16, 16, seed=8)
+    ref, bound = F.gemm(*ops)
+    assert_gemm(gemm(*ops, dtype=torch.float32), ref, bound)
+
+
 @pytest.mark.parametrize("R", [1, 5, 50, 200])
 def test_gemm_large_codes_and_unlike_scales(R):
     """Codes over the whole range and scales orders of magnitude apart."""
