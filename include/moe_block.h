@@ -414,7 +414,9 @@ moe_status moe_block_logits(const moe_plan* plan, const void* x, int32_t R,
  * counterpart on the pages, whose 8-bit files are integer codes).
  * A block of values v with a = max(|v|, 2^-100) has the scale s = a / 448,
  * rounded once to fp32, and the codes e4m3(448 v / a), halves to even; a code q
- * stands for q * s.  A block with a NaN has a NaN scale; one with an infinity an
+ * stands for q * s.  448 v / a is formed in fp32 as (7/8 v) / (a / 512): for 16-bit
+ * values that changes no code; an fp32 value within 2^-23 of the middle between two
+ * codes, relative to it, may count as the middle.  A block with a NaN has a NaN scale; one with an infinity an
  * infinite scale: what is computed from either is NaN. */
 
 /* Rows to codes, a scale for each row and block of 128 along it.

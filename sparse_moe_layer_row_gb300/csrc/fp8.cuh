@@ -8,6 +8,9 @@
 // 448 v / a is formed as (7/8 v) / (a / 512): both operands are exact (7/8 v
 // for inputs of up to 21 significant bits, a / 512 always) and neither
 // overflows, so a quotient that is exactly between two codes is seen as such.
+// For 16-bit values the fp32 quotient changes no code: |448 v - m a| for a middle m is 0
+// or at least 2^-16 of m a (11, 11 and 5 significant bits).  fp32 values (and h) have
+// their two roundings, 2^-23 of the quotient.
 // Every |v| <= a, so no code exceeds 448.  The floor 2^-100 keeps a / 512 and s
 // normal numbers; a block of zeros has codes 0 and the scale 2^-100 / 448.
 // Infinities and NaN: the largest magnitude is taken over the bits of |v|, in

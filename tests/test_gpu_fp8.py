@@ -54,6 +54,16 @@ def test_quantize(R, K, dtype):
         assert torch.equal(q.double(), rq)
 
 
+def test_quantize_fp32_quotient_rule():
+    """fp32 values: the codes of (7/8 v) / (a / 512), each operation rounded to fp32, also
+    where that is a middle of two codes that 448 v / a only comes close to."""
+    x = randn(4096, 2048, seed=11)
+    q, _ = quantize(x)
+    p = x.view(4096, 16, 128)
+    v = p * 0.875 / (p.abs().amax(-1, keepdim=True) * 2.0 ** -9)
+    assert torch.equal(q.view(torch.uint8), v.to(E4M3).view(4096, 2048).view(torch.uint8))
+
+
 def test_quantize_ties_zeros_tiny_and_huge():
     """Values exactly between two codes go to the even one; blocks of zeros, subnormals and
     the largest finite values stay finite."""
