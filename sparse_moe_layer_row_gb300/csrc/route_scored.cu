@@ -457,7 +457,9 @@ __device__ __forceinline__ bool route_row(const RouteScoredArgs& a, int row, int
             t2 = max(max(t2, u2), min(t1, u1));
             t1 = max(t1, u1);
         }
-        if (top2 && t2 > kMaskKey) t1 = order_key(key_value(t1) + key_value(t2));
+        // a sum beyond fp32 stays in its range: no infinity, which is the masked groups' value
+        if (top2 && t2 > kMaskKey)
+            t1 = order_key(fmaxf(fminf(key_value(t1) + key_value(t2), FLT_MAX), -FLT_MAX));
         int rank = 0;
         for (int h = 0; h < G; ++h) {
             const uint32_t x = __shfl_sync(kAll, t1, h * L);
@@ -472,6 +474,7 @@ __device__ __forceinline__ bool route_row(const RouteScoredArgs& a, int row, int
             // a sum of two keys: twice the error, and its own rounding
             const float gt = 2.0f * tol + 4e-7f * (fabsf(x) + fabsf(y));
             if (y > -INFINITY && !(x - y > gt)) {
+                if (!(gt < INFINITY)) return true;   // 32 bits say nothing about keys this large
                 // lane h: group h's score
                 const float mine = key_value(__shfl_sync(kAll, t1, min(lane, G - 1) * L));
                 uint32_t m = 0;
