@@ -382,6 +382,9 @@ typedef struct moe_route_rule {
  * close for 32 bits are compared in 64.  Weight j is s of the j-th expert,
  * divided by the row's sum of k scores with `renormalize`, times `scale`.
  * Without a bias, scores order as logits do, and the logits are compared.
+ * A score below fp32's least number still has its share in a renormalised row (a
+ * row of logits of -100 and -101 has the weights 0.73 and 0.27); one below e^-700 of
+ * 1 (sigmoid) or of the row's largest (softmax) counts as 0.
  *   A logit of -inf masks its expert: score 0, and it is taken only when the
  * chosen groups have fewer than k others.  A NaN logit is treated the same and
  * comes after the masked ones.  A row that is masked throughout gets the

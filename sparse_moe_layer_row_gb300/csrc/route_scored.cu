@@ -217,21 +217,52 @@ __device__ __forceinline__ bool near_groups(const RouteScoredArgs& a, const T* z
     return true;
 }
 
+// Renormalised weights of a row that takes scores near or below fp32's least: numerators
+// e^(z - m) over the largest chosen logit m, and for the sigmoid s e^-p = e^(z - p) / (1 + e^z)
+// with p = min(m, 0), both at most 1.  The low part of z - p counts too (e^l = 1 + l), as the
+// difference may be near 100.  Scores below e^-700 are 0 as they are in 64 bits (`off`: masked).
+__device__ __noinline__ float ratio_weight(bool sig, float z, bool off, float zmax) {
+    off |= z < (sig ? -700.0f : zmax - 700.0f);
+    const float m = warp_max(off ? -INFINITY : z), p = sig ? fminf(m, 0.0f) : m;
+    float t = 0.0f;
+    if (!off) {
+        if (sig && z > 0.0f) {
+            t = __fdiv_rn(1.0f, 1.0f + expf(-z));
+        } else {
+            t = 1.0f;
+            if (z != p) {
+                const Two d = two_sum(z, -p);
+                t = expf(d.h);
+                t = __fmaf_rn(t, d.l, t);
+            }
+            if (sig) t = __fdiv_rn(t, 1.0f + expf(z));
+        }
+    }
+    const float sum = warp_sum(t);
+    return sum > 0.0f ? __fdiv_rn(t, sum) : 0.0f;
+}
+
 // The weights of the chosen experts (lane j: the j-th, my_id), from their unbiased scores.
 template <typename T>
 __device__ __forceinline__ void write_row(const RouteScoredArgs& a, const T* zr, int row, int lane,
                                           int my_id, float zmax, float inv) {
+    const bool sig = a.rule.score == MOE_SCORE_SIGMOID;
+    const float zj = lane < a.k ? ld_logit(zr + my_id) : -INFINITY;
+    const bool off = zj == -INFINITY || zj != zj;
     float s = 0.0f;
-    if (lane < a.k) {
-        const float zj = ld_logit(zr + my_id);
-        if (zj == -INFINITY || zj != zj) s = 0.0f;
-        else if (a.rule.score == MOE_SCORE_SIGMOID) s = __fdiv_rn(1.0f, 1.0f + expf(-zj));
-        else s = zj == zmax ? inv : expf(zj - zmax) * inv;
+    if (!off) {
+        if (!sig) s = zj == zmax ? inv : expf(zj - zmax) * inv;
+        else if (zj < -87.0f) s = expf(zj);   // 1 + e^z is 1, and e^-z may be infinite
+        else s = __fdiv_rn(1.0f, 1.0f + expf(-zj));
     }
     float w = s;
     if (a.rule.renormalize) {
-        const float sum = warp_sum(s);
-        w = sum > 0.0f ? __fdiv_rn(s, sum) : 0.0f;
+        if (__any_sync(kAll, !off && s < 0x1p-100f)) {
+            w = ratio_weight(sig, zj, off, zmax);
+        } else {
+            const float sum = warp_sum(s);
+            w = sum > 0.0f ? __fdiv_rn(s, sum) : 0.0f;
+        }
     }
     if (lane < a.k) {
         const int64_t o = (int64_t)row * a.k + lane;
