@@ -100,6 +100,9 @@ class RouteRule:
             int(self.renormalize), self.scale))
         object.__setattr__(self, "_ref", ctypes.byref(self._c))
 
+    def __reduce__(self):   # a reference cannot be copied: a copy makes its own
+        return type(self), tuple(getattr(self, f.name) for f in dataclasses.fields(self))
+
 
 _lib = None
 
