@@ -630,7 +630,7 @@ k_fp8_gemm(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUt
                     }
                     uint8_t* out = static_cast<uint8_t*>(a.y) + ((int64_t)(start + q * 32) * a.ldy + n0) * es;
                     const int64_t ldb = a.ldy * es;
-                    const int cb = min(256, (a.N - n0) * es);   // bytes of each row
+                    const int cb = min(256 / es, a.N - n0) * es;   // bytes of each row
                     if (a.y_vec && cb % 16 == 0) {
                         copy_rows(stg, out, ldb, cb, n - q * 32, lane);
                     } else {   // rows at any element: a row at a time, consecutive elements per lane
