@@ -151,6 +151,9 @@ k_fp8_stream(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ C
                 const int nkb = blocks(g), nfill = nkb * ((un.w + kPass - 1) / kPass);
                 for (int i = 0; i < nfill; ++i) {
                     const int kb = i % nkb;
+                    // the ring is full: its consumers start when the gate/up kernel has
+                    // ended, and only from then on does the wait's limit count
+                    if (MODE == kDown && nfills == kStages) pdl_wait();
                     if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitNs)) {
                         give_up();
                         ok = false;
