@@ -406,7 +406,9 @@ moe_status moe_route_scored(const moe_route_rule* rule, const void* logits, moe_
  * exact products.  Up to 255 rows (and for shapes that the tensor-core router does
  * not take: E > 256, E % 16, k > 16 or H > 8192) in the fixed order of
  * moe_block_route, bit for bit its logits; from 256 rows on as the tensor cores
- * sum them.
+ * sum them, in parts of H whose number depends on R: a row's logits may differ in
+ * their last bits from call size to call size, and with them the order of nearly
+ * equal experts.
  *   logits  [R, E] fp32 out; other arguments and errors: moe_block_route. */
 moe_status moe_block_logits(const moe_plan* plan, const void* x, int32_t R,
                             const int32_t* block_offsets, int32_t nb, const float* logit_bias,
@@ -419,8 +421,8 @@ moe_status moe_block_logits(const moe_plan* plan, const void* x, int32_t R,
  * rounded once to fp32, and the codes e4m3(448 v / a), halves to even; a code q
  * stands for q * s.  448 v / a is formed in fp32 as (7/8 v) / (a / 512): for 16-bit
  * values that changes no code; an fp32 value within 2^-23 of the middle between two
- * codes, relative to it, may count as the middle.  A block with a NaN has a NaN scale; one with an infinity an
- * infinite scale: what is computed from either is NaN. */
+ * codes, relative to it, may count as the middle.  A block with a NaN has a NaN scale;
+ * one with an infinity an infinite scale: what is computed from either is NaN. */
 
 /* Rows to codes, a scale for each row and block of 128 along it.
  *   x       [R, K] of `dtype`, rows row_stride elements apart (>= K), aligned to
@@ -436,7 +438,8 @@ size_t moe_fp8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K);
 
 /* y = x W^T on codes.
  *   y[r, n] = sum over blocks b of xs[b, r] * ws[n / 128, b] * sum_{k in b} xq[r, k] wq[n, k]
- * Products of codes are exact; sums are fp32; y is rounded once.
+ * Products of codes are exact; the product of the two scales is formed first, in
+ * fp32; sums are fp32; y is rounded once.
  *   xq  [R, K] codes, xs [ceil(K / 128), R] scales (as moe_fp8_quantize writes them)
  *   wq  [N, K] codes, ws [ceil(N / 128), ceil(K / 128)] scales, one per 128 x 128 block
  *   y   [R, N] of `dtype` out, rows row_stride elements apart (>= N)
@@ -464,7 +467,8 @@ typedef struct moe_fp8_weights {
  * [E, H] as for moe_plan_create.  Every call works on such a plan as on a bf16
  * one, with the same routing; the expert FFN of a row x is
  *   x quantised per block of 128;  g, u = products as in moe_fp8_gemm;
- *   h = silu(g) * u in fp32, quantised per block of 128;  the down product,
+ *   h = silu(g) * u in fp32, quantised per block of 128, its codes e4m3(h * (448 / a))
+ *   with both operations rounded to fp32;  the down product,
  * and the outputs are weighted, staged and summed as in moe_block_forward.
  * Errors as moe_plan_create. */
 moe_status moe_plan_create_fp8(const moe_dims* dims, const void* w_router,

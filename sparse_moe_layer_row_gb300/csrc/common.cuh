@@ -134,8 +134,14 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // kernel before it on the stream is still running.  The rule that keeps this
 // safe: a thread calls pdl_wait() -- which returns once the preceding kernel
 // has completed and its writes are visible -- before it reads or writes any
-// global memory that another kernel writes or reads; the only thing done
-// before it is reading the weights (read-only for every kernel).  pdl_trigger()
+// global memory that another kernel writes or reads.  Done before it are only
+// reads of the weights (read-only for every kernel) and, in the down GEMMs'
+// producers and k_fp8_decode_dn, of the unit list and its length (with the counter
+// of bad units bumped).  The list was written two or more kernels back, by the
+// scatter; it may be read early because the kernel between, the gate/up GEMM,
+// does not write it and triggers only after its own wait, by when the scatter has
+// completed.  A gate/up kernel's trigger must therefore stay behind its wait, and
+// no kernel that writes the list may come between.  pdl_trigger()
 // lets the next kernel be scheduled; it is called right after the wait, so at
 // most two kernels of a stream overlap.  The down GEMM on CTA pairs
 // (k_down_pair, bf16 calls over kStreamDownRows rows) does not call it: the

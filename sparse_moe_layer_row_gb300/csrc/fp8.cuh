@@ -87,8 +87,12 @@ struct Fp8Maps {
 };
 // Calls with at most kFp8StreamPairs pairs per expert on average take units of up
 // to kFp8StreamRows pairs and the streaming kernels (fp8_stream.cu).  At H = 2048, I =
-// 512, 8 of 256 experts, streaming against the 128-row tiles: 256 rows (8 pairs) 156
-// against 184 us, 384 rows 185 against 188, 512 rows (16 pairs) 220 against 191.
+// 512, 8 of 256 experts, streaming against the 128-row tiles: 256 rows (8 pairs) 158
+// against 181 us, 384 rows 187 against 183, 512 rows (16 pairs) 221 against 185.
+// The average knows neither the shared expert's rows (1 of 256 experts: 1024 rows 175
+// against 182, 2048 rows 221 against 200, 3072 rows 273 against 210; 2 of 256: 1536 rows 219
+// against 199) nor how many experts a coreset leaves (8 of 256, all pairs on 32 of
+// them: 128 rows 87 against 47, 384 rows 161 against 58): there the tiles would be faster.
 constexpr int kFp8StreamRows = 32;
 constexpr int kFp8StreamPairs = 12;
 inline bool fp8_streams(int64_t rows, int E, int k) { return rows * k <= (int64_t)kFp8StreamPairs * E; }

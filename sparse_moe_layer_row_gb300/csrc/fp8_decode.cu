@@ -68,7 +68,7 @@ __device__ __forceinline__ void block_mma(float (&acc)[4], const Tile& t, const 
 
 __global__ void __launch_bounds__(32 * kWarps) k_fp8_decode_gu(Fp8DecodeArgs a) {
     pdl_wait();  // see common.cuh: nothing global is touched before
-    pdl_trigger();
+    pdl_trigger();   // not earlier: the down kernel reads the unit list before its wait
     __shared__ float part[kWarps][2][kRowsN][17];
     const int u = blockIdx.x / kSub, sub = blockIdx.x % kSub;
     const GemmArgs& ga = a.f.g;

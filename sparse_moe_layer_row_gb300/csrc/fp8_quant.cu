@@ -2,9 +2,12 @@
 // along the row (the value rule is in fp8.cuh).
 //
 // Reads each input once and writes each code and scale once.  8192 x 2048 bf16 takes
-// 12.2 us (4.2 TB/s; 7.6 us at the measured copy rate): the issue slots (0.67 per
-// clock) bound it beside HBM.  A warp takes two blocks of 128 of a row, one per half-warp: eight values per lane, the
-// largest magnitude by four xor steps, eight codes per lane as one 8-byte store.
+// 12.2 us (4.2 TB/s; 7.6 us at the measured copy rate).  No unit is at its limit (0.67
+// issues per clock, 41% of the warps, 26% of HBM): each warp waits for its loads, and
+// 65,536 tasks over 9728 warps are 6.7 each, taken four at a time, so that the second
+// round is partly empty.  A warp takes two blocks of 128 of a row, one per half-warp:
+// eight values per lane, the largest magnitude by four xor steps, eight codes per lane
+// as one 8-byte store.
 // Four such tasks are loaded before the first is used, and the arithmetic is kept
 // small (16-bit maxima of the raw words, packed fp32, no index division): at 207
 // instructions per task the same rows took 17.3 us.

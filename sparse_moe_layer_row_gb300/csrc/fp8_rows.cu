@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_fp8_rows(Fp8RowsArgs a) {
 // SM.  For example (us, this kernel first) 64 x 4096 x 2048: 10.5 and 12.2; 128 x
 // 4096 x 2048: 18.6 and 13.3; 256 x 1024 x 2048: 10.8 and 13.0; 512 x 2048 x 512: 23.7 and
 // 6.8; 77 x 1000 x 1104: 5.5 and 9.1; 32 x 8192 x 8192: 29 and 34; 8 x 8192 x 8192: 11 and 33.
+// Up to 32 rows the rows alone decide, which is right for up to 8 rows (8 x 151,936 x
+// 2048: 54 and 60; x 7168: 168 and 206) and, with 9 to 32, up to some 8192 outputs (16 x
+// 8192 x 2048: 7.8 and 10.5; 32 x 8192 x 2048: 11.1 and 10.6).  Beyond them the tiles
+// would be faster: 16 x 32,768 x 2048: 24 and 16; 32 x 32,768 x 2048: 35 and 16; 32 x
+// 151,936 x 2048: 166 and 64; 32 x 16,384 x 7168: 60 and 32.
 bool fp8_rows_applies(int R, int N, int K, int num_sms) {
     if (R <= kRowsPerCta) return true;
     if (R > 65535 * kRowsPerCta) return false;   // the grid's y: row tiles

@@ -116,6 +116,7 @@ k_fp8_stream(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ C
     __syncthreads();
     // see common.cuh; the down producer reads only weights and the unit list,
     // which the scatter wrote: complete before the gate/up kernel let this one start
+    // (its trigger stays behind its wait)
     if (!(MODE == kDown && warp == 8)) {
         pdl_wait();
         pdl_trigger();

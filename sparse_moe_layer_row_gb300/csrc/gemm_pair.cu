@@ -275,7 +275,7 @@ k_gateup_pair(const __grid_constant__ CUtensorMap tmWg, const __grid_constant__ 
         prefetch_tmap(&tmWg); prefetch_tmap(&tmWu); prefetch_tmap(&tmSg); prefetch_tmap(&tmSu);
     }
     pdl_wait();   // see common.cuh
-    pdl_trigger();
+    pdl_trigger();   // not earlier: the down GEMM reads the unit list before its wait
     const int nunits = __ldg(a.n_units);
     const int nc = active_workers(nunits, (int)cluster_count());   // balanced rounds
     const int c0 = (int)cluster_id() < nc ? (int)cluster_id() : nunits;

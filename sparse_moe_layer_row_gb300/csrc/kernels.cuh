@@ -147,8 +147,8 @@ cudaError_t launch_coreset(const CoresetArgs&, cudaStream_t);
 cudaError_t launch_scatter(const ScatterArgs&, bool small, int num_sms, cudaStream_t);
 // The large-batch scatter after its first kernel.
 cudaError_t launch_scatter_rest(const ScatterArgs&, cudaStream_t);
-// after_pair_down: the down GEMM before it ran on CTA pairs (k_down_pair)
-cudaError_t launch_combine(const CombineArgs&, int num_sms, bool after_pair_down, cudaStream_t);
+// four_ctas: four CTAs per SM instead of one (the rule is beside the kernel)
+cudaError_t launch_combine(const CombineArgs&, int num_sms, bool four_ctas, cudaStream_t);
 cudaError_t gemm_set_attributes();
 cudaError_t launch_gemm(int mode, bool small, int qbits, const GemmMaps&, const GemmArgs&,
                         int grid, cudaStream_t);

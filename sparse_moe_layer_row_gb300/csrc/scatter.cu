@@ -291,11 +291,13 @@ __device__ __forceinline__ void combine_rows(const CombineArgs& a) {
     }
 }
 
-// kMinCtas CTAs per SM: after the CTA-pair down GEMM four, registers capped at 64, 32 warps per SM to keep
-// more loads in flight (8192 rows: 69.6 -> 62.7 us); that down GEMM lets the
-// combine launch only when it ends (common.cuh).  Otherwise one: launched
-// early, four CTAs per SM waiting beside the streaming down GEMM slowed the
-// step.
+// kMinCtas CTAs per SM: four for calls of more than kStreamDownRows rows, registers capped at 64,
+// 32 warps per SM to keep more loads in flight (8192 rows: 69.6 -> 62.7 us after the
+// CTA-pair down GEMM, which lets the combine launch only when it ends, see
+// common.cuh).  The e4m3 down GEMMs let it launch early; with them four took 439.9
+// against one's 447.7 us for the whole forward of 8192 rows, and the same within 1% at
+// 513, 1024 and 2048 rows.  Otherwise one: launched early, four CTAs per SM waiting
+// beside the bf16 streaming down GEMM slowed the step.
 template <int kMinCtas>
 __global__ void __launch_bounds__(256, kMinCtas) k_combine(CombineArgs a) {
     pdl_wait();  // see common.cuh: nothing global is touched before
@@ -318,11 +320,11 @@ cudaError_t launch_scatter_rest(const ScatterArgs& a, cudaStream_t st) {
     return e;
 }
 
-cudaError_t launch_combine(const CombineArgs& a, int num_sms, bool after_pair_down, cudaStream_t st) {
+cudaError_t launch_combine(const CombineArgs& a, int num_sms, bool four_ctas, cudaStream_t st) {
     long blocks = ((long)a.R * (a.H / 256) + 7) / 8;
     if (blocks > (long)num_sms * 16) blocks = (long)num_sms * 16;
     if (blocks < 1) blocks = 1;
-    if (after_pair_down)
+    if (four_ctas)
         return launch_kernel(k_combine<4>, dim3((unsigned)blocks), dim3(256), 0, st, a);
     return launch_kernel(k_combine<1>, dim3((unsigned)blocks), dim3(256), 0, st, a);
 }
