@@ -449,6 +449,73 @@ moe_status moe_fp8_gemm(const void* xq, const float* xs, int32_t R, const void* 
                         int64_t row_stride, void* workspace, size_t workspace_bytes,
                         moe_stream_t stream);
 
+/* ---- 8-bit integers with one fp32 scale per row (no counterpart on the pages, whose
+ * 8-bit files have a scale per 32 weights).
+ * A row of values v with a = max(|v|, 2^-100) has the scale s = a / 127, rounded once
+ * to fp32, and the codes rint(127 v / a), halves to even; a code q stands for q * s.
+ * 127 v / a is formed in fp32 as (127/128 v) / (a / 128): for 16-bit values that
+ * changes no code; an fp32 value within 2^-23 of the middle between two codes, relative
+ * to it, may count as the middle.  A row with a NaN has a NaN scale, one with an infinity
+ * an infinite scale, and either has codes 0: what is computed from them is NaN. */
+
+/* Rows to codes, a scale for each row.  (The same call makes weights' codes: a row is
+ * then an output channel.)
+ *   x       [R, K] of `dtype`, rows row_stride elements apart (>= K), aligned to
+ *           its element; any K >= 1
+ *   codes   [R, K] int8 out
+ *   scales  [R] fp32 out */
+moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, int32_t R,
+                           int32_t K, int8_t* codes, float* scales, moe_stream_t stream);
+
+/* Bytes of device workspace (256-byte aligned; it begins with the status
+ * counters, as in moe_workspace_bytes) of a moe_i8_gemm; 0 on bad sizes. */
+size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K);
+
+/* y = x W^T on int8 codes, x with a scale for each row (token), W for each output channel.
+ *   y[r, n] = (xs[r] * ws[n]) * sum_k xq[r, k] wq[n, k]
+ * The sum is that of integers, held in 32 bits: exact while its partial sums stay
+ * below 2^24, rounded as fp32 sums are beyond; the product of the two scales is
+ * formed first, in fp32; y is rounded once.
+ *   xq  [R, K] codes, xs [R] scales (as moe_i8_quantize writes them)
+ *   wq  [N, K] codes, ws [N] scales
+ *   y   [R, N] of `dtype` out, rows row_stride elements apart (>= N)
+ * K a multiple of 16 below 2^17, xq and wq 16-byte aligned; R >= 0, N >= 1. */
+moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_t* wq,
+                       const float* ws, int32_t N, int32_t K, void* y, moe_dtype dtype,
+                       int64_t row_stride, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream);
+
+/* ---- Residual addition and root-mean-square norm of rows (no counterpart on the pages:
+ * what a model computes between its MoE layers), with the values or their 8-bit codes out.
+ *   r = x + residual, rounded to the residual's type (without a residual: r = x)
+ *   p = r * weight in fp32;  rstd = 1 / sqrt(sum r^2 / H + eps) in fp32
+ * and the normed values p * rstd, as
+ *   y       rounded to the type of x, and / or
+ *   codes   MOE_CODES_E4M3: e4m3, as moe_fp8_quantize's of p (codes do not depend on
+ *           rstd), the scales a * rstd / 448 for each row and block of 128: the
+ *           operands of moe_fp8_gemm;
+ *           MOE_CODES_I8: int8, as moe_i8_quantize's of p, the scale a * rstd / 127
+ *           for each row: the operands of moe_i8_gemm.
+ * Sums are fp32; a row whose sum of squares exceeds fp32 is scaled first.  A row with
+ * a NaN or an infinity has NaN values, or scales, at least there.
+ *   x         [R, H] of `dtype`, rows x_stride elements apart (>= H); any H >= 1
+ *   residual  [R, H] of `residual_dtype` (that of x, or fp32), or NULL
+ *   total     [R, H] of `residual_dtype` out: r, or NULL; needs a residual; may be the
+ *             residual or, of its type, x itself (same pointer and stride), in place
+ *   weight    [H] of `weight_dtype` (that of x, or fp32), or NULL: ones
+ *   eps       2^-100 .. 2^100
+ *   y         [R, H] of `dtype` out, or NULL; without a total in its place it may be x
+ *   codes     [R, H] out, scales [ceil(H / 128), R] (e4m3) or [R] (int8) out, fp32;
+ *             both NULL with MOE_CODES_NONE
+ * At least one of y and codes.  Pointers are aligned to their element. */
+enum { MOE_CODES_NONE = 0, MOE_CODES_E4M3 = 1, MOE_CODES_I8 = 2 };
+moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int32_t R,
+                           int32_t H, const void* residual, moe_dtype residual_dtype,
+                           int64_t residual_stride, void* total, int64_t total_stride,
+                           const void* weight, moe_dtype weight_dtype, float eps, void* y,
+                           int64_t y_stride, int32_t code_type, void* codes, float* scales,
+                           moe_stream_t stream);
+
 /* Expert weights as codes with one fp32 scale per 128 x 128 block (the last
  * block of either dimension may be short).  Device pointers, codes 16-byte
  * aligned:

@@ -41,6 +41,34 @@ __device__ __forceinline__ uint32_t fp8_pair(float v0, float v1) {
     return r;
 }
 
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+// Two values at a time (each half as the scalar operation).
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// n / d by Markstein's method (IBM J. Res. Dev. 34, 1990): with r the correctly rounded
+// reciprocal of d, q0 = n r and q0 + (n - q0 d) r is the correctly rounded quotient
+// (where that is no subnormal; here those have the code 0).
+__device__ __forceinline__ float2 quotient2(float2 n, float d, float r) {
+    const float2 q0 = mul2(n, r);
+    return fma2(fma2(q0, -d, n), r, q0);
+}
+
 __host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
 
 struct Fp8QuantArgs {

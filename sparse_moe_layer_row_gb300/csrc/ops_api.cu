@@ -1,5 +1,6 @@
-// Host side of the calls that need no plan: moe_route_scored, moe_fp8_quantize
-// and moe_fp8_gemm.  Arguments are checked here, before anything is launched.
+// Host side of the calls that need no plan: moe_route_scored, the e4m3 and int8
+// quantising and products, and moe_add_rmsnorm.  Arguments are checked here, before
+// anything is launched.
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -7,6 +8,7 @@
 
 #include "fp8.cuh"
 #include "route_scored.cuh"
+#include "rows8.cuh"
 
 using namespace moe;
 
@@ -180,6 +182,114 @@ moe_status moe_fp8_gemm(const void* xq, const float* xs, int32_t R, const void* 
     a.y_vec = aligned(y, 16) && row_stride * (int64_t)es % 16 == 0;
     return launched(launch_fp8_gemm(kDense, m, a, sms, reinterpret_cast<cudaStream_t>(stream)),
                     "gemm launch");
+}
+
+moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, int32_t R,
+                           int32_t K, int8_t* codes, float* scales, moe_stream_t stream) {
+    moe_status s = check_dtype(dtype);
+    if (s != MOE_OK) return s;
+    if (R < 0 || R > kMaxRows) return fail(MOE_ERR_INVALID_ARG, "R=%d outside [0, 2^30]", R);
+    if (K < 1 || K > kMaxRows) return fail(MOE_ERR_INVALID_ARG, "K=%d outside [1, 2^30]", K);
+    if (row_stride < K) return fail(MOE_ERR_INVALID_ARG, "row_stride=%lld is below K=%d", (long long)row_stride, K);
+    if (R == 0) return set_error(MOE_OK, "");
+    if (!x || !aligned(x, dtype_size(dtype))) return fail(MOE_ERR_INVALID_ARG, "x NULL or misaligned");
+    if (!codes || !scales || !aligned(scales, 4))
+        return fail(MOE_ERR_INVALID_ARG, "codes/scales NULL or misaligned");
+    int sms = 0;
+    if ((s = device_ready(false, &sms)) != MOE_OK) return s;
+    RmsNormArgs a{};
+    a.x = x;
+    a.ldx = row_stride;
+    a.R = R;
+    a.H = K;
+    a.codes = reinterpret_cast<uint8_t*>(codes);
+    a.scales = scales;
+    return launched(launch_rows8(kQuantI8, a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)),
+                    "quantise launch");
+}
+
+size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K) {
+    if (R < 0 || R > kMaxRows || N < 1 || N > kMaxRows || K < 16 || K % 16 || K > kI8MaxK) {
+        fail(MOE_ERR_INVALID_ARG, "R=%d, N=%d, K=%d: R >= 0, N >= 1, K a positive multiple of 16 below 2^17", R, N, K);
+        return 0;
+    }
+    return kGemmWorkspace;
+}
+
+moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_t* wq,
+                       const float* ws, int32_t N, int32_t K, void* y, moe_dtype dtype,
+                       int64_t row_stride, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream) {
+    moe_status s = check_dtype(dtype);
+    if (s != MOE_OK) return s;
+    const size_t need = moe_i8_gemm_workspace_bytes(R, N, K);
+    if (!need) return K >= 16 && (K % 16 || K > kI8MaxK) ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+    if (row_stride < N) return fail(MOE_ERR_INVALID_ARG, "row_stride=%lld is below N=%d", (long long)row_stride, N);
+    if (R == 0) return set_error(MOE_OK, "");
+    if (!xq || !wq || !aligned(xq, 16) || !aligned(wq, 16))
+        return fail(MOE_ERR_INVALID_ARG, "xq/wq NULL or not 16-byte aligned");
+    if (!xs || !ws || !aligned(xs, 4) || !aligned(ws, 4))
+        return fail(MOE_ERR_INVALID_ARG, "xs/ws NULL or misaligned");
+    if (!y || !aligned(y, dtype_size(dtype))) return fail(MOE_ERR_INVALID_ARG, "y NULL or misaligned");
+    if (!workspace || !aligned(workspace, 256))
+        return fail(MOE_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype};
+    return launched(launch_i8_rows(a, reinterpret_cast<cudaStream_t>(stream)), "gemm launch");
+}
+
+moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int32_t R,
+                           int32_t H, const void* residual, moe_dtype residual_dtype,
+                           int64_t residual_stride, void* total, int64_t total_stride,
+                           const void* weight, moe_dtype weight_dtype, float eps, void* y,
+                           int64_t y_stride, int32_t code_type, void* codes, float* scales,
+                           moe_stream_t stream) {
+    moe_status s = check_dtype(dtype);
+    if (s != MOE_OK) return s;
+    if (R < 0 || R > kMaxRows) return fail(MOE_ERR_INVALID_ARG, "R=%d outside [0, 2^30]", R);
+    if (H < 1 || H > kMaxRows) return fail(MOE_ERR_INVALID_ARG, "H=%d outside [1, 2^30]", H);
+    if (residual && residual_dtype != dtype && residual_dtype != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "residual_dtype=%d: that of x, or fp32", residual_dtype);
+    if (weight && weight_dtype != dtype && weight_dtype != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "weight_dtype=%d: that of x, or fp32", weight_dtype);
+    if (code_type != MOE_CODES_NONE && code_type != MOE_CODES_E4M3 && code_type != MOE_CODES_I8)
+        return fail(MOE_ERR_UNSUPPORTED, "code_type=%d: none, e4m3 or int8", code_type);
+    if (!(eps >= 0x1p-100f && eps <= 0x1p100f))
+        return fail(MOE_ERR_INVALID_ARG, "eps=%g outside [2^-100, 2^100]", (double)eps);
+    if (x_stride < H) return fail(MOE_ERR_INVALID_ARG, "x_stride=%lld is below H=%d", (long long)x_stride, H);
+    if (residual && residual_stride < H)
+        return fail(MOE_ERR_INVALID_ARG, "residual_stride=%lld is below H=%d", (long long)residual_stride, H);
+    if (total && total_stride < H)
+        return fail(MOE_ERR_INVALID_ARG, "total_stride=%lld is below H=%d", (long long)total_stride, H);
+    if (y && y_stride < H) return fail(MOE_ERR_INVALID_ARG, "y_stride=%lld is below H=%d", (long long)y_stride, H);
+    if (total && !residual) return fail(MOE_ERR_INVALID_ARG, "total without a residual");
+    if ((code_type == MOE_CODES_NONE) != !codes || !codes != !scales)
+        return fail(MOE_ERR_INVALID_ARG, "codes and scales go with a code_type, and it with them");
+    if (R == 0) return set_error(MOE_OK, "");
+    if (!y && !codes) return fail(MOE_ERR_INVALID_ARG, "neither y nor codes");
+    const size_t es = dtype_size(dtype), rs = dtype_size(residual_dtype);
+    if (!x || !aligned(x, es)) return fail(MOE_ERR_INVALID_ARG, "x NULL or misaligned");
+    if ((residual && !aligned(residual, rs)) || (total && !aligned(total, rs)))
+        return fail(MOE_ERR_INVALID_ARG, "residual or total misaligned");
+    if (weight && !aligned(weight, dtype_size(weight_dtype))) return fail(MOE_ERR_INVALID_ARG, "weight misaligned");
+    if ((y && !aligned(y, es)) || (scales && !aligned(scales, 4)))
+        return fail(MOE_ERR_INVALID_ARG, "y or scales misaligned");
+    if (total && total == y) return fail(MOE_ERR_INVALID_ARG, "total and y are the same");
+    if (total == residual && total && R > 1 && total_stride != residual_stride)
+        return fail(MOE_ERR_INVALID_ARG, "total in the residual's place with another stride");
+    if (total == x && total && (residual_dtype != dtype || (R > 1 && total_stride != x_stride)))
+        return fail(MOE_ERR_INVALID_ARG, "total in x's place with another type or stride");
+    if (y == x && y && R > 1 && y_stride != x_stride)
+        return fail(MOE_ERR_INVALID_ARG, "y in x's place with another stride");
+    int sms = 0;
+    if ((s = device_ready(false, &sms)) != MOE_OK) return s;
+    const bool f32 = dtype == MOE_F32;
+    RmsNormArgs a{x, x_stride, residual, residual_stride, total, total_stride, weight,
+                  !f32 && residual && residual_dtype == MOE_F32, !f32 && weight && weight_dtype == MOE_F32, R, H, eps,
+                  y, y_stride, static_cast<uint8_t*>(codes), scales};
+    const int what = code_type == MOE_CODES_E4M3 ? kNormE4m3 : code_type == MOE_CODES_I8 ? kNormI8 : kNormOnly;
+    return launched(launch_rows8(what, a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)), "rmsnorm launch");
 }
 
 }  // extern "C"

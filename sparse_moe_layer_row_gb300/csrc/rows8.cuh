@@ -1,0 +1,44 @@
+// Argument blocks and launchers of rows8.cu (norm of rows, int8 codes of rows)
+// and i8_gemm.cu (the product on int8 codes).
+#pragma once
+
+#include "fp8.cuh"
+
+namespace moe {
+
+struct RmsNormArgs {
+    const void* x;            // [R] rows of H values, ldx elements apart
+    int64_t ldx;
+    const void* residual;     // likewise, or NULL
+    int64_t ldr;
+    void* total;              // x + residual in the residual's type, or NULL
+    int64_t ldt;
+    const void* w;            // [H], or NULL: ones
+    int res_f32, w_f32;       // residual and total, w: fp32 instead of the type of x
+    int R, H;
+    float eps;
+    void* y;                  // the type of x, or NULL
+    int64_t ldy;
+    uint8_t* codes;           // [R, H], or NULL
+    float* scales;            // e4m3: [ceil(H / 128), R]; int8: [R]
+};
+// What a call makes of its rows.
+enum { kNormOnly = 0, kNormE4m3 = 1, kNormI8 = 2, kQuantI8 = 3 };
+cudaError_t launch_rows8(int what, const RmsNormArgs&, int dtype, int num_sms, cudaStream_t);
+
+struct I8GemmArgs {
+    const int8_t* xq;         // [R, K]
+    const float* xs;          // [R]
+    const int8_t* wq;         // [N, K]
+    const float* ws;          // [N]
+    int R, N, K;
+    void* y;                  // [R] rows of N, ldy elements apart
+    int64_t ldy;
+    int ydtype;
+};
+cudaError_t launch_i8_rows(const I8GemmArgs&, cudaStream_t);
+
+// An int32 sum of K products of codes stays in range (128 * 128 * K < 2^31).
+constexpr int kI8MaxK = (1 << 17) - 16;
+
+}  // namespace moe

@@ -172,6 +172,15 @@ def load(build_if_missing: bool = False):
     L.moe_fp8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
     L.moe_fp8_gemm.restype = ctypes.c_int
     L.moe_fp8_gemm.argtypes = [P, P, i32, P, P, i32, i32, P, ctypes.c_int, i64, P, sz, P]
+    L.moe_i8_quantize.restype = ctypes.c_int
+    L.moe_i8_quantize.argtypes = [P, ctypes.c_int, i64, i32, i32, P, P, P]
+    L.moe_i8_gemm_workspace_bytes.restype = sz
+    L.moe_i8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
+    L.moe_i8_gemm.restype = ctypes.c_int
+    L.moe_i8_gemm.argtypes = [P, P, i32, P, P, i32, i32, P, ctypes.c_int, i64, P, sz, P]
+    L.moe_add_rmsnorm.restype = ctypes.c_int
+    L.moe_add_rmsnorm.argtypes = [P, ctypes.c_int, i64, i32, i32, P, ctypes.c_int, i64, P, i64, P,
+                                  ctypes.c_int, ctypes.c_float, P, i64, i32, P, P, P]
     L.moe_plan_set_forward_events.restype = ctypes.c_int
     L.moe_plan_set_forward_events.argtypes = [P, P, i32]
     L.moe_plan_set_wait_limit.restype = ctypes.c_int
@@ -614,6 +623,95 @@ def moe_fp8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
     dev = _same_device(xq, xs, wq, ws, y, workspace)
     _on(dev, load().moe_fp8_gemm, _ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
         _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(), _stream(stream, dev))
+
+
+def moe_i8_quantize(x, codes, scales, stream=None):
+    """Rows x [R, K] (bf16, fp16 or fp32; rows may be strided) to int8 ``codes`` [R, K] and
+    fp32 ``scales`` [R], one per row (for weights [N, K]: one per output channel)."""
+    ld = _need_rows(x, "x")
+    R, K = x.shape
+    _need(codes, "codes", torch.int8, (R, K))
+    _need(scales, "scales", torch.float32, (R,))
+    dev = _same_device(x, codes, scales)
+    _on(dev, load().moe_i8_quantize, _ptr(x), _DTYPES[x.dtype], ld, R, K, _ptr(codes),
+        _ptr(scales), _stream(stream, dev))
+
+
+def moe_i8_gemm_workspace_bytes(R: int, N: int, K: int) -> int:
+    """Workspace bytes of moe_i8_gemm; raises for sizes it does not take."""
+    n = int(load().moe_i8_gemm_workspace_bytes(R, N, K))
+    if n == 0:
+        raise MoeError(-1, load().moe_last_error().decode())
+    return n
+
+
+def moe_i8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
+    """y [R, N] = x W^T on int8 codes: xq [R, K] with a scale per row xs [R] (as
+    moe_i8_quantize writes them), wq [N, K] with a scale per output ws [N].
+    y: bf16, fp16 or fp32, rows may be strided."""
+    ld = _need_rows(y, "y")
+    R, N = y.shape
+    _need(xq, "xq", torch.int8)
+    if xq.dim() != 2 or xq.shape[0] != R:
+        raise ValueError(f"xq must have shape ({R}, K), got {tuple(xq.shape)}")
+    K = xq.shape[1]
+    _need(xs, "xs", torch.float32, (R,))
+    _need(wq, "wq", torch.int8, (N, K))
+    _need(ws, "ws", torch.float32, (N,))
+    _need(workspace, "workspace", torch.uint8)
+    dev = _same_device(xq, xs, wq, ws, y, workspace)
+    _on(dev, load().moe_i8_gemm, _ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
+        _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(), _stream(stream, dev))
+
+
+def _of_type(t, name, dtype):
+    if t.dtype != dtype and t.dtype != torch.float32:
+        raise ValueError(f"{name} must be {dtype} (the type of x) or torch.float32, got {t.dtype}")
+
+
+def moe_add_rmsnorm(x, weight, eps, residual=None, total=None, y=None, codes=None, scales=None,
+                    stream=None):
+    """Root-mean-square norm of rows x [R, H] (+ ``residual``), times ``weight`` [H] (None: ones).
+
+    ``residual`` (the type of x, or fp32) is added first; ``total`` receives the sum in that
+    type and may be ``residual`` itself.  Outputs, at least one: ``y`` [R, H] in the type of
+    x; ``codes`` [R, H] with ``scales``: float8_e4m3fn with [ceil(H / 128), R] (the operands
+    of moe_fp8_gemm) or int8 with [R] (those of moe_i8_gemm).  Rows of x, residual, total and
+    y may be strided."""
+    ldx = _need_rows(x, "x")
+    shape = x.shape
+    R, H = shape
+    dt = x.dtype
+    ldr = ldt = ldy = 0
+    rt = wt = dt
+    if residual is not None:
+        ldr = _need_rows(residual, "residual", shape)
+        rt = residual.dtype
+        _of_type(residual, "residual", dt)
+    if total is not None:
+        if residual is None:
+            raise ValueError("total needs a residual")
+        ldt = _need_rows(total, "total", shape)
+        if total.dtype != rt:
+            raise ValueError(f"total must be {rt}, got {total.dtype}")
+    if weight is not None:
+        wt = weight.dtype if isinstance(weight, torch.Tensor) else None
+        _need(weight, "weight", dt if wt == dt else torch.float32, (H,))
+    if y is not None:
+        ldy = _need_rows(y, "y", shape)
+        if y.dtype != dt:
+            raise ValueError(f"y must be {dt}, got {y.dtype}")
+    kind = 0
+    if codes is not None:
+        kind = 2 if codes.dtype == torch.int8 else 1
+        _need(codes, "codes", torch.int8 if kind == 2 else torch.float8_e4m3fn, shape)
+        _need(scales, "scales", torch.float32, (R,) if kind == 2 else (-(-H // 128), R))
+    elif scales is not None:
+        raise ValueError("scales go with codes")
+    dev = _same_device(x, weight, residual, total, y, codes, scales)
+    _on(dev, load().moe_add_rmsnorm, _ptr(x), _DTYPES[dt], ldx, R, H, _ptr(residual), _DTYPES[rt],
+        ldr, _ptr(total), ldt, _ptr(weight), _DTYPES[wt], eps, _ptr(y), ldy, kind, _ptr(codes),
+        _ptr(scales), _stream(stream, dev))
 
 
 def moe_read_device_status(workspace: torch.Tensor, stream=None) -> dict:
