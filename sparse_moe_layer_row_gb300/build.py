@@ -18,9 +18,10 @@ LIB = os.path.join(OUT_DIR, "libmoeblock.so")
 SOURCES = ["api.cu", "router.cu", "router_tc.cu", "coreset.cu", "scatter.cu",
            "gemm.cu", "gemm_pair.cu", "noalloc.cu", "ops_api.cu", "route_scored.cu",
            "fp8_quant.cu", "fp8_gemm.cu", "fp8_stream.cu",
-           "fp8_rows.cu", "fp8_decode.cu", "rows8.cu", "i8_gemm.cu"]
+           "fp8_rows.cu", "fp8_decode.cu", "rows8.cu", "i8_gemm.cu",
+           "token.cu"]
 HEADERS = ["common.cuh", "kernels.cuh", "route_common.cuh", "coreset_dev.cuh", "scatter_dev.cuh",
-           "route_scored.cuh", "fp8.cuh", "rows8.cuh"]
+           "route_scored.cuh", "fp8.cuh", "rows8.cuh", "token.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]

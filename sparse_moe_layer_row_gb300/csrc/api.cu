@@ -11,6 +11,7 @@
 
 #include "fp8.cuh"
 #include "kernels.cuh"
+#include "token.cuh"
 
 using namespace moe;
 
@@ -355,6 +356,53 @@ moe_status enqueue_forward(const moe_plan* p, const void* x, int32_t R,
     return ok();
 }
 
+// The one launch of moe_token_pass and moe_token_forward after validation.
+moe_status enqueue_token(const moe_plan* p, const void* x, int32_t R, bool given, const float* logit_bias,
+                         int32_t* topk_idx, float* topk_w, void* y, float* y_f32, void* workspace,
+                         cudaStream_t st) {
+    const moe_dims& d = p->d;
+    const Layout L = make_layout(d);
+    TokenArgs a{};
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.R = R; a.H = d.H; a.E = d.E; a.k = d.k; a.I = d.I; a.Is = d.Is;
+    a.given = given;
+    a.wr = static_cast<const __nv_bfloat16*>(p->wr);
+    a.bias = logit_bias;
+    a.wg = p->wg; a.wu = p->wu; a.wd = p->wd;
+    a.sg = p->sg; a.su = p->su; a.sd = p->sd;
+    a.cg = p->f8.gate_scale; a.cu = p->f8.up_scale; a.cd = p->f8.down_scale;
+    a.csg = p->f8.shared_gate_scale; a.csu = p->f8.shared_up_scale; a.csd = p->f8.shared_down_scale;
+    a.logits = at<float>(workspace, L.logits);
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.h = at<void>(workspace, L.h32);
+    a.flags = at<uint32_t>(workspace, L.flags);
+    a.status = at<uint32_t>(workspace, L.status);
+    a.y = static_cast<__nv_bfloat16*>(y);
+    a.y_f32 = y_f32;
+    a.wait_ns = p->wait_ns;
+    cudaError_t e = launch_token(p->fp8, a, p->num_sms, st);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "token launch");
+}
+
+// What both calls check.
+moe_status check_token(const moe_plan* p, const void* x, int32_t R, const void* topk_idx, const void* topk_w,
+                       const void* y, const void* y_f32, void* ws, size_t ws_bytes) {
+    static const int32_t none = 0;
+    moe_status s = check_call(p, R, &none, 1, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    if (p->qbits) return fail(MOE_ERR_UNSUPPORTED, "a plan of 8- or 4-bit integer experts: bf16 or e4m3");
+    if (R > kTokenRows) return fail(MOE_ERR_UNSUPPORTED, "R=%d: at most %d rows", R, kTokenRows);
+    if (p->d.H > kTokenMaxH) return fail(MOE_ERR_UNSUPPORTED, "H=%d: at most %d", p->d.H, kTokenMaxH);
+    if (R == 0) return MOE_OK;
+    if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x is NULL or not 16-byte aligned");
+    if (!y || !aligned(y, 16)) return fail(MOE_ERR_INVALID_ARG, "y is NULL or not 16-byte aligned");
+    if (y_f32 && !aligned(y_f32, 16)) return fail(MOE_ERR_INVALID_ARG, "y_f32 not 16-byte aligned");
+    if (!topk_idx || !topk_w || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return fail(MOE_ERR_INVALID_ARG, "topk_idx/topk_w NULL or misaligned");
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -389,6 +437,7 @@ moe_status moe_plan_create(const moe_dims* dims, const void* w_router, const voi
     if (e == cudaSuccess) e = gateup_pair_set_attributes(p->num_sms);
     if (e == cudaSuccess) e = down_pair_set_attributes(p->num_sms);
     if (e == cudaSuccess) e = route_tc_set_attributes();
+    if (e == cudaSuccess) e = token_set_attributes();
     if (e != cudaSuccess) {
         delete p;
         return cuda_fail(e, "device query");
@@ -517,6 +566,7 @@ moe_status moe_plan_create_fp8(const moe_dims* dims, const void* w_router,
     if (e == cudaSuccess) e = fp8_gemm_set_attributes();
     if (e == cudaSuccess) e = fp8_stream_set_attributes();
     if (e == cudaSuccess) e = route_tc_set_attributes();
+    if (e == cudaSuccess) e = token_set_attributes();
     if (e != cudaSuccess) {
         delete p;
         return cuda_fail(e, "device query");
@@ -734,6 +784,27 @@ moe_status moe_block_pass(const moe_plan* p, const void* x, int32_t R, const int
     if (s != MOE_OK) return s;
     return enqueue_forward(p, x, R, block_offsets, nb, topk_idx, w_renorm, keep, nullptr, y, y_f32,
                            workspace, st, true);
+}
+
+moe_status moe_token_pass(const moe_plan* p, const void* x, int32_t R, const float* logit_bias,
+                          int32_t* topk_idx, float* topk_w, void* y, float* y_f32, void* workspace,
+                          size_t workspace_bytes, moe_stream_t stream) {
+    moe_status s = check_token(p, x, R, topk_idx, topk_w, y, y_f32, workspace, workspace_bytes);
+    if (s != MOE_OK) return s;
+    if (logit_bias && !aligned(logit_bias, 4)) return fail(MOE_ERR_INVALID_ARG, "logit_bias misaligned");
+    if (R == 0) return ok();
+    return enqueue_token(p, x, R, false, logit_bias, topk_idx, topk_w, y, y_f32, workspace,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_token_forward(const moe_plan* p, const void* x, int32_t R, const int32_t* topk_idx,
+                             const float* topk_w, void* y, float* y_f32, void* workspace,
+                             size_t workspace_bytes, moe_stream_t stream) {
+    moe_status s = check_token(p, x, R, topk_idx, topk_w, y, y_f32, workspace, workspace_bytes);
+    if (s != MOE_OK) return s;
+    if (R == 0) return ok();
+    return enqueue_token(p, x, R, true, nullptr, const_cast<int32_t*>(topk_idx), const_cast<float*>(topk_w),
+                         y, y_f32, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_plan_set_forward_events(moe_plan* p, moe_event_t const* events,

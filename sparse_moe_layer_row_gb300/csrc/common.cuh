@@ -19,6 +19,8 @@ namespace moe {
 
 struct Layout {
     size_t status;       // uint32[MOE_STATUS_WORDS]
+    size_t flags;        // uint32[1024]               grid barriers of token.cu; at the same place in
+                         // every layout, so that plans of any shape may share a workspace
     size_t route_cnt;    // uint32[max_rows]          router row / row-group tickets
     size_t logits;       // fp32 [max_rows, E]        router logits (before bias)
     size_t wnorm;        // fp32 [E]                  |w_e|_2
@@ -41,7 +43,8 @@ struct Layout {
     size_t ys;           // fp16 [max_pairs + max_rows, H] staged per-pair and shared outputs
     size_t ysx;          // uint8 [H / 32, max_pairs + max_rows] power-of-two exponent of each
                          // 32-column quarter of a staged row (ys holds value * 2^-exponent)
-    size_t h32;          // fp32: h of calls of up to 8 rows on e4m3 experts, routed pairs then shared rows
+    size_t h32;          // fp32 (or two bf16 parts): h of calls of up to 8 rows in fp8_decode.cu and
+                         // token.cu, routed pairs then shared rows
     size_t total;
     int64_t max_pairs, max_units_gu, max_units_dn;
 };
@@ -86,6 +89,7 @@ inline Layout make_layout(const moe_dims& d) {
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 1024); return at; };
     L.status = take(sizeof(uint32_t) * 64);
+    L.flags = take(sizeof(uint32_t) * 1024);
     L.route_cnt = take(sizeof(uint32_t) * (size_t)R);
     L.logits = take(sizeof(float) * (size_t)(logit_rows(R) * E));
     L.wnorm = take(sizeof(float) * (size_t)E);

@@ -172,6 +172,10 @@ def load(build_if_missing: bool = False):
     L.moe_fp8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
     L.moe_fp8_gemm.restype = ctypes.c_int
     L.moe_fp8_gemm.argtypes = [P, P, i32, P, P, i32, i32, P, ctypes.c_int, i64, P, sz, P]
+    L.moe_token_pass.restype = ctypes.c_int
+    L.moe_token_pass.argtypes = [P, P, i32, P, P, P, P, P, P, sz, P]
+    L.moe_token_forward.restype = ctypes.c_int
+    L.moe_token_forward.argtypes = [P, P, i32, P, P, P, P, P, sz, P]
     L.moe_i8_quantize.restype = ctypes.c_int
     L.moe_i8_quantize.argtypes = [P, ctypes.c_int, i64, i32, i32, P, P, P]
     L.moe_i8_gemm_workspace_bytes.restype = sz
@@ -548,6 +552,38 @@ def moe_block_pass(plan: Plan, x, block_offsets, logit_bias, tau: float, max_exp
                                  _stream(stream)))
 
 
+def _token_args(plan, x, topk_idx, topk_w, y, y_f32, workspace):
+    d = plan.dims
+    R = x.shape[0]
+    _need(x, "x", torch.bfloat16, (R, d.H))
+    _need(topk_idx, "topk_idx", torch.int32, (R, d.k))
+    _need(topk_w, "topk_w", torch.float32, (R, d.k))
+    _need(y, "y", torch.bfloat16, (R, d.H))
+    if y_f32 is not None:
+        _need(y_f32, "y_f32", torch.float32, (R, d.H))
+    _need(workspace, "workspace", torch.uint8)
+    return R, _same_device(plan.weights[0], x, topk_idx, topk_w, y, y_f32, workspace)
+
+
+def moe_token_pass(plan: Plan, x, logit_bias, topk_idx, topk_w, y, y_f32, workspace, stream=None):
+    """The whole layer for up to 8 rows in one kernel (the full route: no coreset).  Writes
+    topk_idx, topk_w, y and, when given, y_f32; ``logit_bias``: fp32 [E] or None.  The
+    workspace must have been zeroed once (Plan.new_workspace)."""
+    R, dev = _token_args(plan, x, topk_idx, topk_w, y, y_f32, workspace)
+    if logit_bias is not None:
+        _need(logit_bias, "logit_bias", torch.float32, (plan.dims.E,))
+        _same_device(x, logit_bias)
+    _on(dev, load().moe_token_pass, plan.handle, _ptr(x), R, _ptr(logit_bias), _ptr(topk_idx),
+        _ptr(topk_w), _ptr(y), _ptr(y_f32), _ptr(workspace), workspace.numel(), _stream(stream, dev))
+
+
+def moe_token_forward(plan: Plan, x, topk_idx, topk_w, y, y_f32, workspace, stream=None):
+    """moe_token_pass under a given routing: topk_idx and topk_w are read."""
+    R, dev = _token_args(plan, x, topk_idx, topk_w, y, y_f32, workspace)
+    _on(dev, load().moe_token_forward, plan.handle, _ptr(x), R, _ptr(topk_idx), _ptr(topk_w),
+        _ptr(y), _ptr(y_f32), _ptr(workspace), workspace.numel(), _stream(stream, dev))
+
+
 def moe_block_logits(plan: Plan, x, block_offsets, logit_bias, logits, workspace, stream=None):
     """The router's logits (fp32 [R, E]) alone, for moe_route_scored."""
     d = plan.dims
@@ -858,6 +894,23 @@ class MoeBlockLayer:
         moe_block_pass(self.plan, x, block_offsets, bias, tau, max_experts, self._topk_idx[:R],
                        self._topk_w[:R], p, self._keep[:nb], self._core[:nb], self._w_renorm[:R],
                        self._empty[:nb], y, y_f32, self.workspace, stream)
+        return y
+
+    def token_pass(self, x, bias=None, topk_idx=None, topk_w=None, y=None, y_f32=None, stream=None):
+        """The whole layer for up to 8 rows in one kernel (moe_token_pass); returns y.  The
+        routing goes to ``topk_idx`` and ``topk_w``, or else to the layer's buffers."""
+        R = x.shape[0]
+        y = self._y[:R] if y is None else y
+        idx = self._topk_idx[:R] if topk_idx is None else topk_idx
+        w = self._topk_w[:R] if topk_w is None else topk_w
+        moe_token_pass(self.plan, x, bias, idx, w, y, y_f32, self.workspace, stream)
+        return y
+
+    def token_forward(self, x, topk_idx, topk_w, y=None, y_f32=None, stream=None):
+        """The experts of up to 8 rows under a given routing in one kernel
+        (moe_token_forward); returns y."""
+        y = self._y[:x.shape[0]] if y is None else y
+        moe_token_forward(self.plan, x, topk_idx, topk_w, y, y_f32, self.workspace, stream)
         return y
 
     def status(self, stream=None) -> dict:

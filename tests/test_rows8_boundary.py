@@ -96,3 +96,10 @@ def test_binding_refuses_cpu_tensors():
                  lambda: mb.moe_i8_gemm(x, x, x, x, x, x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_token_calls_refuse_a_null_plan(lib):
+    assert lib.moe_token_pass(None, OK, 1, None, OK, OK, OK2, None, OK3, 1 << 30, None) == -1
+    assert b"plan" in lib.moe_last_error()
+    assert lib.moe_token_forward(None, OK, 1, OK, OK, OK2, None, OK3, 1 << 30, None) == -1
+    assert b"plan" in lib.moe_last_error()
