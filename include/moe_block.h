@@ -301,16 +301,15 @@ moe_status moe_block_forward_live(const moe_plan* plan, const void* x, int32_t R
  * Does what moe_block_pass does with one block and tau = 1 (every chosen expert
  * kept): topk_idx and topk_w are moe_block_route's, bit for bit; y is the same sum
  *   y[r] = S(x[r]) + sum over the slots j of row r of topk_w[r, j] * E_{topk_idx[r, j]}(x[r])
- * with other roundings on the way: h enters the down projection as two bf16 parts (about
- * 16 significant bits; e4m3 plans: quantised as moe_plan_create_fp8 states), the experts'
- * outputs are summed in fp32 without being stored, in ascending order of the experts.
+ * with h rounded as there, and the experts' outputs summed in fp32 without being stored, the
+ * shared expert's first, in ascending order of the experts.
  * The result is reproducible, and does not depend on the other rows of a call but for the
  * order of fp32 sums.
  *   R           0 .. min(8, max_rows)
  *   logit_bias  [E] fp32 added to every row's logits, or NULL
  *   topk_idx, topk_w  [R, k] out;  y [R, H] bf16 out;  y_f32 [R, H] fp32 out, or NULL
- * Plans of bf16 or e4m3 experts (moe_plan_create, moe_plan_create_fp8) with H up to 8192;
- * others: MOE_ERR_UNSUPPORTED.  The kernel's CTAs wait for one another (it is launched
+ * Plans of bf16 or e4m3 experts (moe_plan_create, moe_plan_create_fp8) with H up to 8192
+ * and I and Is up to 16384; others: MOE_ERR_UNSUPPORTED.  The kernel's CTAs wait for one another (it is launched
  * cooperatively, one CTA per SM); their waits have the limit of moe_plan_set_wait_limit.
  * The workspace must have been zeroed once before its first use here.  MOE_STATUS_NONFINITE_OUTPUT
  * counts 16-column pieces. */

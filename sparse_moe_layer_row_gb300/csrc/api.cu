@@ -376,7 +376,7 @@ moe_status enqueue_token(const moe_plan* p, const void* x, int32_t R, bool given
     a.topk_idx = topk_idx;
     a.topk_w = topk_w;
     a.h = at<void>(workspace, L.h32);
-    a.flags = at<uint32_t>(workspace, L.flags);
+    a.counters = at<uint64_t>(workspace, L.barriers);
     a.status = at<uint32_t>(workspace, L.status);
     a.y = static_cast<__nv_bfloat16*>(y);
     a.y_f32 = y_f32;
@@ -394,6 +394,8 @@ moe_status check_token(const moe_plan* p, const void* x, int32_t R, const void* 
     if (p->qbits) return fail(MOE_ERR_UNSUPPORTED, "a plan of 8- or 4-bit integer experts: bf16 or e4m3");
     if (R > kTokenRows) return fail(MOE_ERR_UNSUPPORTED, "R=%d: at most %d rows", R, kTokenRows);
     if (p->d.H > kTokenMaxH) return fail(MOE_ERR_UNSUPPORTED, "H=%d: at most %d", p->d.H, kTokenMaxH);
+    if (p->d.I > kTokenMaxI || p->d.Is > kTokenMaxI)
+        return fail(MOE_ERR_UNSUPPORTED, "I=%d, Is=%d: at most %d", p->d.I, p->d.Is, kTokenMaxI);
     if (R == 0) return MOE_OK;
     if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x is NULL or not 16-byte aligned");
     if (!y || !aligned(y, 16)) return fail(MOE_ERR_INVALID_ARG, "y is NULL or not 16-byte aligned");

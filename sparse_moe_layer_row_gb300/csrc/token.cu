@@ -20,17 +20,23 @@
 // unit's K; all sixteen share the down step's experts and K.  K is permuted alike in both
 // operands, so that a lane's are 16-byte loads.
 //
-// h lies in global memory between the steps: with bf16 weights as two bf16 parts
-// (16 significant bits), with e4m3 ones in fp32, quantised by every reader with
-// the formula of the other paths.
+// h lies in global memory between the steps: with bf16 weights rounded as the other paths
+// round it (bf16; the shared expert's, which enters every row with weight 1, as two bf16 parts),
+// with e4m3 ones in fp32, quantised by every reader with the formula of the other paths.
+// Every CTA needs all of it: it is staged in shared memory first, where it fits (STAGED; 8
+// rows of 8 experts of 512 do), so that a tile costs no round trip to L2.
 //
-// Barriers: an array of one flag per CTA each, polled by a warp.  A CTA clears its flag
-// of the second before it arrives at the first, and that of the first when it has
-// passed the second, which every CTA then has reached; so the flags need no clearing by
-// the host.  With the routing given there is one barrier: CTAs that have passed it set
-// their second flag, and one CTA, beside its work, waits for all of those and clears the first
-// array.  Every wait is bounded; a CTA that gives up counts MOE_STATUS_WAIT_TIMEOUT, clears its
-// flags and leaves.
+// Latency is what costs: a grid barrier takes a microsecond or two, in which HBM would stand
+// still.  So every warp keeps tiles of weights in flight, in shared memory, across the ends
+// of units and across the barrier before the down step, and the CTA's down weights go to
+// L2 while gate/up runs (the shared expert's while the router does).  Code that runs once is
+// fetched while everything waits for it: loops are not unrolled, and nothing is divided.
+//
+// Barriers: a 64-bit counter each, to which every CTA adds one; it waits until the
+// counter has reached the next multiple of the grid.  Each call adds a whole grid to
+// each counter that it uses, so that they need no clearing.  Every wait is bounded; a CTA that
+// gives up counts MOE_STATUS_WAIT_TIMEOUT, adds its one to the barrier that it will not reach, and
+// leaves.
 #include "route_common.cuh"
 #include "token.cuh"
 
@@ -41,32 +47,47 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kGroup = 4;                       // warps that share a gate/up unit
 constexpr int kGroups = kWarps / kGroup;
-constexpr uint32_t kArrived = 0x5EEDF1A6u;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxPairs = kTokenRows * 32;      // k <= 32
 constexpr int64_t kPrefetchBytes = 32 << 20;    // of the down weights, a quarter of L2
 
+// A tile: 16 weight rows by 128 bytes of K; a lane holds 32 bytes of two rows.
+template <bool FP8>
+constexpr int kTileK = FP8 ? 128 : 64;
+constexpr int kStage = 2048;   // shared memory of a tile in flight, per warp: each lane's 4 x 16 bytes
+
 struct Smem {
-    float part[2][kWarps][kTokenRows][17];      // partial sums (token, weight row)
+    float part[2][kWarps][kTokenRows][17];      // partial sums (row, weight row)
     float wt[kMaxPairs][kTokenRows];            // weight of (listed expert, row)
-    float w[kMaxPairs];                         // [R, k]
-    int32_t idx[kMaxPairs];
     uint32_t mask[kMaxExperts];                 // rows of an expert
+    uint32_t used[kMaxExperts / 32];            // experts touched, a bit each
     int32_t list[kMaxPairs];                    // experts touched, ascending
-    uint32_t lmask[kMaxPairs];                  // their rows
-    int32_t first[kMaxPairs];                   // pairs before them
-    uint32_t count[kWarps];
+    uint8_t lmask[kMaxPairs];                   // their rows
+    uint8_t slot[kMaxPairs][kTokenRows];        // first slot of (listed expert, row)
     uint32_t scratch[MOE_STATUS_WORDS];         // for status counts that another CTA makes
-    uint32_t bad;                               // rows with a non-finite output
-    int nl, ok;
+    int32_t idx[kMaxPairs];                     // [R, k]
+    float w[kMaxPairs];
+    int ok;
 };
 
 // x in shared memory: rows far enough apart that a quarter-warp's 16-byte reads share no bank
 template <bool FP8>
 __host__ __device__ constexpr int x_stride(int H) { return FP8 ? H + 16 : 2 * H + 64; }
 template <bool FP8>
-__host__ __device__ constexpr int x_bytes(int H) {
+__host__ __device__ constexpr int x_bytes(int H) {   // a multiple of 128: H % 256 == 0
     return kTokenRows * x_stride<FP8>(H) + (FP8 ? (H / kFp8Block) * kTokenRows * 4 : 0);
+}
+constexpr int kSmemHead = (int)(sizeof(Smem) + 127) / 128 * 128;
+constexpr int kSmemMax = 227 * 1024;
+// h in x's place: routed pairs (row r k + slot), then the shared expert's; bf16: its hi, then its
+// lo parts; e4m3: codes, then the scales per block of 128
+template <bool FP8>
+__host__ __device__ constexpr int h_stride(int I) { return FP8 ? I + 16 : 2 * I + 64; }
+template <bool FP8>
+__host__ __device__ inline int64_t h_bytes(int R, int k, int I, int Is) {
+    int64_t n = (int64_t)R * k * h_stride<FP8>(I) + (int64_t)R * (FP8 ? 1 : 2) * h_stride<FP8>(Is);
+    if (FP8) n += 4 * (int64_t)R * (k * fp8_blocks(I) + fp8_blocks(Is));
+    return (n + 127) / 128 * 128;
 }
 
 __device__ __forceinline__ uint4 ld_weights(const void* p) {
@@ -78,6 +99,24 @@ __device__ __forceinline__ uint4 ld_weights(const void* p) {
 }
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+// 16 bytes, of which the first `bytes` (all or none) are read and the rest are zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// All but the newest depth - 1 of this thread's copy groups are complete.
+__device__ __forceinline__ void wait_tile(int depth) {
+    if (depth == 4) cp_async_wait<3>();
+    else if (depth == 3) cp_async_wait<2>();
+    else cp_async_wait<1>();
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -97,74 +136,59 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// What a lane holds of 16 weight rows and 128 of K: rows gi and gi + 8.  bf16: 16 bytes of
-// each 32 of K (8 elements); e4m3: 32 bytes in a row.
+// A lane's part of a tile, rows gi (a) and gi + 8 (b): bf16: 16 bytes of each 32 of K;
+// e4m3: 32 bytes in a row.
 template <bool FP8>
-struct Tile {
-    static constexpr int kN = FP8 ? 2 : 4;
-    uint4 a[kN], b[kN];
-};
-// pa, pb: the rows' first element of these 128 of K for lane c; `left`: elements of K from
-// there on to the end (zeros past it)
+__device__ __forceinline__ int tile_at(int c, int i) { return FP8 ? 32 * c + 16 * i : 64 * i + 16 * c; }
+// From pa and pb (the rows at the tile's start) to the lane's slots; `left`: bytes of K from
+// there to the end, zeros past it.
 template <bool FP8>
-__device__ __forceinline__ void load_tile(Tile<FP8>& t, const uint8_t* pa, const uint8_t* pb, int c, int left) {
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* pa, const uint8_t* pb, int c, int left) {
 #pragma unroll
-    for (int i = 0; i < Tile<FP8>::kN; ++i) {
-        const int at = FP8 ? 32 * c + 16 * i : 64 * i + 16 * c;   // bytes
-        const bool in = FP8 ? at < left : at < 2 * left;
-        t.a[i] = in ? ld_weights(pa + at) : make_uint4(0, 0, 0, 0);
-        t.b[i] = in ? ld_weights(pb + at) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+        const int at = tile_at<FP8>(c, i);
+        const int n = at < left ? 16 : 0, from = at < left ? at : 0;
+        copy16(dst + 512 * i, pa + from, n);
+        copy16(dst + 1024 + 512 * i, pb + from, n);
     }
 }
+// d += tile . x, the tile in the lane's slots
 template <bool FP8>
-__device__ __forceinline__ void tile_mma(float (&d)[4], const Tile<FP8>& t, const uint4 (&x)[Tile<FP8>::kN]) {
+__device__ __forceinline__ void tile_mma(float (&d)[4], const uint4 (&a)[2], const uint4 (&b)[2], const uint4 (&x)[2]) {
 #pragma unroll
-    for (int i = 0; i < Tile<FP8>::kN; ++i) {
+    for (int i = 0; i < 2; ++i) {
         if (FP8) {
-            mma_e4m3(d, t.a[i].x, t.b[i].x, t.a[i].y, t.b[i].y, x[i].x, x[i].y);
-            mma_e4m3(d, t.a[i].z, t.b[i].z, t.a[i].w, t.b[i].w, x[i].z, x[i].w);
+            mma_e4m3(d, a[i].x, b[i].x, a[i].y, b[i].y, x[i].x, x[i].y);
+            mma_e4m3(d, a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
         } else {
-            mma_bf16(d, t.a[i].x, t.b[i].x, t.a[i].y, t.b[i].y, x[i].x, x[i].y);
-            mma_bf16(d, t.a[i].z, t.b[i].z, t.a[i].w, t.b[i].w, x[i].z, x[i].w);
+            mma_bf16(d, a[i].x, b[i].x, a[i].y, b[i].y, x[i].x, x[i].y);
+            mma_bf16(d, a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
         }
     }
 }
 
-__device__ __forceinline__ uint32_t ld_flag(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ uint64_t ld_counter(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_flag(uint32_t* p, uint32_t v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+// Releases what the CTA wrote before the __syncthreads ahead of it.
+__device__ __forceinline__ void arrive(uint64_t* p) {
+    asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p), "l"((uint64_t)1) : "memory");
 }
-
-// Wait, as one warp, until every CTA's flag is set; false: gave up.
-__device__ __forceinline__ bool wait_flags(const uint32_t* flags, int n, uint64_t limit_ns, int lane) {
-    const uint64_t t0 = globaltimer_ns();
-    for (int i = lane;; ) {
-        while (i < n && ld_flag(flags + i) == kArrived) i += 32;
-        if (__all_sync(0xffffffffu, i >= n)) break;
-        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
-    }
-    __threadfence();
-    return true;
-}
-
-// A grid barrier on `flags`; the whole CTA calls it.  False: gave up, the same in every thread.
-__device__ __forceinline__ bool grid_barrier(uint32_t* flags, const TokenArgs& a, Smem& s) {
+// A grid barrier; the whole CTA calls it.  goal: the counter's next multiple of the grid (in
+// thread 0).  False: gave up, the same in every thread.
+__device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t goal, uint64_t limit_ns, int* ok) {
     __syncthreads();
-    if (threadIdx.x < 32) {
-        if (threadIdx.x == 0) {
-            __threadfence();
-            st_flag(flags + blockIdx.x, kArrived);
-        }
-        __syncwarp();
-        const bool ok = wait_flags(flags, gridDim.x, a.wait_ns ? a.wait_ns : kWaitLimitNs, threadIdx.x);
-        if (threadIdx.x == 0) s.ok = ok;
+    if (threadIdx.x == 0) {
+        arrive(counter);
+        bool in = true;
+        const uint64_t t0 = globaltimer_ns();
+        while (in && ld_counter(counter) < goal) in = globaltimer_ns() - t0 <= limit_ns;
+        *ok = in;
     }
     __syncthreads();
-    return s.ok;
+    return *ok;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {   // the xor butterfly of route_common.cuh
@@ -175,7 +199,7 @@ __device__ __forceinline__ float warp_sum(float v) {   // the xor butterfly of r
 
 // Logits of one expert for all rows, one warp.
 __device__ __forceinline__ void expert_logits(const TokenArgs& a, int e, int lane) {
-    constexpr int kS = 4;   // stripes of 256 at a time
+    constexpr int kS = 8;   // stripes of 256 at a time
     float acc[kTokenRows];
 #pragma unroll
     for (int r = 0; r < kTokenRows; ++r) acc[r] = 0.0f;
@@ -189,9 +213,13 @@ __device__ __forceinline__ void expert_logits(const TokenArgs& a, int e, int lan
         for (int r = 0; r < kTokenRows; ++r) {
             if (r >= a.R) break;
             const __nv_bfloat16* xr = a.x + (int64_t)r * a.H + lane * 8 + s0;
+            uint4 xv[kS];
 #pragma unroll
             for (int i = 0; i < kS; ++i)
-                if (s0 + 256 * i < a.H) acc[r] = dot8_bf16(__ldg(reinterpret_cast<const uint4*>(xr + 256 * i)), wv[i], acc[r]);
+                xv[i] = s0 + 256 * i < a.H ? __ldg(reinterpret_cast<const uint4*>(xr + 256 * i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kS; ++i)
+                if (s0 + 256 * i < a.H) acc[r] = dot8_bf16(xv[i], wv[i], acc[r]);
         }
     }
 #pragma unroll
@@ -201,6 +229,9 @@ __device__ __forceinline__ void expert_logits(const TokenArgs& a, int e, int lan
         if (lane == 0) a.logits[(int64_t)r * a.E + e] = z;
     }
 }
+
+// Top-k of one row: not inlined, its variants by E are most of the kernel's code.
+__device__ __noinline__ void token_topk(const RouteArgs& ra, int row, int lane) { route_topk(ra, row, row + 1, lane); }
 
 // x into shared memory: as it is, or as e4m3 codes and scales per block of 128 (fp8.cuh).
 template <bool FP8>
@@ -235,31 +266,35 @@ __device__ __forceinline__ void stage_x(const TokenArgs& a, uint8_t* sx) {
 
 }  // namespace
 
-template <bool FP8>
+template <bool FP8, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     extern __shared__ __align__(128) uint8_t base[];
     Smem& s = *reinterpret_cast<Smem*>(base);
-    uint8_t* sx = base + (sizeof(Smem) + 127) / 128 * 128;
+    uint8_t* sx = base + kSmemHead;
     const float* xs = reinterpret_cast<const float*>(sx + kTokenRows * x_stride<FP8>(a.H));
     constexpr int kES = FP8 ? 1 : 2;   // bytes per weight
+    constexpr int kTK = kTileK<FP8>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, c = lane & 3;
     const int G = gridDim.x, cta = blockIdx.x;
-    uint32_t* flags1 = a.flags;
-    uint32_t* flags2 = a.flags + kTokenMaxCtas;
-    if (tid == 0) st_flag(flags2 + cta, 0);   // released before this CTA's arrival below
+    const uint64_t limit = a.wait_ns ? a.wait_ns : kWaitLimitNs;
+    uint64_t goal1 = 0, goal2 = 0;   // thread 0's
+    if (tid == 0) {   // this CTA's own arrivals are missing, so neither can have passed its multiple
+        goal1 = (ld_counter(a.counters) / G + 1) * G;
+        goal2 = (ld_counter(a.counters + 1) / G + 1) * G;
+    }
     const uint8_t *wg = static_cast<const uint8_t*>(a.wg), *wu = static_cast<const uint8_t*>(a.wu),
                   *wd = static_cast<const uint8_t*>(a.wd), *sg = static_cast<const uint8_t*>(a.sg),
                   *su = static_cast<const uint8_t*>(a.su), *sd = static_cast<const uint8_t*>(a.sd);
-    const int utiles = a.I / 8, stiles = a.Is / 8, dtiles = a.H / 16;
-    auto give_up = [&]() {   // the whole CTA
-        if (tid == 0) {
-            status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
-            st_flag(flags1 + cta, 0);
-        }
-    };
+    const int utiles = a.I / 8, stiles = a.Is / 8, dtiles = a.H / 16, np = a.R * a.k;
 
     // ---- step 1: logits; the shared expert's weights, which do not depend on them, to L2
-    if (tid == kThreads - 1) {
+    int my_e = -1;         // given: lane j of warp r holds slot j of row r
+    float my_w = 0.0f;
+    if (a.given && warp < a.R && lane < a.k) {
+        my_e = __ldg(a.topk_idx + warp * a.k + lane);
+        my_w = __ldg(a.topk_w + warp * a.k + lane);
+    }
+    if (tid == 0) {
         const uint32_t gb = 8u * a.H * kES, db = 16u * a.Is * kES;
         for (int t = cta; t < stiles; t += G) {
             prefetch_l2(sg + (int64_t)t * gb, gb);
@@ -267,21 +302,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         }
         for (int t = cta; t < dtiles; t += G) prefetch_l2(sd + (int64_t)t * db, db);
     }
-    if (!a.given)
-        for (int e = cta + G * warp; e < a.E; e += G * kWarps) expert_logits(a, e, lane);
+    if (!a.given)   // the last warps: the first ones stage x meanwhile
+        for (int e = cta + G * (kWarps - 1 - warp); e < a.E; e += G * kWarps) expert_logits(a, e, lane);
     stage_x<FP8>(a, sx);
     for (int i = tid; i < a.E; i += kThreads) s.mask[i] = 0;
+    if (tid < kMaxExperts / 32) s.used[tid] = 0;
     if (tid < MOE_STATUS_WORDS) s.scratch[tid] = 0;
-    if (tid == 0) s.bad = 0;
-    if (!a.given && !grid_barrier(flags1, a, s)) {
-        give_up();
+    if (a.given) {
+        __syncthreads();
+    } else if (!grid_barrier(a.counters, goal1, limit, &s.ok)) {
+        if (tid == 0) {
+            status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
+            arrive(a.counters + 1);   // the barrier that this CTA will not reach
+        }
         return;
     }
 
     // ---- step 2: the experts of each row and the list of all of them
-    const int np = a.R * a.k;
-    if (!a.given) {
-        if (warp < a.R) {
+    uint32_t same = 0;     // slots of the row with the same expert
+    if (warp < a.R) {
+        if (!a.given) {
             RouteArgs ra{};
             ra.bias = a.bias;
             ra.R = a.R;
@@ -292,321 +332,497 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             ra.topk_idx = s.idx;
             ra.topk_w = s.w;
             ra.status = cta == 0 ? a.status : s.scratch;
-            route_topk(ra, warp, warp + 1, lane);
-        }
-        __syncthreads();
-        if (cta == 0)
-            for (int i = tid; i < np; i += kThreads) {
-                a.topk_idx[i] = s.idx[i];
-                a.topk_w[i] = s.w[i];
-            }
-    } else {
-        for (int i = tid; i < np; i += kThreads) {
-            s.idx[i] = __ldg(a.topk_idx + i);
-            s.w[i] = __ldg(a.topk_w + i);
-        }
-        __syncthreads();
-    }
-    for (int i = tid; i < np; i += kThreads) {
-        const int e = s.idx[i];
-        if (e >= 0 && e < a.E) atomicOr(&s.mask[e], 1u << (i / a.k));
-        else if (cta == 0) status_add(a.status, MOE_STATUS_BAD_EXPERT_ID, 1);
-    }
-    __syncthreads();
-    // experts in ascending order: two per thread (E <= 1024)
-    {
-        const uint32_t m0 = 2 * tid < a.E ? s.mask[2 * tid] : 0u, m1 = 2 * tid + 1 < a.E ? s.mask[2 * tid + 1] : 0u;
-        // low half: experts, high half: pairs
-        const uint32_t mine = (m0 != 0) + (m1 != 0) + ((__popc(m0) + __popc(m1)) << 16);
-        uint32_t at = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(0xffffffffu, at, o);
-            if (lane >= o) at += t;
-        }
-        if (lane == 31) s.count[warp] = at;
-        __syncthreads();
-        uint32_t total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) at += s.count[w];
-            total += s.count[w];
-        }
-        at -= mine;
-        if (tid == 0) s.nl = total & 0xFFFF;
-        if (m0) {
-            const int l = at & 0xFFFF;
-            s.list[l] = 2 * tid;
-            s.lmask[l] = m0;
-            s.first[l] = at >> 16;
-            at += 1 + (__popc(m0) << 16);
-        }
-        if (m1) {
-            const int l = at & 0xFFFF;
-            s.list[l] = 2 * tid + 1;
-            s.lmask[l] = m1;
-            s.first[l] = at >> 16;
-        }
-    }
-    __syncthreads();
-    const int nl = s.nl;
-    for (int i = tid; i < nl * kTokenRows; i += kThreads) {   // weights in slot order
-        const int l = i / kTokenRows, r = i % kTokenRows;
-        float w = 0.0f;
-        if (r < a.R)
-            for (int j = 0; j < a.k; ++j)
-                if (s.idx[r * a.k + j] == s.list[l]) w += s.w[r * a.k + j];
-        s.wt[l][r] = w;
-    }
-    if (tid < a.R && cta == 0) {   // rows left with the shared expert alone
-        bool any = false;
-        for (int j = 0; j < a.k; ++j) any |= s.idx[tid * a.k + j] >= 0 && s.idx[tid * a.k + j] < a.E;
-        if (!any) status_add(a.status, MOE_STATUS_EMPTY_ROWS, 1);
-    }
-    // this CTA's part of the down weights, to L2 while gate/up runs
-    if (tid == kThreads - 1) {
-        const uint32_t db = 16u * a.I * kES;
-        int64_t left = kPrefetchBytes / G;
-        for (int t = cta; t < dtiles; t += G)
-            for (int l = 0; l < nl && (left -= db) >= 0; ++l)
-                prefetch_l2(wd + ((int64_t)s.list[l] * a.H + 16 * t) * a.I * kES, db);
-    }
-
-    // ---- gate/up
-    __nv_bfloat16* hb = static_cast<__nv_bfloat16*>(a.h);   // bf16: hi | lo, then the shared expert's
-    float* hf = static_cast<float*>(a.h);                   // e4m3: fp32
-    const int64_t hpart = (int64_t)np * a.I, spart = (int64_t)a.R * a.Is;
-    {
-        const int group = warp / kGroup, gw = warp % kGroup;
-        const int nunits = stiles + nl * utiles;
-        const int kblocks = a.H / 128;   // of which this warp takes gw, gw + 4, ...
-        const int steps = (kblocks - gw + kGroup - 1) / kGroup;
-        const int ustep = G * kGroups;
-        // the unit's rows for this lane; a unit past the last has none
-        struct Rows { const uint8_t *g, *u; const float *cg, *cu; };
-        auto rows_of = [&](int u) {
-            Rows q{};
-            const bool sh = u < stiles;
-            const int l = sh ? 0 : (u - stiles) / utiles;
-            const int t = sh ? u : (u - stiles) - l * utiles;
-            const int64_t e = sh ? 0 : s.list[l];
-            const int ld = sh ? a.Is : a.I;
-            const int64_t o = ((e * ld + 8 * t + gi) * a.H + gw * 128) * kES;
-            q.g = (sh ? sg : wg) + o;
-            q.u = (sh ? su : wu) + o;
-            if (FP8) {
-                const int64_t so = (e * fp8_blocks(ld) + t / 16) * kblocks + gw;
-                q.cg = (sh ? a.csg : a.cg) + so;
-                q.cu = (sh ? a.csu : a.cu) + so;
-            }
-            return q;
-        };
-        // the tiles of all units of this warp, one ahead
-        int u = cta + G * group;
-        Tile<FP8> t[2];
-        float fg[2] = {0.0f, 0.0f}, fu[2] = {0.0f, 0.0f};
-        Rows q{};
-        auto load = [&](const Rows& p, int step, int b) {
-            load_tile<FP8>(t[b], p.g + (int64_t)step * kGroup * 128 * kES, p.u + (int64_t)step * kGroup * 128 * kES, c, 128);
-            if (FP8) {
-                fg[b] = __ldg(p.cg + step * kGroup);
-                fu[b] = __ldg(p.cu + step * kGroup);
-            }
-        };
-        if (u < nunits) q = rows_of(u);
-        bool have = u < nunits && steps > 0;
-        if (have) load(q, 0, 0);
-        int pb = 0;
-        while (u < nunits) {
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            Rows qn{};
-            const int un = u + ustep;
-            if (un < nunits) qn = rows_of(un);
-            for (int st = 0; st < steps; st += 2) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (st + b < steps) {
-                        // the next tile: of this unit, or the first of the next
-                        if (st + b + 1 < steps) load(q, st + b + 1, b ^ 1);
-                        else if (un < nunits && b == 1) load(qn, 0, 0);
-                        const int kb = gw + (st + b) * kGroup;
-                        uint4 x[Tile<FP8>::kN];
-                        const uint8_t* xr = sx + gi * x_stride<FP8>(a.H) + kb * 128 * kES;
-#pragma unroll
-                        for (int i = 0; i < Tile<FP8>::kN; ++i)
-                            x[i] = gi < a.R ? *reinterpret_cast<const uint4*>(xr + (FP8 ? 32 * c + 16 * i : 64 * i + 16 * c))
-                                            : make_uint4(0, 0, 0, 0);
-                        if (FP8) {
-                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            tile_mma<FP8>(d, t[b], x);
-                            const float x0 = xs[kb * kTokenRows + 2 * c], x1 = xs[kb * kTokenRows + 2 * c + 1];
-                            acc[0] = fmaf(x0 * fg[b], d[0], acc[0]);
-                            acc[1] = fmaf(x1 * fg[b], d[1], acc[1]);
-                            acc[2] = fmaf(x0 * fu[b], d[2], acc[2]);
-                            acc[3] = fmaf(x1 * fu[b], d[3], acc[3]);
-                        } else {
-                            tile_mma<FP8>(acc, t[b], x);
-                        }
-                    }
+            token_topk(ra, warp, lane);
+            __syncwarp();
+            if (lane < a.k) {
+                my_e = s.idx[warp * a.k + lane];
+                my_w = s.w[warp * a.k + lane];
+                if (cta == 0) {
+                    a.topk_idx[warp * a.k + lane] = my_e;
+                    a.topk_w[warp * a.k + lane] = my_w;
                 }
             }
-            // an odd number of steps leaves the next unit's first tile to load here
-            if (un < nunits && (steps & 1)) load(qn, 0, 0);
+        }
+        const bool good = lane < a.k && my_e >= 0 && my_e < a.E;
+        const uint32_t ok = __ballot_sync(0xffffffffu, good);
+        same = __match_any_sync(0xffffffffu, good ? my_e : -1 - lane);
+        if (good && lane == __ffs(same) - 1) {
+            atomicOr(&s.mask[my_e], 1u << warp);
+            atomicOr(&s.used[my_e >> 5], 1u << (my_e & 31));
+        }
+        if (cta == 0 && lane == 0) {
+            status_add(a.status, MOE_STATUS_BAD_EXPERT_ID, a.k - __popc(ok));
+            status_add(a.status, MOE_STATUS_EMPTY_ROWS, ok == 0);
+        }
+        if (!good) my_e = -1;
+        // an expert in several slots: their weights in slot order, in the first of them
+        uint32_t rest = same & (same - 1);
+        if (__any_sync(0xffffffffu, rest != 0)) {
+            float sum = my_w;
+            for (int j = 0; j < 32; ++j) {
+                const float o = __shfl_sync(0xffffffffu, my_w, j);
+                if ((rest >> j) & 1u) sum += o;
+            }
+            my_w = sum;
+        }
+    }
+    __syncthreads();
+    // an expert's place in the list: touched experts below it.  Lane i has word i of `used`.
+    const uint32_t word = s.used[lane];
+    int upto = __popc(word);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const int nl = __shfl_sync(0xffffffffu, upto, 31);
+    auto place = [&](int e) {   // all lanes take part
+        const int i = e >> 5;
+        const uint32_t w = __shfl_sync(0xffffffffu, word, i);
+        return __shfl_sync(0xffffffffu, upto, i) - __popc(w) + __popc(w & ((1u << (e & 31)) - 1));
+    };
+    for (int e0 = 32 * warp; e0 < a.E; e0 += kThreads) {
+        const int l = place(e0 + lane);
+        const uint32_t m = e0 + lane < a.E ? s.mask[e0 + lane] : 0u;
+        if (m) {
+            s.list[l] = e0 + lane;
+            s.lmask[l] = (uint8_t)m;
+        }
+    }
+    if (warp < a.R) {
+        const int l = place(my_e >= 0 ? my_e : 0);
+        if (my_e >= 0 && lane == __ffs(same) - 1) {
+            s.wt[l][warp] = my_w;
+            s.slot[l][warp] = (uint8_t)lane;
+        }
+    }
+    __syncthreads();
+    // ---- gate/up: units of 8 intermediate indices, the shared expert's first
+    __nv_bfloat16* hb = static_cast<__nv_bfloat16*>(a.h);   // bf16: routed, then the shared expert's hi and lo parts
+    float* hf = static_cast<float*>(a.h);                   // e4m3: fp32
+    const int64_t hpart = (int64_t)np * a.I, spart = (int64_t)a.R * a.Is;
+    const uint32_t all = (1u << a.R) - 1;
+    // the lane's slots of the tiles in flight, taken in turn
+    const int depth = a.depth;
+    const uint32_t ring = smem_u32(sx) + a.arena + warp * (depth * kStage) + lane * 16;
+    const uint32_t ring_end = ring + depth * kStage;
+    uint32_t fill = ring, take = ring;
+    auto next_slot = [&](uint32_t at) {
+        at += kStage;
+        return at == ring_end ? ring : at;
+    };
+    {
+        const int group = warp / kGroup, gw = warp % kGroup;
+        const int nunits = stiles + nl * utiles, ustep = G * kGroups;
+        const int tiles = a.H / kTK;                        // of which this warp takes gw, gw + 4, ...
+        const int kend = (tiles + kGroup - 1) / kGroup * kGroup;   // alike for all warps: zeros past the end
+        int lu = cta + G * group, lk = gw;   // the next tile to copy
+        const uint8_t *lg = wg, *lv = wu;
+        // unit u: its expert (list index; shared: -1) and its tile there
+        auto unit = [&](int u, int& ti) {
+            if (u < stiles) {
+                ti = u;
+                return -1;
+            }
+            const int l = (int)__umulhi(u - stiles, a.inv_utiles);
+            ti = u - stiles - l * utiles;
+            return l;
+        };
+        auto copy_next = [&]() {
+            if (lu < nunits) {
+                if (lk == gw) {   // a new unit
+                    int ti;
+                    const int l = unit(lu, ti);
+                    const int64_t o = ((l < 0 ? 0 : (int64_t)s.list[l] * a.I) + 8 * ti + gi) * a.H * kES;
+                    lg = (l < 0 ? sg : wg) + o;
+                    lv = (l < 0 ? su : wu) + o;
+                }
+                const int k = lk < tiles ? lk : 0;
+                copy_tile<FP8>(fill, lg + k * 128, lv + k * 128, c, lk < tiles ? 128 : 0);
+                lk += kGroup;
+                if (lk >= kend) {
+                    lk = gw;
+                    lu += ustep;
+                }
+            }
+            cp_async_commit();
+            fill = next_slot(fill);
+        };
+        // e4m3: the scales of this warp's tiles of a unit, gate's in lanes 0 .., up's in 16 ..
+        // (H / 128 is at most 64, a quarter of it 16)
+        auto scales_of = [&](int u) {
+            const int k = gw + kGroup * (lane & 15);
+            if (!FP8 || u >= nunits || k >= tiles) return 0.0f;
+            int ti;
+            const int l = unit(u, ti);
+            const int64_t o = ((l < 0 ? 0 : (int64_t)s.list[l] * fp8_blocks(a.I)) + (ti >> 4)) * tiles + k;
+            return __ldg((l < 0 ? (lane < 16 ? a.csg : a.csu) : (lane < 16 ? a.cg : a.cu)) + o);
+        };
+        float sc_next = scales_of(lu);
+#pragma unroll 1
+        for (int i = 0; i < depth - 1; ++i) copy_next();
+        const uint32_t xrow = smem_u32(sx) + gi * x_stride<FP8>(a.H);
+        int pb = 0;
+#pragma unroll 1
+        for (int u = cta + G * group; u < nunits; u += ustep) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float sc = sc_next;
+            sc_next = scales_of(u + ustep);
+#pragma unroll 1
+            for (int kt = gw; kt < kend; kt += kGroup) {
+                copy_next();
+                wait_tile(depth);
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                const bool in = gi < a.R && kt < tiles;
+                const uint4 x[2] = {in ? lds16(xrow + kt * 128 + tile_at<FP8>(c, 0)) : z,
+                                    in ? lds16(xrow + kt * 128 + tile_at<FP8>(c, 1)) : z};
+                const uint4 ta[2] = {lds16(take), lds16(take + 512)}, tb[2] = {lds16(take + 1024), lds16(take + 1536)};
+                if (FP8) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    tile_mma<FP8>(d, ta, tb, x);
+                    const float fa = __shfl_sync(0xffffffffu, sc, kt / kGroup), fb = __shfl_sync(0xffffffffu, sc, 16 + kt / kGroup);
+                    const int kc = kt < tiles ? kt : 0;
+                    const float x0 = 2 * c < a.R ? xs[kc * kTokenRows + 2 * c] : 0.0f;
+                    const float x1 = 2 * c + 1 < a.R ? xs[kc * kTokenRows + 2 * c + 1] : 0.0f;
+                    acc[0] = fmaf(x0 * fa, d[0], acc[0]);
+                    acc[1] = fmaf(x1 * fa, d[1], acc[1]);
+                    acc[2] = fmaf(x0 * fb, d[2], acc[2]);
+                    acc[3] = fmaf(x1 * fb, d[3], acc[3]);
+                } else {
+                    tile_mma<FP8>(acc, ta, tb, x);
+                }
+                take = next_slot(take);
+            }
+            // the unit's sums over its four warps, and h
 #pragma unroll
             for (int j = 0; j < 4; ++j) s.part[pb][warp][2 * c + (j & 1)][gi + 8 * (j >> 1)] = acc[j];
             asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kGroup) : "memory");
-            const int t8 = (tid & (32 * kGroup - 1)) >> 3, i = tid & 7;   // row, index
-            const bool sh = u < stiles;
-            const int l = sh ? 0 : (u - stiles) / utiles, tt = sh ? u : (u - stiles) - l * utiles;
-            const uint32_t m = sh ? (1u << a.R) - 1 : s.lmask[l];
-            if (t8 < kTokenRows && ((m >> t8) & 1u)) {
+            const int r = (tid & (32 * kGroup - 1)) >> 3, i = tid & 7;   // row, index
+            int ti;
+            const int l = unit(u, ti);
+            const bool sh = l < 0;
+            const uint32_t m = sh ? all : s.lmask[l];
+            if (r < kTokenRows && ((m >> r) & 1u)) {
                 float g = 0.0f, v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kGroup; ++w) {
-                    g += s.part[pb][group * kGroup + w][t8][i];
-                    v += s.part[pb][group * kGroup + w][t8][8 + i];
+                    g += s.part[pb][group * kGroup + w][r][i];
+                    v += s.part[pb][group * kGroup + w][r][8 + i];
                 }
                 const float h = silu_fast(g) * v;
-                const int p = sh ? t8 : s.first[l] + __popc(m & ((1u << t8) - 1));
-                const int64_t at = (int64_t)p * (sh ? a.Is : a.I) + 8 * tt + i;
+                const int p = sh ? r : r * a.k + s.slot[l][r];
+                const int64_t at = (int64_t)p * (sh ? a.Is : a.I) + 8 * ti + i;
                 if (FP8) {
                     hf[(sh ? hpart : 0) + at] = h;
                 } else {
                     const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                    __nv_bfloat16* o = hb + (sh ? 2 * hpart : 0) + at;
+                    __nv_bfloat16* o = hb + (sh ? hpart : 0) + at;
                     o[0] = hi;
-                    o[sh ? spart : hpart] = __float2bfloat16_rn(h - __bfloat162float(hi));
+                    if (sh) o[spart] = __float2bfloat16_rn(h - __bfloat162float(hi));
                 }
             }
-            pb ^= 1;   // read before the barrier of the unit after the next, written after that of the next
-            u = un;
-            q = qn;
+            pb ^= 1;   // written again behind the next unit's barrier: read by then
         }
     }
 
-    if (!grid_barrier(a.given ? flags1 : flags2, a, s)) {
-        give_up();
+    // ---- step 3: down.  Turn by turn 16 hidden outputs; the tiles of all experts (the shared
+    // one's first) go round the warps.  The first tiles are on their way before the barrier.
+    const int kb_r = (a.I + kTK - 1) / kTK, kb_s = (a.Is + kTK - 1) / kTK;   // tiles of an expert's K
+    const int items = kb_s + nl * kb_r;
+    const int iend = (items + kWarps - 1) / kWarps * kWarps;   // alike for all warps: nothing past the end
+    struct Item { int t, it, l, kb; };   // turn's outputs, tile; its expert (-1: shared) and place in K
+    auto first = [&](Item& q) {
+        q.it = warp;
+        q.l = -1;
+        q.kb = warp;
+        while (q.kb >= (q.l < 0 ? kb_s : kb_r)) {
+            q.kb -= q.l < 0 ? kb_s : kb_r;
+            ++q.l;
+        }
+    };
+    auto advance = [&](Item& q) {
+        q.it += kWarps;
+        if (q.it >= iend) {
+            q.t += G;
+            first(q);
+        } else {
+            q.kb += kWarps;
+            while (q.kb >= (q.l < 0 ? kb_s : kb_r)) {
+                q.kb -= q.l < 0 ? kb_s : kb_r;
+                ++q.l;
+            }
+        }
+    };
+    Item ld;
+    ld.t = cta;
+    first(ld);
+    auto copy_next = [&]() {
+        if (ld.t < dtiles && ld.it < items) {
+            const bool sh = ld.l < 0;
+            const int K = sh ? a.Is : a.I;
+            const int64_t e = sh ? 0 : s.list[ld.l];
+            const uint8_t* w = (sh ? sd : wd) + ((e * a.H + 16 * ld.t + gi) * K + ld.kb * kTK) * kES;
+            copy_tile<FP8>(fill, w, w + (int64_t)8 * K * kES, c, (K - ld.kb * kTK) * kES);
+        }
+        cp_async_commit();
+        fill = next_slot(fill);
+        advance(ld);
+    };
+    fill = take;   // every tile of gate/up has been taken
+#pragma unroll 1
+    for (int i = 0; i < depth - 1; ++i) copy_next();
+    // the rest of this CTA's first turns' weights, to L2 meanwhile
+    if (warp == kWarps - 1) {
+        const uint32_t db = 16u * a.I * kES;
+        const int most = (int)(kPrefetchBytes / G / db), mine = (dtiles - cta + G - 1) / G * nl;
+        for (int i = lane; i < min(most, mine); i += 32)
+            prefetch_l2(wd + ((int64_t)s.list[i % nl] * a.H + 16 * (cta + i / nl * G)) * a.I * kES, db);
+    }
+
+    if (!grid_barrier(a.counters + (a.given ? 0 : 1), a.given ? goal1 : goal2, limit, &s.ok)) {
+        cp_async_wait<0>();
+        if (tid == 0) status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
         return;
     }
-    if (tid == 0) {
-        if (a.given) st_flag(flags2 + cta, kArrived);   // passed
-        else st_flag(flags1 + cta, 0);
+    if (cta >= dtiles) {
+        cp_async_wait<0>();
+        return;
     }
-
-    // ---- step 3: down
-    const int kb_r = fp8_blocks(a.I), kb_s = fp8_blocks(a.Is);   // blocks of 128 of an expert's K
-    const int items = kb_s + nl * kb_r;
-    for (int t = cta; t < dtiles; t += G) {
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int it = warp; it < items; it += kWarps) {
-            const bool sh = it < kb_s;
-            const int l = sh ? 0 : (it - kb_s) / kb_r;
-            const int kb = sh ? it : (it - kb_s) - l * kb_r;
-            const int K = sh ? a.Is : a.I;
-            const int64_t e = sh ? 0 : s.list[l];
-            const uint8_t* w = (sh ? sd : wd) + ((e * a.H + 16 * t + gi) * K + kb * 128) * kES;
-            Tile<FP8> tl;
-            load_tile<FP8>(tl, w, w + (int64_t)8 * K * kES, c, K - kb * 128);
-            const uint32_t m = sh ? (1u << a.R) - 1 : s.lmask[l];
-            const bool on = (m >> gi) & 1u;
-            const int p = sh ? gi : s.first[l] + __popc(m & ((1u << gi) - 1));
-            const int64_t at = (int64_t)p * K + kb * 128;
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            float f0 = sh ? 1.0f : s.wt[l][2 * c], f1 = sh ? 1.0f : s.wt[l][2 * c + 1];
-            if constexpr (FP8) {
-                const float sw = __ldg((sh ? a.csd : a.cd) + (e * (a.H / kFp8Block) + t / 8) * (sh ? kb_s : kb_r) + kb);
-                const float* ph = hf + (sh ? hpart : 0) + at + 32 * c;
-                const bool in = on && kb * 128 + 32 * c < K;   // K % 64 == 0: all 32 values or none
-                float4 v[8];
-                uint32_t mx = 0;
+    // h, staged: offsets of the shared expert's part and of the scales
+    const int rstr = h_stride<FP8>(a.I), sstr = h_stride<FP8>(a.Is);
+    const int hs0 = np * rstr, hsc0 = hs0 + a.R * (FP8 ? 1 : 2) * sstr;
+    if constexpr (STAGED) {
+        if constexpr (FP8) {   // a warp per row, two blocks at a time
+            float* hsc = reinterpret_cast<float*>(sx + hsc0);
+            for (int p = warp; p < np + a.R; p += kWarps) {
+                const bool sh = p >= np;
+                const int K = sh ? a.Is : a.I, nb = sh ? kb_s : kb_r;
+                const float* src = hf + (sh ? hpart + (int64_t)(p - np) * K : (int64_t)p * K);
+                uint8_t* dst = sx + (sh ? hs0 + (p - np) * sstr : p * rstr);
+                float* sc = hsc + (sh ? np * kb_r + (p - np) * kb_s : p * kb_r);
+#pragma unroll 2
+                for (int b0 = 0; b0 < nb; b0 += 2) {   // half a warp per block
+                    const int k = 128 * b0 + 8 * lane;
+                    float v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = in ? __ldcg(reinterpret_cast<const float4*>(ph) + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    mx = max(mx, max(max(__float_as_uint(v[i].x) & 0x7FFFFFFFu, __float_as_uint(v[i].y) & 0x7FFFFFFFu),
-                                     max(__float_as_uint(v[i].z) & 0x7FFFFFFFu, __float_as_uint(v[i].w) & 0x7FFFFFFFu)));
+                    for (int i = 0; i < 2; ++i) {   // K % 64 == 0: eight values are all inside or none
+                        const float4 f = k < K ? __ldcg(reinterpret_cast<const float4*>(src + k) + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+                    }
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+                    for (int o = 8; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float bm = __uint_as_float(fp8_amax_bits(mx));
+                    const float inv = __fdiv_rn(448.0f, bm);
+                    if (k < K)
+                        *reinterpret_cast<uint2*>(dst + k) = make_uint2(
+                            fp8_pair(v[0] * inv, v[1] * inv) | fp8_pair(v[2] * inv, v[3] * inv) << 16,
+                            fp8_pair(v[4] * inv, v[5] * inv) | fp8_pair(v[6] * inv, v[7] * inv) << 16);
+                    if ((lane & 15) == 0 && k < K) sc[k >> 7] = __fdiv_rn(bm, 448.0f);
                 }
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float bm = __uint_as_float(fp8_amax_bits(mx));
-                const float inv = __fdiv_rn(448.0f, bm), scale = __fdiv_rn(bm, 448.0f);
-                uint32_t q[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    q[i] = fp8_pair(v[i].x * inv, v[i].y * inv) | fp8_pair(v[i].z * inv, v[i].w * inv) << 16;
-                const uint4 x[2] = {make_uint4(q[0], q[1], q[2], q[3]), make_uint4(q[4], q[5], q[6], q[7])};
-                tile_mma<FP8>(d, tl, x);
-                f0 *= __shfl_sync(0xffffffffu, scale, 8 * c) * sw;   // row r's scale is in lanes 4 r ..
-                f1 *= __shfl_sync(0xffffffffu, scale, 8 * c + 4) * sw;
-            } else {
-                const __nv_bfloat16* ph = hb + (sh ? 2 * hpart : 0) + at;
-                const int64_t lo = sh ? spart : hpart;
-                uint4 x[2][Tile<FP8>::kN];
-#pragma unroll
-                for (int i = 0; i < Tile<FP8>::kN; ++i) {
-                    const int k = 32 * i + 8 * c;
-                    const bool in = on && kb * 128 + k < K;
-                    x[0][i] = in ? __ldcg(reinterpret_cast<const uint4*>(ph + k)) : make_uint4(0, 0, 0, 0);
-                    x[1][i] = in ? __ldcg(reinterpret_cast<const uint4*>(ph + lo + k)) : make_uint4(0, 0, 0, 0);
-                }
-                tile_mma<FP8>(d, tl, x[0]);
-                tile_mma<FP8>(d, tl, x[1]);
             }
-            // columns of rows that did not choose the expert stay out (its weights may not be finite)
-            if ((m >> (2 * c)) & 1u) { acc[0] = fmaf(f0, d[0], acc[0]); acc[2] = fmaf(f0, d[2], acc[2]); }
-            if ((m >> (2 * c + 1)) & 1u) { acc[1] = fmaf(f1, d[1], acc[1]); acc[3] = fmaf(f1, d[3], acc[3]); }
-        }
-        __syncthreads();   // an earlier turn's sums have been read
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s.part[0][warp][2 * c + (j & 1)][gi + 8 * (j >> 1)] = acc[j];
-        __syncthreads();
-        if (tid < kTokenRows * 16 && (tid >> 4) < a.R) {
-            const int r = tid >> 4, n = tid & 15;
-            float v = s.part[0][0][r][n];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) v += s.part[0][w][r][n];
-            const int64_t at = (int64_t)r * a.H + 16 * t + n;
-            a.y[at] = __float2bfloat16_rn(v);
-            if (a.y_f32) a.y_f32[at] = v;
-            if (!(fabsf(v) < INFINITY)) atomicOr(&s.bad, 1u << r);
+        } else {
+            for (int p = warp; p < np + 2 * a.R; p += kWarps) {
+                const bool sh = p >= np;
+                const int K = sh ? a.Is : a.I;
+                const __nv_bfloat16* src = hb + (sh ? hpart + (int64_t)(p - np) * K : (int64_t)p * K);
+                const uint32_t dst = smem_u32(sx) + (sh ? hs0 + (p - np) * sstr : p * rstr);
+                for (int k = 8 * lane; k < K; k += 256) copy16(dst + 2 * k, src + k, 16);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
         }
         __syncthreads();
-        if (tid == 0) {
-            status_add(a.status, MOE_STATUS_NONFINITE_OUTPUT, __popc(s.bad));
-            s.bad = 0;
-        }
     }
-    // clear the barrier's flags once every CTA has passed it
-    if (a.given && cta == G - 1 && warp == kWarps - 1) {
-        const bool ok = wait_flags(flags2, G, a.wait_ns ? a.wait_ns : kWaitLimitNs, lane);
-        if (!ok && lane == 0) status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
-        for (int i = lane; i < G; i += 32) st_flag(flags1 + i, 0);
+    {
+        constexpr int kHN = FP8 ? 8 : 4;   // not staged: 16-byte pieces of h per lane and tile (bf16: hi, lo)
+        // what the lane multiplies of tile q: row gi's part; zeros where the row did not choose the expert
+        auto load_h = [&](const Item& q, uint4 (&v)[kHN]) {
+            const bool sh = q.l < 0;
+            const int K = sh ? a.Is : a.I;
+            bool on = q.t < dtiles && q.it < items;
+            if (on) on = ((sh ? all : (uint32_t)s.lmask[q.l]) >> gi) & 1u;
+            if (FP8) on = on && q.kb * kTK + 32 * c < K;   // K % 64 == 0: all of the 32 values or none
+            const int64_t at = on ? (int64_t)(sh ? gi : gi * a.k + s.slot[q.l][gi]) * K + q.kb * kTK : 0;
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            if constexpr (FP8) {
+                const float* src = hf + (sh ? hpart : 0) + at + 32 * c;
+#pragma unroll
+                for (int i = 0; i < kHN; ++i) v[i] = on ? __ldcg(reinterpret_cast<const uint4*>(src) + i) : z;
+            } else {
+                const __nv_bfloat16* src = hb + (sh ? hpart : 0) + at + 8 * c;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    v[i] = on ? __ldcg(reinterpret_cast<const uint4*>(src + 32 * i)) : z;
+                    v[2 + i] = on && sh ? __ldcg(reinterpret_cast<const uint4*>(src + spart + 32 * i)) : z;
+                }
+            }
+        };
+        auto scale_of = [&](const Item& q) {   // 16 outputs lie in one block of 128
+            if (!FP8 || q.t >= dtiles || q.it >= items) return 0.0f;
+            const bool sh = q.l < 0;
+            const int64_t e = sh ? 0 : s.list[q.l];
+            return __ldg((sh ? a.csd : a.cd) + (e * (a.H / kFp8Block) + (q.t >> 3)) * (sh ? kb_s : kb_r) + q.kb);
+        };
+        Item cur, nxt;
+        cur.t = cta;
+        first(cur);
+        nxt = cur;
+        uint4 h[STAGED ? 1 : kHN], hn[STAGED ? 1 : kHN];
+        if constexpr (!STAGED) load_h(cur, h);
+        float sw = scale_of(cur);
+        int pb = 0;
+#pragma unroll 1
+        for (int t = cta; t < dtiles; t += G) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int it = warp; it < iend; it += kWarps) {
+                copy_next();
+                advance(nxt);
+                if constexpr (!STAGED) load_h(nxt, hn);
+                const float sw_next = scale_of(nxt);
+                wait_tile(depth);
+                if (it < items) {
+                    const bool sh = cur.l < 0;
+                    const uint32_t m = sh ? all : s.lmask[cur.l];
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float f0 = sh ? 1.0f : s.wt[cur.l][2 * c], f1 = sh ? 1.0f : s.wt[cur.l][2 * c + 1];
+                    const uint4 ta[2] = {lds16(take), lds16(take + 512)}, tb[2] = {lds16(take + 1024), lds16(take + 1536)};
+                    const bool on = (m >> gi) & 1u;
+                    const int p = sh ? gi : gi * a.k + (on ? s.slot[cur.l][gi] : 0);
+                    const uint32_t hrow = smem_u32(sx) + (sh ? hs0 + p * sstr : p * rstr) + cur.kb * 128;
+                    if constexpr (FP8) {
+                        float scale;
+                        uint4 x[2];
+                        if constexpr (STAGED) {
+                            const bool in = on && cur.kb * kTK + 32 * c < (sh ? a.Is : a.I);
+                            x[0] = in ? lds16(hrow + 32 * c) : z;
+                            x[1] = in ? lds16(hrow + 32 * c + 16) : z;
+                            scale = on ? reinterpret_cast<const float*>(sx + hsc0)[(sh ? np * kb_r + p * kb_s : p * kb_r) + cur.kb] : 0.0f;
+                        } else {
+                            uint32_t mx = 0;
+#pragma unroll
+                            for (int i = 0; i < kHN; ++i)
+                                mx = max(mx, max(max(h[i].x & 0x7FFFFFFFu, h[i].y & 0x7FFFFFFFu),
+                                                 max(h[i].z & 0x7FFFFFFFu, h[i].w & 0x7FFFFFFFu)));
+                            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                            const float bm = __uint_as_float(fp8_amax_bits(mx));
+                            const float inv = __fdiv_rn(448.0f, bm);
+                            scale = __fdiv_rn(bm, 448.0f);
+                            uint32_t q[8];
+#pragma unroll
+                            for (int i = 0; i < kHN; ++i)
+                                q[i] = fp8_pair(__uint_as_float(h[i].x) * inv, __uint_as_float(h[i].y) * inv) |
+                                       fp8_pair(__uint_as_float(h[i].z) * inv, __uint_as_float(h[i].w) * inv) << 16;
+                            x[0] = make_uint4(q[0], q[1], q[2], q[3]);
+                            x[1] = make_uint4(q[4], q[5], q[6], q[7]);
+                        }
+                        tile_mma<FP8>(d, ta, tb, x);
+                        f0 *= __shfl_sync(0xffffffffu, scale, 8 * c) * sw;   // row r's scale is in lanes 4 r ..
+                        f1 *= __shfl_sync(0xffffffffu, scale, 8 * c + 4) * sw;
+                    } else if constexpr (STAGED) {
+                        const uint32_t at = hrow + 16 * c;
+                        const uint4 xh[2] = {on ? lds16(at) : z, on ? lds16(at + 64) : z};
+                        tile_mma<FP8>(d, ta, tb, xh);
+                        if (sh) {   // the lo part
+                            const uint32_t lo = at + a.R * sstr;
+                            const uint4 xl[2] = {on ? lds16(lo) : z, on ? lds16(lo + 64) : z};
+                            tile_mma<FP8>(d, ta, tb, xl);
+                        }
+                    } else {
+                        const uint4 xh[2] = {h[0], h[1]}, xl[2] = {h[2], h[3]};
+                        tile_mma<FP8>(d, ta, tb, xh);
+                        if (sh) tile_mma<FP8>(d, ta, tb, xl);
+                    }
+                    // columns of rows that did not choose the expert stay out (its weights may not be finite)
+                    if ((m >> (2 * c)) & 1u) { acc[0] = fmaf(f0, d[0], acc[0]); acc[2] = fmaf(f0, d[2], acc[2]); }
+                    if ((m >> (2 * c + 1)) & 1u) { acc[1] = fmaf(f1, d[1], acc[1]); acc[3] = fmaf(f1, d[3], acc[3]); }
+                }
+                take = next_slot(take);
+                cur = nxt;
+                sw = sw_next;
+                if constexpr (!STAGED) {
+#pragma unroll
+                    for (int i = 0; i < kHN; ++i) h[i] = hn[i];
+                }
+            }
+            // the turn's sums over the warps
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s.part[pb][warp][2 * c + (j & 1)][gi + 8 * (j >> 1)] = acc[j];
+            __syncthreads();
+            if (warp < kTokenRows / 2) {   // two rows per warp
+                const int r = tid >> 4, n = tid & 15;
+                float v = s.part[pb][0][r][n];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v += s.part[pb][w][r][n];
+                const uint32_t nf = __ballot_sync(0xffffffffu, !(fabsf(v) < INFINITY));
+                if (r < a.R) {
+                    const int64_t at = (int64_t)r * a.H + 16 * t + n;
+                    a.y[at] = __float2bfloat16_rn(v);
+                    if (a.y_f32) a.y_f32[at] = v;
+                    if (n == 0) status_add(a.status, MOE_STATUS_NONFINITE_OUTPUT, ((nf >> (lane & 16)) & 0xFFFFu) != 0);
+                }
+            }
+            pb ^= 1;   // written again behind the next turn's barrier: read by then
+        }
+        cp_async_wait<0>();
     }
 }
 
 namespace {
+
+// Where x or h lie, and how many tiles are in flight: four where both fit beside them, else
+// three or two; h is staged where two do.
 template <bool FP8>
-int smem_bytes(int H) { return (int)(sizeof(Smem) + 127) / 128 * 128 + x_bytes<FP8>(H); }
+void plan_smem(TokenArgs& a, bool* staged, int* bytes) {
+    const int64_t x = x_bytes<FP8>(a.H), h = h_bytes<FP8>(a.R, a.k, a.I, a.Is), room = kSmemMax - kSmemHead;
+    *staged = h <= room - 2 * kWarps * kStage;
+    a.arena = (int)(*staged && h > x ? h : x);
+    const int64_t d = (room - a.arena) / (kWarps * kStage);
+    a.depth = d < 4 ? (int)d : 4;
+    *bytes = kSmemHead + a.arena + a.depth * kWarps * kStage;
+}
+static_assert(x_bytes<false>(kTokenMaxH) + 2 * kWarps * kStage <= kSmemMax - kSmemHead &&
+              x_bytes<true>(kTokenMaxH) + 2 * kWarps * kStage <= kSmemMax - kSmemHead, "two tiles in flight");
+
 }  // namespace
 
 cudaError_t token_set_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(k_token<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<false>(kTokenMaxH));
-    return e == cudaSuccess ? cudaFuncSetAttribute(k_token<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   smem_bytes<true>(kTokenMaxH)) : e;
+    cudaError_t e = cudaSuccess;
+    auto set = [&](auto k) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    };
+    set(k_token<false, false>);
+    set(k_token<false, true>);
+    set(k_token<true, false>);
+    set(k_token<true, true>);
+    return e;
 }
 
-cudaError_t launch_token(bool fp8, const TokenArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_token(bool fp8, TokenArgs a, int num_sms, cudaStream_t st) {
+    // u / d = umulhi(u, ceil(2^32 / d)) while u d < 2^32: u below 256 d and d up to 2048
+    a.inv_utiles = (uint32_t)((((uint64_t)1 << 32) + a.I / 8 - 1) / (uint64_t)(a.I / 8));
+    bool staged;
+    int bytes;
+    if (fp8) plan_smem<true>(a, &staged, &bytes);
+    else plan_smem<false>(a, &staged, &bytes);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(num_sms < kTokenMaxCtas ? num_sms : kTokenMaxCtas));
+    cfg.gridDim = dim3((unsigned)num_sms);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = fp8 ? smem_bytes<true>(a.H) : smem_bytes<false>(a.H);
+    cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;   // every CTA is resident: they wait for one another
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return fp8 ? cudaLaunchKernelEx(&cfg, k_token<true>, a) : cudaLaunchKernelEx(&cfg, k_token<false>, a);
+    auto k = fp8 ? (staged ? k_token<true, true> : k_token<true, false>)
+                 : (staged ? k_token<false, true> : k_token<false, false>);
+    return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 }  // namespace moe

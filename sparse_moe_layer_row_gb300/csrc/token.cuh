@@ -7,7 +7,7 @@ namespace moe {
 
 constexpr int kTokenRows = 8;      // the N of one mma.sync tile
 constexpr int kTokenMaxH = 8192;   // x lies in shared memory
-constexpr int kTokenMaxCtas = 512; // flags per barrier
+constexpr int kTokenMaxI = 16384;  // I and Is (a division by multiplication)
 
 struct TokenArgs {
     const __nv_bfloat16* x;       // [R, H]
@@ -23,13 +23,15 @@ struct TokenArgs {
     int32_t* topk_idx;            // [R, k]
     float* topk_w;
     void* h;                      // 4 bytes for each of R (k I + Is) values
-    uint32_t* flags;              // 2 x kTokenMaxCtas (see token.cu)
+    uint64_t* counters;           // of the two grid barriers
     uint32_t* status;
     __nv_bfloat16* y;             // [R, H]
     float* y_f32;                 // or NULL
+    uint32_t inv_utiles;          // set by the launcher, as are the next two
+    int arena, depth;             // shared memory of x and h; tiles in flight
     uint64_t wait_ns;             // limit of a grid barrier's wait (0: the built-in limit)
 };
 cudaError_t token_set_attributes();
-cudaError_t launch_token(bool fp8, const TokenArgs&, int num_sms, cudaStream_t);
+cudaError_t launch_token(bool fp8, TokenArgs, int num_sms, cudaStream_t);
 
 }  // namespace moe

@@ -3,8 +3,8 @@ plain 64-bit references.
 
 Bounds (fp8_ref's terms): a sum over K is off by at most sum_factor(K) of its addends'
 magnitudes; silu by 2^-21 + |g| 2^-23 of itself (fast exponential and quotient) and
-1.1 times the error of g; two bf16 parts keep h to 2^-16 of itself; the sum over experts
-adds a rounding of 2^-24 per addend.
+1.1 times the error of g; bf16 keeps a routed h to 2^-8 of itself, two bf16 parts the shared
+expert's to 2^-16; the sum over experts adds a rounding of 2^-24 per addend.
 """
 from __future__ import annotations
 
@@ -53,7 +53,7 @@ class Case:
         self.idx = torch.rand(R, E, generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
         self.wt = torch.softmax(torch.randn(R, k, generator=g, device="cuda"), 1)
 
-    def ffn(self, x, wg, wu, wd):
+    def ffn(self, x, wg, wu, wd, h_step=2.0 ** -8):
         """(o, bound) of rows x in 64 bits."""
         if self.kind == "e4m3":
             return F.swiglu(x, wg, wu, wd)
@@ -62,14 +62,14 @@ class Case:
         dg, du = (x.abs() @ wg.abs().t()) * f, (x.abs() @ wu.abs().t()) * f
         silu = g * torch.sigmoid(g)
         h = silu * u
-        dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + h.abs() * (g.abs() * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -16)
+        dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + h.abs() * (g.abs() * 2.0 ** -23 + 2.0 ** -21 + h_step)
         return h @ wd.t(), dh @ wd.abs().t() + (h.abs() @ wd.abs().t()) * 2 * F.sum_factor(self.I + self.Is)
 
     def reference(self, idx=None, wt=None, x=None):
         idx, wt = self.idx if idx is None else idx, self.wt if wt is None else wt
         x = self.x if x is None else x
         xv = F.row_values(*F.quantize(x)) if self.kind == "e4m3" else x.double()
-        y, bound = self.ffn(xv, *self.w[3:])
+        y, bound = self.ffn(xv, *self.w[3:], h_step=2.0 ** -16)
         mag = y.abs()
         for e in idx.unique().tolist():
             if not 0 <= e < self.E:
@@ -110,7 +110,7 @@ class Case:
 
 
 SHAPES = [dict(), dict(H=512, E=24, k=3, I=192, Is=64), dict(H=1280, E=64, k=6, I=320, Is=640),
-          dict(H=768, E=300, k=8, I=64, Is=64), dict(H=256, E=1024, k=32, I=64, Is=128), dict(H=256, E=1, k=1, I=64, Is=64)]
+          dict(H=768, E=300, k=8, I=64, Is=64), dict(H=256, E=32, k=32, I=512, Is=1024), dict(H=2560, E=6, k=2, I=4096, Is=2112), dict(H=256, E=1024, k=32, I=64, Is=128), dict(H=256, E=1, k=1, I=64, Is=64)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
