@@ -19,7 +19,7 @@ namespace moe {
 
 struct Layout {
     size_t status;       // uint32[MOE_STATUS_WORDS]
-    size_t barriers;     // uint64[2]                  grid barriers of token.cu; at the same place in
+    size_t barriers;     // uint32[2]                  grid barriers of token.cu; at the same place in
                          // every layout, so that plans of any shape may share a workspace
     size_t route_cnt;    // uint32[max_rows]          router row / row-group tickets
     size_t logits;       // fp32 [max_rows, E]        router logits (before bias)
@@ -89,7 +89,7 @@ inline Layout make_layout(const moe_dims& d) {
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 1024); return at; };
     L.status = take(sizeof(uint32_t) * 64);
-    L.barriers = take(sizeof(uint64_t) * 2);
+    L.barriers = take(sizeof(uint32_t) * 2);
     L.route_cnt = take(sizeof(uint32_t) * (size_t)R);
     L.logits = take(sizeof(float) * (size_t)(logit_rows(R) * E));
     L.wnorm = take(sizeof(float) * (size_t)E);

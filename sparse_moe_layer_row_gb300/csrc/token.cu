@@ -8,8 +8,8 @@
 // A few rows touch a few experts, whose weights take HBM some microseconds: what a row
 // of kernels costs between them is what there is to save.  One CTA per SM, launched
 // cooperatively, goes through three steps with a grid barrier between them:
-//   1  a warp per expert: its logits for all rows, in the order of route_common.cuh
-//   2  every CTA: top-k of all rows (the same code as moe_block_route's, so the same
+//   1  a warp per expert and row: its logit, in the order of route_common.cuh
+//   2  every CTA: top-k of all rows (in moe_block_route's order and arithmetic, so the same
 //      ids and weights), the list of the experts touched, and its share of gate/up
 //   3  16 hidden outputs per CTA and turn: down, summed over all experts in registers, so
 //      that nothing is staged or combined
@@ -32,11 +32,11 @@
 // L2 while gate/up runs (the shared expert's while the router does).  Code that runs once is
 // fetched while everything waits for it: loops are not unrolled, and nothing is divided.
 //
-// Barriers: a 64-bit counter each, to which every CTA adds one; it waits until the
-// counter has reached the next multiple of the grid.  Each call adds a whole grid to
-// each counter that it uses, so that they need no clearing.  Every wait is bounded; a CTA that
-// gives up counts MOE_STATUS_WAIT_TIMEOUT, adds its one to the barrier that it will not reach, and
-// leaves.
+// Barriers: a counter each, to which the CTAs add 1024 in all (the first one what the others,
+// 1 each, leave); a CTA waits until the counter has left the 1024 that it started in.  Each
+// call adds 1024 to each counter that it uses, so that they need no clearing.  Every wait is
+// bounded; a CTA that gives up counts MOE_STATUS_WAIT_TIMEOUT, adds its share to the barrier
+// that it will not reach, and leaves.
 #include "route_common.cuh"
 #include "token.cuh"
 
@@ -54,7 +54,9 @@ constexpr int64_t kPrefetchBytes = 32 << 20;    // of the down weights, a quarte
 // A tile: 16 weight rows by 128 bytes of K; a lane holds 32 bytes of two rows.
 template <bool FP8>
 constexpr int kTileK = FP8 ? 128 : 64;
-constexpr int kStage = 2048;   // shared memory of a tile in flight, per warp: each lane's 4 x 16 bytes
+// Shared memory of a tile in flight, per warp: each lane's 4 x 16 bytes, and a scale (down, e4m3)
+template <bool FP8>
+constexpr int kStage = 2048 + (FP8 ? 128 : 0);
 
 struct Smem {
     float part[2][kWarps][kTokenRows][17];      // partial sums (row, weight row)
@@ -70,19 +72,22 @@ struct Smem {
     int ok;
 };
 
-// x in shared memory: rows far enough apart that a quarter-warp's 16-byte reads share no bank
+// x in shared memory: rows an odd multiple of 64 bytes apart, so that a quarter-warp's reads (two
+// rows, 64 bytes each) share no bank
+__host__ __device__ constexpr int odd64(int bytes) { return bytes + (bytes % 128 ? 0 : 64); }
 template <bool FP8>
-__host__ __device__ constexpr int x_stride(int H) { return FP8 ? H + 16 : 2 * H + 64; }
+__host__ __device__ constexpr int x_stride(int H) { return odd64(FP8 ? H : 2 * H); }
 template <bool FP8>
 __host__ __device__ constexpr int x_bytes(int H) {   // a multiple of 128: H % 256 == 0
     return kTokenRows * x_stride<FP8>(H) + (FP8 ? (H / kFp8Block) * kTokenRows * 4 : 0);
 }
 constexpr int kSmemHead = (int)(sizeof(Smem) + 127) / 128 * 128;
 constexpr int kSmemMax = 227 * 1024;
+static_assert(kTokenRows * 4 * (kMaxExperts + 128) <= 2 * kWarps * 2048, "keys and candidates fit the ring");
 // h in x's place: routed pairs (row r k + slot), then the shared expert's; bf16: its hi, then its
 // lo parts; e4m3: codes, then the scales per block of 128
 template <bool FP8>
-__host__ __device__ constexpr int h_stride(int I) { return FP8 ? I + 16 : 2 * I + 64; }
+__host__ __device__ constexpr int h_stride(int I) { return odd64(FP8 ? I : 2 * I); }
 template <bool FP8>
 __host__ __device__ inline int64_t h_bytes(int R, int k, int I, int Is) {
     int64_t n = (int64_t)R * k * h_stride<FP8>(I) + (int64_t)R * (FP8 ? 1 : 2) * h_stride<FP8>(Is);
@@ -90,13 +95,6 @@ __host__ __device__ inline int64_t h_bytes(int R, int k, int I, int Is) {
     return (n + 127) / 128 * 128;
 }
 
-__device__ __forceinline__ uint4 ld_weights(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -111,6 +109,14 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 // 16 bytes, of which the first `bytes` (all or none) are read and the rest are zeros
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float lds4(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 // All but the newest depth - 1 of this thread's copy groups are complete.
 __device__ __forceinline__ void wait_tile(int depth) {
@@ -136,17 +142,15 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A lane's part of a tile, rows gi (a) and gi + 8 (b): bf16: 16 bytes of each 32 of K;
-// e4m3: 32 bytes in a row.
-template <bool FP8>
-__device__ __forceinline__ int tile_at(int c, int i) { return FP8 ? 32 * c + 16 * i : 64 * i + 16 * c; }
+// A lane's part of a tile, rows gi (a) and gi + 8 (b): 16 of each 64 bytes, so that four
+// lanes read 64 in a row.
+__device__ __forceinline__ int tile_at(int c, int i) { return 64 * i + 16 * c; }
 // From pa and pb (the rows at the tile's start) to the lane's slots; `left`: bytes of K from
 // there to the end, zeros past it.
-template <bool FP8>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* pa, const uint8_t* pb, int c, int left) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int at = tile_at<FP8>(c, i);
+        const int at = tile_at(c, i);
         const int n = at < left ? 16 : 0, from = at < left ? at : 0;
         copy16(dst + 512 * i, pa + from, n);
         copy16(dst + 1024 + 512 * i, pb + from, n);
@@ -167,24 +171,26 @@ __device__ __forceinline__ void tile_mma(float (&d)[4], const uint4 (&a)[2], con
     }
 }
 
-__device__ __forceinline__ uint64_t ld_counter(const uint64_t* p) {
-    uint64_t v;
-    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
+constexpr uint32_t kRound = 1024;
+__device__ __forceinline__ uint32_t ld_round(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v & ~(kRound - 1);
 }
 // Releases what the CTA wrote before the __syncthreads ahead of it.
-__device__ __forceinline__ void arrive(uint64_t* p) {
-    asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p), "l"((uint64_t)1) : "memory");
+__device__ __forceinline__ void arrive(uint32_t* p) {
+    const uint32_t n = blockIdx.x == 0 ? kRound - (gridDim.x - 1) : 1;
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(n) : "memory");
 }
-// A grid barrier; the whole CTA calls it.  goal: the counter's next multiple of the grid (in
+// A grid barrier; the whole CTA calls it.  round: the counter's at the start of the kernel (in
 // thread 0).  False: gave up, the same in every thread.
-__device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t goal, uint64_t limit_ns, int* ok) {
+__device__ __forceinline__ bool grid_barrier(uint32_t* counter, uint32_t round, uint64_t limit_ns, int* ok) {
     __syncthreads();
     if (threadIdx.x == 0) {
         arrive(counter);
         bool in = true;
         const uint64_t t0 = globaltimer_ns();
-        while (in && ld_counter(counter) < goal) in = globaltimer_ns() - t0 <= limit_ns;
+        while (in && ld_round(counter) == round) in = globaltimer_ns() - t0 <= limit_ns;
         *ok = in;
     }
     __syncthreads();
@@ -197,41 +203,83 @@ __device__ __forceinline__ float warp_sum(float v) {   // the xor butterfly of r
     return v;
 }
 
-// Logits of one expert for all rows, one warp.
-__device__ __forceinline__ void expert_logits(const TokenArgs& a, int e, int lane) {
+// The logit of one expert and row, one warp.
+__device__ __forceinline__ void expert_logit(const TokenArgs& a, int e, int r, int lane) {
     constexpr int kS = 8;   // stripes of 256 at a time
-    float acc[kTokenRows];
-#pragma unroll
-    for (int r = 0; r < kTokenRows; ++r) acc[r] = 0.0f;
+    float acc = 0.0f;
     const __nv_bfloat16* w = a.wr + (int64_t)e * a.H + lane * 8;
+    const __nv_bfloat16* x = a.x + (int64_t)r * a.H + lane * 8;
     for (int s0 = 0; s0 < a.H; s0 += 256 * kS) {
-        uint4 wv[kS];
+        uint4 wv[kS], xv[kS];
+#pragma unroll
+        for (int i = 0; i < kS; ++i) {
+            const bool in = s0 + 256 * i < a.H;
+            wv[i] = in ? __ldg(reinterpret_cast<const uint4*>(w + s0 + 256 * i)) : make_uint4(0, 0, 0, 0);
+            xv[i] = in ? __ldg(reinterpret_cast<const uint4*>(x + s0 + 256 * i)) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < kS; ++i)
-            wv[i] = s0 + 256 * i < a.H ? ld_weights(w + s0 + 256 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < kTokenRows; ++r) {
-            if (r >= a.R) break;
-            const __nv_bfloat16* xr = a.x + (int64_t)r * a.H + lane * 8 + s0;
-            uint4 xv[kS];
-#pragma unroll
-            for (int i = 0; i < kS; ++i)
-                xv[i] = s0 + 256 * i < a.H ? __ldg(reinterpret_cast<const uint4*>(xr + 256 * i)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kS; ++i)
-                if (s0 + 256 * i < a.H) acc[r] = dot8_bf16(xv[i], wv[i], acc[r]);
-        }
+            if (s0 + 256 * i < a.H) acc = dot8_bf16(xv[i], wv[i], acc);
     }
-#pragma unroll
-    for (int r = 0; r < kTokenRows; ++r) {
-        if (r >= a.R) break;
-        const float z = warp_sum(acc[r]);
-        if (lane == 0) a.logits[(int64_t)r * a.E + e] = z;
-    }
+    const float z = warp_sum(acc);
+    if (lane == 0) a.logits[(int64_t)r * a.E + e] = z;
 }
 
-// Top-k of one row: not inlined, its variants by E are most of the kernel's code.
-__device__ __noinline__ void token_topk(const RouteArgs& ra, int row, int lane) { route_topk(ra, row, row + 1, lane); }
+// Rows with many equal logits: the top-k of route_common.cuh.  Not inlined: rarely called code.
+__device__ __noinline__ void topk_slow(const RouteArgs& ra, int row, int lane) { route_topk(ra, row, row + 1, lane); }
+
+// Top-k of one row and the weights, one warp: what route_topk writes, in fewer steps and less code.
+// The k-th largest of the lanes' own largest keys is a lower bound of the k-th largest key; few keys
+// reach it, and their ranks among each other are counted.  buf: E keys, then 2 x 32 (key, id).
+__device__ __forceinline__ void topk_row(const RouteArgs& ra, int row, int lane, uint32_t* buf) {
+    uint32_t top = 0, nonfinite = 0;
+#pragma unroll 8
+    for (int e = lane; e < ra.E; e += 32) {
+        const float z = finish_logit_v(__ldcg(ra.logits + (int64_t)row * ra.E + e), ra.bias != nullptr,
+                                       ra.bias ? __ldg(ra.bias + e) : 0.0f);
+        nonfinite += !isfinite(z);
+        const uint32_t key = order_key(z);
+        buf[e] = key;
+        top = max(top, key);
+    }
+    uint2* cand = reinterpret_cast<uint2*>(buf + ((ra.E + 1) & ~1));
+    bool alive = true;
+    uint32_t bound = 0;
+    for (int got = 0; got < ra.k;) {   // k <= 32 lanes
+        bound = __reduce_max_sync(0xffffffffu, alive ? top : 0u);
+        const bool mine = alive && top == bound;
+        got += __popc(__ballot_sync(0xffffffffu, mine));
+        alive = alive && !mine;
+    }
+    __syncwarp();
+    int count = 0;
+    for (int e0 = 0; e0 < ra.E; e0 += 32) {
+        const int e = e0 + lane;
+        const uint32_t key = e < ra.E ? buf[e] : 0u;
+        const bool in = e < ra.E && key >= bound;
+        const uint32_t b = __ballot_sync(0xffffffffu, in);
+        const int at = count + __popc(b & ((1u << lane) - 1));
+        if (in && at < 32) cand[at] = make_uint2(key, (uint32_t)e);
+        count += __popc(b);
+    }
+    if (count > 32) {
+        topk_slow(ra, row, lane);
+        return;
+    }
+    __syncwarp();
+    const uint2 mine = cand[lane < count ? lane : 0];
+    int rank = 0;
+    for (int h = 0; h < count; ++h) {
+        const uint2 o = cand[h];
+        rank += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+    }
+    if (lane < count) cand[32 + rank] = mine;
+    __syncwarp();
+    const uint2 my = lane < ra.k ? cand[32 + lane] : make_uint2(0, 0);
+    write_topk(ra.topk_idx + (int64_t)row * ra.k, ra.topk_w + (int64_t)row * ra.k, ra.k, lane, my.y, my.x);
+    nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
+    if (lane == 0) status_add(ra.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
+}
 
 // x into shared memory: as it is, or as e4m3 codes and scales per block of 128 (fp8.cuh).
 template <bool FP8>
@@ -277,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, c = lane & 3;
     const int G = gridDim.x, cta = blockIdx.x;
     const uint64_t limit = a.wait_ns ? a.wait_ns : kWaitLimitNs;
-    uint64_t goal1 = 0, goal2 = 0;   // thread 0's
-    if (tid == 0) {   // this CTA's own arrivals are missing, so neither can have passed its multiple
-        goal1 = (ld_counter(a.counters) / G + 1) * G;
-        goal2 = (ld_counter(a.counters + 1) / G + 1) * G;
+    uint32_t round1 = 0, round2 = 0;   // thread 0's
+    if (tid == 0) {   // this CTA's own arrivals are missing: neither round can have ended
+        round1 = ld_round(a.counters);
+        round2 = ld_round(a.counters + 1);
     }
     const uint8_t *wg = static_cast<const uint8_t*>(a.wg), *wu = static_cast<const uint8_t*>(a.wu),
                   *wd = static_cast<const uint8_t*>(a.wd), *sg = static_cast<const uint8_t*>(a.sg),
@@ -302,15 +350,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         }
         for (int t = cta; t < dtiles; t += G) prefetch_l2(sd + (int64_t)t * db, db);
     }
-    if (!a.given)   // the last warps: the first ones stage x meanwhile
-        for (int e = cta + G * (kWarps - 1 - warp); e < a.E; e += G * kWarps) expert_logits(a, e, lane);
+    if (!a.given) {   // the last warps first: the first ones stage x meanwhile
+        const int tasks = ((a.E - cta + G - 1) / G) * a.R;
+        for (int i = kWarps - 1 - warp; i < tasks; i += kWarps) expert_logit(a, cta + i / a.R * G, i % a.R, lane);
+    }
     stage_x<FP8>(a, sx);
     for (int i = tid; i < a.E; i += kThreads) s.mask[i] = 0;
     if (tid < kMaxExperts / 32) s.used[tid] = 0;
     if (tid < MOE_STATUS_WORDS) s.scratch[tid] = 0;
     if (a.given) {
         __syncthreads();
-    } else if (!grid_barrier(a.counters, goal1, limit, &s.ok)) {
+    } else if (!grid_barrier(a.counters, round1, limit, &s.ok)) {
         if (tid == 0) {
             status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
             arrive(a.counters + 1);   // the barrier that this CTA will not reach
@@ -332,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             ra.topk_idx = s.idx;
             ra.topk_w = s.w;
             ra.status = cta == 0 ? a.status : s.scratch;
-            token_topk(ra, warp, lane);
+            topk_row(ra, warp, lane, reinterpret_cast<uint32_t*>(sx + a.arena) + warp * (((a.E + 1) & ~1) + 128));   // the ring is idle
             __syncwarp();
             if (lane < a.k) {
                 my_e = s.idx[warp * a.k + lane];
@@ -404,11 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     const uint32_t all = (1u << a.R) - 1;
     // the lane's slots of the tiles in flight, taken in turn
     const int depth = a.depth;
-    const uint32_t ring = smem_u32(sx) + a.arena + warp * (depth * kStage) + lane * 16;
-    const uint32_t ring_end = ring + depth * kStage;
+    const uint32_t ring = smem_u32(sx) + a.arena + warp * (depth * kStage<FP8>) + lane * 16;
+    const uint32_t ring_end = ring + depth * kStage<FP8>;
+    const int scale_at = 2048 - 12 * lane;   // from a lane's slot to its copy of the scale
     uint32_t fill = ring, take = ring;
     auto next_slot = [&](uint32_t at) {
-        at += kStage;
+        at += kStage<FP8>;
         return at == ring_end ? ring : at;
     };
     {
@@ -438,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                     lv = (l < 0 ? su : wu) + o;
                 }
                 const int k = lk < tiles ? lk : 0;
-                copy_tile<FP8>(fill, lg + k * 128, lv + k * 128, c, lk < tiles ? 128 : 0);
+                copy_tile(fill, lg + k * 128, lv + k * 128, c, lk < tiles ? 128 : 0);
                 lk += kGroup;
                 if (lk >= kend) {
                     lk = gw;
@@ -474,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 wait_tile(depth);
                 const uint4 z = make_uint4(0, 0, 0, 0);
                 const bool in = gi < a.R && kt < tiles;
-                const uint4 x[2] = {in ? lds16(xrow + kt * 128 + tile_at<FP8>(c, 0)) : z,
-                                    in ? lds16(xrow + kt * 128 + tile_at<FP8>(c, 1)) : z};
+                const uint4 x[2] = {in ? lds16(xrow + kt * 128 + tile_at(c, 0)) : z,
+                                    in ? lds16(xrow + kt * 128 + tile_at(c, 1)) : z};
                 const uint4 ta[2] = {lds16(take), lds16(take + 512)}, tb[2] = {lds16(take + 1024), lds16(take + 1536)};
                 if (FP8) {
                     float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -562,7 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             const int K = sh ? a.Is : a.I;
             const int64_t e = sh ? 0 : s.list[ld.l];
             const uint8_t* w = (sh ? sd : wd) + ((e * a.H + 16 * ld.t + gi) * K + ld.kb * kTK) * kES;
-            copy_tile<FP8>(fill, w, w + (int64_t)8 * K * kES, c, (K - ld.kb * kTK) * kES);
+            copy_tile(fill, w, w + (int64_t)8 * K * kES, c, (K - ld.kb * kTK) * kES);
+            if (FP8)   // 16 outputs lie in one block of 128
+                copy4(fill + scale_at, (sh ? a.csd : a.cd) + (e * (a.H / kFp8Block) + (ld.t >> 3)) * (sh ? kb_s : kb_r) + ld.kb);
         }
         cp_async_commit();
         fill = next_slot(fill);
@@ -579,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             prefetch_l2(wd + ((int64_t)s.list[i % nl] * a.H + 16 * (cta + i / nl * G)) * a.I * kES, db);
     }
 
-    if (!grid_barrier(a.counters + (a.given ? 0 : 1), a.given ? goal1 : goal2, limit, &s.ok)) {
+    if (!grid_barrier(a.counters + (a.given ? 0 : 1), a.given ? round1 : round2, limit, &s.ok)) {
         cp_async_wait<0>();
         if (tid == 0) status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
         return;
@@ -644,13 +697,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             const int K = sh ? a.Is : a.I;
             bool on = q.t < dtiles && q.it < items;
             if (on) on = ((sh ? all : (uint32_t)s.lmask[q.l]) >> gi) & 1u;
-            if (FP8) on = on && q.kb * kTK + 32 * c < K;   // K % 64 == 0: all of the 32 values or none
             const int64_t at = on ? (int64_t)(sh ? gi : gi * a.k + s.slot[q.l][gi]) * K + q.kb * kTK : 0;
             const uint4 z = make_uint4(0, 0, 0, 0);
             if constexpr (FP8) {
-                const float* src = hf + (sh ? hpart : 0) + at + 32 * c;
+                const float* src = hf + (sh ? hpart : 0) + at + 16 * c;
 #pragma unroll
-                for (int i = 0; i < kHN; ++i) v[i] = on ? __ldcg(reinterpret_cast<const uint4*>(src) + i) : z;
+                for (int i = 0; i < kHN; ++i)   // K % 64 == 0: of 64 values all or none
+                    v[i] = on && q.kb * kTK + 64 * (i >> 2) < K
+                         ? __ldcg(reinterpret_cast<const uint4*>(src + 64 * (i >> 2)) + (i & 3)) : z;
             } else {
                 const __nv_bfloat16* src = hb + (sh ? hpart : 0) + at + 8 * c;
 #pragma unroll
@@ -660,19 +714,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 }
             }
         };
-        auto scale_of = [&](const Item& q) {   // 16 outputs lie in one block of 128
-            if (!FP8 || q.t >= dtiles || q.it >= items) return 0.0f;
-            const bool sh = q.l < 0;
-            const int64_t e = sh ? 0 : s.list[q.l];
-            return __ldg((sh ? a.csd : a.cd) + (e * (a.H / kFp8Block) + (q.t >> 3)) * (sh ? kb_s : kb_r) + q.kb);
-        };
         Item cur, nxt;
         cur.t = cta;
         first(cur);
         nxt = cur;
         uint4 h[STAGED ? 1 : kHN], hn[STAGED ? 1 : kHN];
         if constexpr (!STAGED) load_h(cur, h);
-        float sw = scale_of(cur);
         int pb = 0;
 #pragma unroll 1
         for (int t = cta; t < dtiles; t += G) {
@@ -682,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 copy_next();
                 advance(nxt);
                 if constexpr (!STAGED) load_h(nxt, hn);
-                const float sw_next = scale_of(nxt);
                 wait_tile(depth);
                 if (it < items) {
                     const bool sh = cur.l < 0;
@@ -698,9 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                         float scale;
                         uint4 x[2];
                         if constexpr (STAGED) {
-                            const bool in = on && cur.kb * kTK + 32 * c < (sh ? a.Is : a.I);
-                            x[0] = in ? lds16(hrow + 32 * c) : z;
-                            x[1] = in ? lds16(hrow + 32 * c + 16) : z;
+                            x[0] = on ? lds16(hrow + 16 * c) : z;
+                            x[1] = on && cur.kb * kTK + 64 < (sh ? a.Is : a.I) ? lds16(hrow + 64 + 16 * c) : z;
                             scale = on ? reinterpret_cast<const float*>(sx + hsc0)[(sh ? np * kb_r + p * kb_s : p * kb_r) + cur.kb] : 0.0f;
                         } else {
                             uint32_t mx = 0;
@@ -722,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                             x[1] = make_uint4(q[4], q[5], q[6], q[7]);
                         }
                         tile_mma<FP8>(d, ta, tb, x);
+                        const float sw = lds4(take + scale_at);
                         f0 *= __shfl_sync(0xffffffffu, scale, 8 * c) * sw;   // row r's scale is in lanes 4 r ..
                         f1 *= __shfl_sync(0xffffffffu, scale, 8 * c + 4) * sw;
                     } else if constexpr (STAGED) {
@@ -744,7 +790,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 }
                 take = next_slot(take);
                 cur = nxt;
-                sw = sw_next;
                 if constexpr (!STAGED) {
 #pragma unroll
                     for (int i = 0; i < kHN; ++i) h[i] = hn[i];
@@ -780,14 +825,14 @@ namespace {
 template <bool FP8>
 void plan_smem(TokenArgs& a, bool* staged, int* bytes) {
     const int64_t x = x_bytes<FP8>(a.H), h = h_bytes<FP8>(a.R, a.k, a.I, a.Is), room = kSmemMax - kSmemHead;
-    *staged = h <= room - 2 * kWarps * kStage;
+    *staged = h <= room - 2 * kWarps * kStage<FP8>;
     a.arena = (int)(*staged && h > x ? h : x);
-    const int64_t d = (room - a.arena) / (kWarps * kStage);
+    const int64_t d = (room - a.arena) / (kWarps * kStage<FP8>);
     a.depth = d < 4 ? (int)d : 4;
-    *bytes = kSmemHead + a.arena + a.depth * kWarps * kStage;
+    *bytes = kSmemHead + a.arena + a.depth * kWarps * kStage<FP8>;
 }
-static_assert(x_bytes<false>(kTokenMaxH) + 2 * kWarps * kStage <= kSmemMax - kSmemHead &&
-              x_bytes<true>(kTokenMaxH) + 2 * kWarps * kStage <= kSmemMax - kSmemHead, "two tiles in flight");
+static_assert(x_bytes<false>(kTokenMaxH) + 2 * kWarps * kStage<false> <= kSmemMax - kSmemHead &&
+              x_bytes<true>(kTokenMaxH) + 2 * kWarps * kStage<false> <= kSmemMax - kSmemHead, "two tiles in flight");
 
 }  // namespace
 

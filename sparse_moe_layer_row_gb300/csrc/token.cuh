@@ -23,7 +23,7 @@ struct TokenArgs {
     int32_t* topk_idx;            // [R, k]
     float* topk_w;
     void* h;                      // 4 bytes for each of R (k I + Is) values
-    uint64_t* counters;           // of the two grid barriers
+    uint32_t* counters;           // of the two grid barriers
     uint32_t* status;
     __nv_bfloat16* y;             // [R, H]
     float* y_f32;                 // or NULL

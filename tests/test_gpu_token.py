@@ -110,7 +110,7 @@ class Case:
 
 
 SHAPES = [dict(), dict(H=512, E=24, k=3, I=192, Is=64), dict(H=1280, E=64, k=6, I=320, Is=640),
-          dict(H=768, E=300, k=8, I=64, Is=64), dict(H=256, E=32, k=32, I=512, Is=1024), dict(H=2560, E=6, k=2, I=4096, Is=2112), dict(H=256, E=1024, k=32, I=64, Is=128), dict(H=256, E=1, k=1, I=64, Is=64)]
+          dict(H=768, E=300, k=8, I=64, Is=64), dict(H=256, E=32, k=32, I=512, Is=1024), dict(H=2560, E=6, k=2, I=4096, Is=2112), dict(H=256, E=1024, k=32, I=64, Is=128), dict(H=256, E=1, k=1, I=64, Is=64), dict(H=256, E=31, k=7, I=128, Is=64)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
@@ -205,6 +205,23 @@ def test_nonfinite_values_stay_in_their_rows(kind):
     z, z32 = c.given()
     hit = (c.idx == e).any(1)
     assert torch.isnan(z32[hit]).all() and torch.equal(z32[~hit], y32[~hit]) and bool((~hit).any())
+
+
+@pytest.mark.parametrize("E,k", [(64, 5), (300, 8), (1000, 32), (40, 32)])
+def test_equal_and_extreme_logits(E, k):
+    """Rows of equal logits (the lowest ids), of a few values, and of infinities: the order and
+    weights of moe_block_route."""
+    c = Case("bf16", 4, E=E, k=k, I=64, Is=64, seed=70)
+    c.router.zero_()
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    biases = [torch.zeros(E, device="cuda"), torch.arange(E, device="cuda").float() % 3,
+              -torch.arange(E, device="cuda").float(), torch.full((E,), float("-inf"), device="cuda"),
+              torch.full((E,), float("nan"), device="cuda"), torch.where(torch.arange(E, device="cuda") % 7 == 0, float("inf"), 0.0)]
+    for bias in biases:
+        y, y32, idx, wt = c.routed(bias)
+        ri, rw = c.layer.route(c.x, off, bias[None])
+        torch.cuda.synchronize()
+        assert torch.equal(idx, ri) and torch.equal(wt.view(torch.int32), rw.view(torch.int32))
 
 
 def test_nonfinite_logits_are_counted_once():
