@@ -54,21 +54,24 @@ constexpr int64_t kPrefetchBytes = 32 << 20;    // of the down weights, a quarte
 // A tile: 16 weight rows by 128 bytes of K; a lane holds 32 bytes of two rows.
 template <bool FP8>
 constexpr int kTileK = FP8 ? 128 : 64;
-// Shared memory of a tile in flight, per warp: each lane's 4 x 16 bytes, and a scale (down, e4m3)
-template <bool FP8>
-constexpr int kStage = 2048 + (FP8 ? 128 : 0);
+constexpr int kStage = 2048;   // shared memory of a tile in flight, per warp: each lane's 4 x 16 bytes
 
 struct Smem {
-    float part[2][kWarps][kTokenRows][17];      // partial sums (row, weight row)
-    float wt[kMaxPairs][kTokenRows];            // weight of (listed expert, row)
-    uint32_t mask[kMaxExperts];                 // rows of an expert
-    uint32_t used[kMaxExperts / 32];            // experts touched, a bit each
-    int32_t list[kMaxPairs];                    // experts touched, ascending
-    uint8_t lmask[kMaxPairs];                   // their rows
+    union {
+        float part[2][kWarps][kTokenRows][17];  // partial sums (row, weight row)
+        struct {                                // before the list is made:
+            uint32_t mask[kMaxExperts];         // rows of an expert
+            int32_t idx[kMaxPairs];             // [R, k]
+            float w[kMaxPairs];
+        };
+    };
+    float wt[kMaxPairs + 1][kTokenRows];        // weight of (listed expert, row); last the shared expert
+    uint16_t hrow[kMaxPairs + 1][kTokenRows];   // staged h of (listed expert, row): 64 bytes from its start
     uint8_t slot[kMaxPairs][kTokenRows];        // first slot of (listed expert, row)
+    int32_t list[kMaxPairs + 1];                // experts touched, ascending; then the shared one: 0
+    uint8_t lmask[kMaxPairs + 1];               // their rows
+    uint32_t used[kMaxExperts / 32];            // experts touched, a bit each
     uint32_t scratch[MOE_STATUS_WORDS];         // for status counts that another CTA makes
-    int32_t idx[kMaxPairs];                     // [R, k]
-    float w[kMaxPairs];
     int ok;
 };
 
@@ -83,16 +86,31 @@ __host__ __device__ constexpr int x_bytes(int H) {   // a multiple of 128: H % 2
 }
 constexpr int kSmemHead = (int)(sizeof(Smem) + 127) / 128 * 128;
 constexpr int kSmemMax = 227 * 1024;
-static_assert(kTokenRows * 4 * (kMaxExperts + 128) <= 2 * kWarps * 2048, "keys and candidates fit the ring");
-// h in x's place: routed pairs (row r k + slot), then the shared expert's; bf16: its hi, then its
-// lo parts; e4m3: codes, then the scales per block of 128
+static_assert(kTokenRows * 4 * (kMaxExperts + 96) <= 2 * kWarps * 2048, "keys and candidates fit the ring");
+// h in x's place: a row of zeros, routed pairs (row r k + slot), then the shared expert's; bf16: its
+// hi, then its lo parts; e4m3: codes, then their scales per block of 128, then a turn's scales of W
 template <bool FP8>
 __host__ __device__ constexpr int h_stride(int I) { return odd64(FP8 ? I : 2 * I); }
+struct HPlan {
+    int rstr, sstr, routed, shared, scales, wscales;   // strides and offsets in bytes
+    int64_t bytes;
+};
 template <bool FP8>
-__host__ __device__ inline int64_t h_bytes(int R, int k, int I, int Is) {
-    int64_t n = (int64_t)R * k * h_stride<FP8>(I) + (int64_t)R * (FP8 ? 1 : 2) * h_stride<FP8>(Is);
-    if (FP8) n += 4 * (int64_t)R * (k * fp8_blocks(I) + fp8_blocks(Is));
-    return (n + 127) / 128 * 128;
+__host__ __device__ inline HPlan h_plan(int R, int k, int I, int Is) {
+    HPlan p{};
+    p.rstr = h_stride<FP8>(I);
+    p.sstr = h_stride<FP8>(Is);
+    p.routed = p.rstr > p.sstr ? p.rstr : p.sstr;
+    const int64_t shared = p.routed + (int64_t)R * k * p.rstr, scales = shared + (int64_t)R * (FP8 ? 1 : 2) * p.sstr;
+    const int64_t tiles = (int64_t)R * k * fp8_blocks(I) + fp8_blocks(Is);
+    const int64_t wscales = scales + (FP8 ? 4 * ((int64_t)R * k * fp8_blocks(I) + R * fp8_blocks(Is)) : 0);
+    p.bytes = (wscales + (FP8 ? 4 * tiles : 0) + 127) / 128 * 128;
+    if (p.bytes < kSmemMax) {
+        p.shared = (int)shared;
+        p.scales = (int)scales;
+        p.wscales = (int)wscales;
+    }
+    return p;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
@@ -110,17 +128,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ float lds4(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-// All but the newest depth - 1 of this thread's copy groups are complete.
+// All but the newest depth - 1 of this thread's copy groups are complete (depth 2 .. 5).
 __device__ __forceinline__ void wait_tile(int depth) {
-    if (depth == 4) cp_async_wait<3>();
+    if (depth == 5) cp_async_wait<4>();
+    else if (depth == 4) cp_async_wait<3>();
     else if (depth == 3) cp_async_wait<2>();
     else cp_async_wait<1>();
 }
@@ -142,18 +153,19 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A lane's part of a tile, rows gi (a) and gi + 8 (b): 16 of each 64 bytes, so that four
-// lanes read 64 in a row.
-__device__ __forceinline__ int tile_at(int c, int i) { return 64 * i + 16 * c; }
-// From pa and pb (the rows at the tile's start) to the lane's slots; `left`: bytes of K from
-// there to the end, zeros past it.
-__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* pa, const uint8_t* pb, int c, int left) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = tile_at(c, i);
-        const int n = at < left ? 16 : 0, from = at < left ? at : 0;
-        copy16(dst + 512 * i, pa + from, n);
-        copy16(dst + 1024 + 512 * i, pb + from, n);
+// A lane's part of a tile, rows gi (a) and gi + 8 (b): bytes 16 c .. and 64 + 16 c .., so that
+// four lanes read 64 in a row.
+// From pa and pb (its first bytes of either row) to the lane's slots; `half`: K ends after 64
+// bytes, zeros there.
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* pa, const uint8_t* pb, bool half) {
+    cp_async16(dst, pa);
+    cp_async16(dst + 1024, pb);
+    if (half) {
+        copy16(dst + 512, pa, 0);
+        copy16(dst + 1536, pb, 0);
+    } else {
+        cp_async16(dst + 512, pa + 64);
+        cp_async16(dst + 1536, pb + 64);
     }
 }
 // d += tile . x, the tile in the lane's slots
@@ -228,10 +240,24 @@ __device__ __forceinline__ void expert_logit(const TokenArgs& a, int e, int r, i
 // Rows with many equal logits: the top-k of route_common.cuh.  Not inlined: rarely called code.
 __device__ __noinline__ void topk_slow(const RouteArgs& ra, int row, int lane) { route_topk(ra, row, row + 1, lane); }
 
+// How many of the 32 keys at `keys` come before this lane's: larger ones, and equal ones in lower lanes.
+__device__ __forceinline__ int rank_of(const uint32_t* keys, uint32_t mine, int lane) {
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 o = *reinterpret_cast<const uint4*>(keys + 4 * i);
+        rank += (o.x > mine || (o.x == mine && 4 * i < lane)) + (o.y > mine || (o.y == mine && 4 * i + 1 < lane)) +
+                (o.z > mine || (o.z == mine && 4 * i + 2 < lane)) + (o.w > mine || (o.w == mine && 4 * i + 3 < lane));
+    }
+    return rank;
+}
+
 // Top-k of one row and the weights, one warp: what route_topk writes, in fewer steps and less code.
 // The k-th largest of the lanes' own largest keys is a lower bound of the k-th largest key; few keys
-// reach it, and their ranks among each other are counted.  buf: E keys, then 2 x 32 (key, id).
+// reach it, and their ranks among each other are counted.  buf: 96 words, then E keys.
+constexpr int kTopkWords = 96;
 __device__ __forceinline__ void topk_row(const RouteArgs& ra, int row, int lane, uint32_t* buf) {
+    uint32_t* keys = buf + kTopkWords;
     uint32_t top = 0, nonfinite = 0;
 #pragma unroll 8
     for (int e = lane; e < ra.E; e += 32) {
@@ -239,44 +265,48 @@ __device__ __forceinline__ void topk_row(const RouteArgs& ra, int row, int lane,
                                        ra.bias ? __ldg(ra.bias + e) : 0.0f);
         nonfinite += !isfinite(z);
         const uint32_t key = order_key(z);
-        buf[e] = key;
+        keys[e] = key;
         top = max(top, key);
     }
-    uint2* cand = reinterpret_cast<uint2*>(buf + ((ra.E + 1) & ~1));
-    bool alive = true;
-    uint32_t bound = 0;
-    for (int got = 0; got < ra.k;) {   // k <= 32 lanes
-        bound = __reduce_max_sync(0xffffffffu, alive ? top : 0u);
-        const bool mine = alive && top == bound;
-        got += __popc(__ballot_sync(0xffffffffu, mine));
-        alive = alive && !mine;
-    }
+    buf[lane] = top;
+    buf[32 + lane] = 0;   // candidates' keys
     __syncwarp();
+    const uint32_t kth = __ballot_sync(0xffffffffu, rank_of(buf, top, lane) == ra.k - 1);
+    const uint32_t bound = __shfl_sync(0xffffffffu, top, __ffs(kth) - 1);
     int count = 0;
-    for (int e0 = 0; e0 < ra.E; e0 += 32) {
-        const int e = e0 + lane;
-        const uint32_t key = e < ra.E ? buf[e] : 0u;
-        const bool in = e < ra.E && key >= bound;
-        const uint32_t b = __ballot_sync(0xffffffffu, in);
-        const int at = count + __popc(b & ((1u << lane) - 1));
-        if (in && at < 32) cand[at] = make_uint2(key, (uint32_t)e);
-        count += __popc(b);
+    for (int e0 = 0; e0 < ra.E; e0 += 128) {   // in ascending order of the experts
+        uint32_t key[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) key[i] = e0 + 32 * i + lane < ra.E ? keys[e0 + 32 * i + lane] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = e0 + 32 * i + lane;
+            const bool in = e < ra.E && key[i] >= bound;
+            const uint32_t b = __ballot_sync(0xffffffffu, in);
+            const int at = count + __popc(b & ((1u << lane) - 1));
+            if (in && at < 32) {
+                buf[32 + at] = key[i];
+                buf[64 + at] = (uint32_t)e;
+            }
+            count += __popc(b);
+        }
     }
     if (count > 32) {
         topk_slow(ra, row, lane);
         return;
     }
     __syncwarp();
-    const uint2 mine = cand[lane < count ? lane : 0];
-    int rank = 0;
-    for (int h = 0; h < count; ++h) {
-        const uint2 o = cand[h];
-        rank += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
-    }
-    if (lane < count) cand[32 + rank] = mine;
+    const uint32_t key = buf[32 + lane], id = buf[64 + lane];
+    const int rank = rank_of(buf + 32, key, lane);
     __syncwarp();
-    const uint2 my = lane < ra.k ? cand[32 + lane] : make_uint2(0, 0);
-    write_topk(ra.topk_idx + (int64_t)row * ra.k, ra.topk_w + (int64_t)row * ra.k, ra.k, lane, my.y, my.x);
+    if (lane < count) {
+        buf[rank] = key;
+        buf[64 + rank] = id;   // each lane has read its own
+    }
+    __syncwarp();
+    const bool on = lane < ra.k;
+    write_topk(ra.topk_idx + (int64_t)row * ra.k, ra.topk_w + (int64_t)row * ra.k, ra.k, lane, on ? buf[64 + lane] : 0u,
+               on ? buf[lane] : 0u);
     nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
     if (lane == 0) status_add(ra.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
 }
@@ -356,6 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     }
     stage_x<FP8>(a, sx);
     for (int i = tid; i < a.E; i += kThreads) s.mask[i] = 0;
+    const HPlan hp = h_plan<FP8>(a.R, a.k, a.I, a.Is);
+    if (STAGED)   // rows that did not choose an expert multiply zeros
+        for (int i = tid; i < (kMaxPairs + 1) * kTokenRows; i += kThreads) (&s.hrow[0][0])[i] = 0;
     if (tid < kMaxExperts / 32) s.used[tid] = 0;
     if (tid < MOE_STATUS_WORDS) s.scratch[tid] = 0;
     if (a.given) {
@@ -382,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             ra.topk_idx = s.idx;
             ra.topk_w = s.w;
             ra.status = cta == 0 ? a.status : s.scratch;
-            topk_row(ra, warp, lane, reinterpret_cast<uint32_t*>(sx + a.arena) + warp * (((a.E + 1) & ~1) + 128));   // the ring is idle
+            topk_row(ra, warp, lane, reinterpret_cast<uint32_t*>(sx + a.arena) + warp * (((a.E + 3) & ~3) + kTopkWords));   // the ring is idle
             __syncwarp();
             if (lane < a.k) {
                 my_e = s.idx[warp * a.k + lane];
@@ -444,30 +477,91 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         if (my_e >= 0 && lane == __ffs(same) - 1) {
             s.wt[l][warp] = my_w;
             s.slot[l][warp] = (uint8_t)lane;
+            s.hrow[l][warp] = (uint16_t)((hp.routed + (warp * a.k + lane) * hp.rstr) / 64);
         }
     }
+    if (tid < kTokenRows) {   // the shared expert follows
+        s.wt[nl][tid] = 1.0f;
+        s.hrow[nl][tid] = tid < a.R ? (uint16_t)((hp.shared + tid * hp.sstr) / 64) : 0;
+        s.list[nl] = 0;
+        s.lmask[nl] = (uint8_t)((1u << a.R) - 1);
+    }
     __syncthreads();
+    // The down step's tiles follow gate/up's without a gap: turn by turn 16 hidden outputs; the
+    // tiles of all experts (the shared one's first) go round the warps.
+    // the lane's slots of the tiles in flight, taken in turn
+    const int depth = a.depth;
+    const uint32_t ring = smem_u32(sx) + a.arena + warp * (depth * kStage) + lane * 16;
+    const uint32_t ring_end = ring + depth * kStage;
+    uint32_t fill = ring, take = ring;
+    auto next_slot = [&](uint32_t at) {
+        at += kStage;
+        return at == ring_end ? ring : at;
+    };
+    const int kb_r = (a.I + kTK - 1) / kTK, kb_s = (a.Is + kTK - 1) / kTK;   // tiles of an expert's K
+    const int nr = nl * kb_r, items = nr + kb_s;
+    const int iend = (items + kWarps - 1) / kWarps * kWarps;   // alike for all warps: nothing past the end
+    const int dl = kWarps / kb_r, dk = kWarps - dl * kb_r, l0 = warp / kb_r;
+    struct Item { int it, l, kb; };   // tile; its expert in the list and place in K
+    auto settle = [&](Item& q) {      // tiles past the routed experts' are the shared one's
+        if (q.it >= nr) {
+            q.l = nl;
+            q.kb = q.it - nr;
+        }
+    };
+    auto first = [&](Item& q) {
+        q.it = warp;
+        q.l = l0;
+        q.kb = warp - l0 * kb_r;
+        settle(q);
+    };
+    auto advance = [&](Item& q) {
+        q.it += kWarps;
+        q.l += dl;
+        q.kb += dk;
+        if (q.kb >= kb_r) {
+            q.kb -= kb_r;
+            ++q.l;
+        }
+        settle(q);
+    };
+    // the next tile to copy, and the lane's first bytes of the turn's rows of expert 0 and of the shared one
+    Item ld;
+    first(ld);
+    int lt = cta;
+    const uint8_t *ldr = wd + (16 * (int64_t)lt + gi) * a.I * kES + 16 * c,
+                  *lds = sd + (16 * (int64_t)lt + gi) * a.Is * kES + 16 * c;
+    const uint32_t estride = (uint32_t)a.H * a.I * kES, turn_r = 16u * G * a.I * kES, turn_s = 16u * G * a.Is * kES;
+    auto copy_down = [&]() {   // without the commit
+        if (lt >= dtiles) return;
+        if (ld.it < items) {
+            const bool sh = ld.l == nl;
+            const uint8_t* w = sh ? lds : ldr + (uint64_t)(uint32_t)s.list[ld.l] * estride;
+            w += ld.kb * 128;
+            const int K = sh ? a.Is : a.I;
+            copy_tile(fill, w, w + 8 * K * kES, FP8 && K - ld.kb * 128 < 128);
+        }
+        if (ld.it + kWarps < iend) {
+            advance(ld);
+        } else {
+            first(ld);
+            lt += G;
+            ldr += turn_r;
+            lds += turn_s;
+        }
+    };
     // ---- gate/up: units of 8 intermediate indices, the shared expert's first
     __nv_bfloat16* hb = static_cast<__nv_bfloat16*>(a.h);   // bf16: routed, then the shared expert's hi and lo parts
     float* hf = static_cast<float*>(a.h);                   // e4m3: fp32
     const int64_t hpart = (int64_t)np * a.I, spart = (int64_t)a.R * a.Is;
     const uint32_t all = (1u << a.R) - 1;
-    // the lane's slots of the tiles in flight, taken in turn
-    const int depth = a.depth;
-    const uint32_t ring = smem_u32(sx) + a.arena + warp * (depth * kStage<FP8>) + lane * 16;
-    const uint32_t ring_end = ring + depth * kStage<FP8>;
-    const int scale_at = 2048 - 12 * lane;   // from a lane's slot to its copy of the scale
-    uint32_t fill = ring, take = ring;
-    auto next_slot = [&](uint32_t at) {
-        at += kStage<FP8>;
-        return at == ring_end ? ring : at;
-    };
     {
         const int group = warp / kGroup, gw = warp % kGroup;
         const int nunits = stiles + nl * utiles, ustep = G * kGroups;
         const int tiles = a.H / kTK;                        // of which this warp takes gw, gw + 4, ...
-        const int kend = (tiles + kGroup - 1) / kGroup * kGroup;   // alike for all warps: zeros past the end
+        const int kend = (tiles + kGroup - 1) / kGroup * kGroup + gw;   // as many steps in every warp: none past the end
         int lu = cta + G * group, lk = gw;   // the next tile to copy
+        bool prefetched = false;
         const uint8_t *lg = wg, *lv = wu;
         // unit u: its expert (list index; shared: -1) and its tile there
         auto unit = [&](int u, int& ti) {
@@ -484,17 +578,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 if (lk == gw) {   // a new unit
                     int ti;
                     const int l = unit(lu, ti);
-                    const int64_t o = ((l < 0 ? 0 : (int64_t)s.list[l] * a.I) + 8 * ti + gi) * a.H * kES;
+                    const int64_t o = ((l < 0 ? 0 : (int64_t)s.list[l] * a.I) + 8 * ti + gi) * a.H * kES + gw * 128 + 16 * c;
                     lg = (l < 0 ? sg : wg) + o;
                     lv = (l < 0 ? su : wu) + o;
                 }
-                const int k = lk < tiles ? lk : 0;
-                copy_tile(fill, lg + k * 128, lv + k * 128, c, lk < tiles ? 128 : 0);
+                if (lk < tiles) copy_tile(fill, lg, lv, false);
+                lg += kGroup * 128;
+                lv += kGroup * 128;
                 lk += kGroup;
                 if (lk >= kend) {
                     lk = gw;
                     lu += ustep;
                 }
+            } else {
+                // then, once, the rest of this CTA's first turns' weights to L2
+                if (warp == kWarps - 1 && !prefetched) {
+                    prefetched = true;
+                    const uint32_t db = 16u * a.I * kES;
+                    const int most = (int)(kPrefetchBytes / G / db), mine = (dtiles - cta + G - 1) / G * nl;
+#pragma unroll 1
+                    for (int i = lane; i < min(most, mine); i += 32)
+                        prefetch_l2(wd + ((int64_t)s.list[i % nl] * a.H + 16 * (cta + i / nl * G)) * a.I * kES, db);
+                }
+                copy_down();
             }
             cp_async_commit();
             fill = next_slot(fill);
@@ -512,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         float sc_next = scales_of(lu);
 #pragma unroll 1
         for (int i = 0; i < depth - 1; ++i) copy_next();
-        const uint32_t xrow = smem_u32(sx) + gi * x_stride<FP8>(a.H);
+        const uint32_t xrow = smem_u32(sx) + gi * x_stride<FP8>(a.H) + 16 * c;
+        const bool on = gi < a.R;
         int pb = 0;
 #pragma unroll 1
         for (int u = cta + G * group; u < nunits; u += ustep) {
@@ -523,24 +630,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             for (int kt = gw; kt < kend; kt += kGroup) {
                 copy_next();
                 wait_tile(depth);
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                const bool in = gi < a.R && kt < tiles;
-                const uint4 x[2] = {in ? lds16(xrow + kt * 128 + tile_at(c, 0)) : z,
-                                    in ? lds16(xrow + kt * 128 + tile_at(c, 1)) : z};
-                const uint4 ta[2] = {lds16(take), lds16(take + 512)}, tb[2] = {lds16(take + 1024), lds16(take + 1536)};
-                if (FP8) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    tile_mma<FP8>(d, ta, tb, x);
-                    const float fa = __shfl_sync(0xffffffffu, sc, kt / kGroup), fb = __shfl_sync(0xffffffffu, sc, 16 + kt / kGroup);
-                    const int kc = kt < tiles ? kt : 0;
-                    const float x0 = 2 * c < a.R ? xs[kc * kTokenRows + 2 * c] : 0.0f;
-                    const float x1 = 2 * c + 1 < a.R ? xs[kc * kTokenRows + 2 * c + 1] : 0.0f;
-                    acc[0] = fmaf(x0 * fa, d[0], acc[0]);
-                    acc[1] = fmaf(x1 * fa, d[1], acc[1]);
-                    acc[2] = fmaf(x0 * fb, d[2], acc[2]);
-                    acc[3] = fmaf(x1 * fb, d[3], acc[3]);
-                } else {
-                    tile_mma<FP8>(acc, ta, tb, x);
+                if (kt < tiles) {
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    const uint4 x[2] = {on ? lds16(xrow + kt * 128) : z, on ? lds16(xrow + kt * 128 + 64) : z};
+                    const uint4 ta[2] = {lds16(take), lds16(take + 512)}, tb[2] = {lds16(take + 1024), lds16(take + 1536)};
+                    if (FP8) {
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        tile_mma<FP8>(d, ta, tb, x);
+                        const float fa = __shfl_sync(0xffffffffu, sc, kt / kGroup), fb = __shfl_sync(0xffffffffu, sc, 16 + kt / kGroup);
+                        // (scales of rows past R are left over: their columns are not read)
+                        const float2 f = *reinterpret_cast<const float2*>(xs + kt * kTokenRows + 2 * c);
+                        acc[0] = fmaf(f.x * fa, d[0], acc[0]);
+                        acc[1] = fmaf(f.y * fa, d[1], acc[1]);
+                        acc[2] = fmaf(f.x * fb, d[2], acc[2]);
+                        acc[3] = fmaf(f.y * fb, d[3], acc[3]);
+                    } else {
+                        tile_mma<FP8>(acc, ta, tb, x);
+                    }
                 }
                 take = next_slot(take);
             }
@@ -576,62 +682,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         }
     }
 
-    // ---- step 3: down.  Turn by turn 16 hidden outputs; the tiles of all experts (the shared
-    // one's first) go round the warps.  The first tiles are on their way before the barrier.
-    const int kb_r = (a.I + kTK - 1) / kTK, kb_s = (a.Is + kTK - 1) / kTK;   // tiles of an expert's K
-    const int items = kb_s + nl * kb_r;
-    const int iend = (items + kWarps - 1) / kWarps * kWarps;   // alike for all warps: nothing past the end
-    struct Item { int t, it, l, kb; };   // turn's outputs, tile; its expert (-1: shared) and place in K
-    auto first = [&](Item& q) {
-        q.it = warp;
-        q.l = -1;
-        q.kb = warp;
-        while (q.kb >= (q.l < 0 ? kb_s : kb_r)) {
-            q.kb -= q.l < 0 ? kb_s : kb_r;
-            ++q.l;
-        }
+    // ---- step 3: down
+    // e4m3: the scale of W for a tile: 16 outputs lie in one block of 128
+    auto scale_of = [&](int t, int l, int kb) {
+        return __ldg(l == nl ? a.csd + (int64_t)(t >> 3) * kb_s + kb
+                             : a.cd + ((int64_t)s.list[l] * (a.H / kFp8Block) + (t >> 3)) * kb_r + kb);
     };
-    auto advance = [&](Item& q) {
-        q.it += kWarps;
-        if (q.it >= iend) {
-            q.t += G;
-            first(q);
-        } else {
-            q.kb += kWarps;
-            while (q.kb >= (q.l < 0 ? kb_s : kb_r)) {
-                q.kb -= q.l < 0 ? kb_s : kb_r;
-                ++q.l;
-            }
-        }
+    auto scale_at = [&](int t, int it) {
+        const int l = it < nr ? it / kb_r : nl;
+        return scale_of(t, l, it < nr ? it - l * kb_r : it - nr);
     };
-    Item ld;
-    ld.t = cta;
-    first(ld);
-    auto copy_next = [&]() {
-        if (ld.t < dtiles && ld.it < items) {
-            const bool sh = ld.l < 0;
-            const int K = sh ? a.Is : a.I;
-            const int64_t e = sh ? 0 : s.list[ld.l];
-            const uint8_t* w = (sh ? sd : wd) + ((e * a.H + 16 * ld.t + gi) * K + ld.kb * kTK) * kES;
-            copy_tile(fill, w, w + (int64_t)8 * K * kES, c, (K - ld.kb * kTK) * kES);
-            if (FP8)   // 16 outputs lie in one block of 128
-                copy4(fill + scale_at, (sh ? a.csd : a.cd) + (e * (a.H / kFp8Block) + (ld.t >> 3)) * (sh ? kb_s : kb_r) + ld.kb);
-        }
-        cp_async_commit();
-        fill = next_slot(fill);
-        advance(ld);
-    };
-    fill = take;   // every tile of gate/up has been taken
-#pragma unroll 1
-    for (int i = 0; i < depth - 1; ++i) copy_next();
-    // the rest of this CTA's first turns' weights, to L2 meanwhile
-    if (warp == kWarps - 1) {
-        const uint32_t db = 16u * a.I * kES;
-        const int most = (int)(kPrefetchBytes / G / db), mine = (dtiles - cta + G - 1) / G * nl;
-        for (int i = lane; i < min(most, mine); i += 32)
-            prefetch_l2(wd + ((int64_t)s.list[i % nl] * a.H + 16 * (cta + i / nl * G)) * a.I * kES, db);
-    }
-
+    float* wsc = reinterpret_cast<float*>(sx + hp.wscales);
+    const bool early = FP8 && STAGED && cta < dtiles && tid < items;   // the first turn's are loaded before the barrier
+    const float first_sc = early ? scale_at(cta, tid) : 0.0f;
     if (!grid_barrier(a.counters + (a.given ? 0 : 1), a.given ? round1 : round2, limit, &s.ok)) {
         cp_async_wait<0>();
         if (tid == 0) status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
@@ -641,20 +704,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         cp_async_wait<0>();
         return;
     }
-    // h, staged: offsets of the shared expert's part and of the scales
-    const int rstr = h_stride<FP8>(a.I), sstr = h_stride<FP8>(a.Is);
-    const int hs0 = np * rstr, hsc0 = hs0 + a.R * (FP8 ? 1 : 2) * sstr;
     if constexpr (STAGED) {
-        if constexpr (FP8) {   // a warp per row, two blocks at a time
-            float* hsc = reinterpret_cast<float*>(sx + hsc0);
+        for (int i = tid; i < hp.routed / 16; i += kThreads) *reinterpret_cast<uint4*>(sx + 16 * i) = make_uint4(0, 0, 0, 0);
+        if constexpr (FP8) {   // a warp per row, half of it per block
+            float* hsc = reinterpret_cast<float*>(sx + hp.scales);
             for (int p = warp; p < np + a.R; p += kWarps) {
                 const bool sh = p >= np;
                 const int K = sh ? a.Is : a.I, nb = sh ? kb_s : kb_r;
                 const float* src = hf + (sh ? hpart + (int64_t)(p - np) * K : (int64_t)p * K);
-                uint8_t* dst = sx + (sh ? hs0 + (p - np) * sstr : p * rstr);
+                uint8_t* dst = sx + (sh ? hp.shared + (p - np) * hp.sstr : hp.routed + p * hp.rstr);
                 float* sc = hsc + (sh ? np * kb_r + (p - np) * kb_s : p * kb_r);
 #pragma unroll 2
-                for (int b0 = 0; b0 < nb; b0 += 2) {   // half a warp per block
+                for (int b0 = 0; b0 < nb; b0 += 2) {
                     const int k = 128 * b0 + 8 * lane;
                     float v[8];
 #pragma unroll
@@ -681,22 +742,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 const bool sh = p >= np;
                 const int K = sh ? a.Is : a.I;
                 const __nv_bfloat16* src = hb + (sh ? hpart + (int64_t)(p - np) * K : (int64_t)p * K);
-                const uint32_t dst = smem_u32(sx) + (sh ? hs0 + (p - np) * sstr : p * rstr);
-                for (int k = 8 * lane; k < K; k += 256) copy16(dst + 2 * k, src + k, 16);
+                const uint32_t dst = smem_u32(sx) + (sh ? hp.shared + (p - np) * hp.sstr : hp.routed + p * hp.rstr);
+                for (int k = 8 * lane; k < K; k += 256) cp_async16(dst + 2 * k, src + k);
             }
             cp_async_commit();
             cp_async_wait<0>();
         }
-        __syncthreads();
     }
     {
         constexpr int kHN = FP8 ? 8 : 4;   // not staged: 16-byte pieces of h per lane and tile (bf16: hi, lo)
         // what the lane multiplies of tile q: row gi's part; zeros where the row did not choose the expert
         auto load_h = [&](const Item& q, uint4 (&v)[kHN]) {
-            const bool sh = q.l < 0;
+            const bool sh = q.l == nl, on = q.it < items && ((s.lmask[q.l] >> gi) & 1u);
             const int K = sh ? a.Is : a.I;
-            bool on = q.t < dtiles && q.it < items;
-            if (on) on = ((sh ? all : (uint32_t)s.lmask[q.l]) >> gi) & 1u;
             const int64_t at = on ? (int64_t)(sh ? gi : gi * a.k + s.slot[q.l][gi]) * K + q.kb * kTK : 0;
             const uint4 z = make_uint4(0, 0, 0, 0);
             if constexpr (FP8) {
@@ -714,79 +772,84 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                 }
             }
         };
-        Item cur, nxt;
-        cur.t = cta;
-        first(cur);
-        nxt = cur;
+        const uint32_t hbase = smem_u32(sx) + 16 * c;
         uint4 h[STAGED ? 1 : kHN], hn[STAGED ? 1 : kHN];
-        if constexpr (!STAGED) load_h(cur, h);
         int pb = 0;
 #pragma unroll 1
         for (int t = cta; t < dtiles; t += G) {
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            Item cur;
+            first(cur);
+            if constexpr (STAGED) {
+                if (FP8) {
+                    if (t == cta && early) wsc[tid] = first_sc;
+                    for (int it = tid + (t == cta ? kThreads : 0); it < items; it += kThreads) wsc[it] = scale_at(t, it);
+                }
+                __syncthreads();   // h and the scales are there
+            } else {
+                load_h(cur, h);
+            }
 #pragma unroll 1
-            for (int it = warp; it < iend; it += kWarps) {
-                copy_next();
+            for (; cur.it < iend; ) {
+                copy_down();
+                cp_async_commit();
+                fill = next_slot(fill);
+                Item nxt = cur;
                 advance(nxt);
                 if constexpr (!STAGED) load_h(nxt, hn);
                 wait_tile(depth);
-                if (it < items) {
-                    const bool sh = cur.l < 0;
-                    const uint32_t m = sh ? all : s.lmask[cur.l];
-                    const uint4 z = make_uint4(0, 0, 0, 0);
+                if (cur.it < items) {
+                    const bool sh = cur.l == nl;
                     float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    float f0 = sh ? 1.0f : s.wt[cur.l][2 * c], f1 = sh ? 1.0f : s.wt[cur.l][2 * c + 1];
+                    const uint32_t m = (uint32_t)s.lmask[cur.l] >> (2 * c);
+                    float2 f = *reinterpret_cast<const float2*>(&s.wt[cur.l][2 * c]);
                     const uint4 ta[2] = {lds16(take), lds16(take + 512)}, tb[2] = {lds16(take + 1024), lds16(take + 1536)};
-                    const bool on = (m >> gi) & 1u;
-                    const int p = sh ? gi : gi * a.k + (on ? s.slot[cur.l][gi] : 0);
-                    const uint32_t hrow = smem_u32(sx) + (sh ? hs0 + p * sstr : p * rstr) + cur.kb * 128;
-                    if constexpr (FP8) {
-                        float scale;
-                        uint4 x[2];
-                        if constexpr (STAGED) {
-                            x[0] = on ? lds16(hrow + 16 * c) : z;
-                            x[1] = on && cur.kb * kTK + 64 < (sh ? a.Is : a.I) ? lds16(hrow + 64 + 16 * c) : z;
-                            scale = on ? reinterpret_cast<const float*>(sx + hsc0)[(sh ? np * kb_r + p * kb_s : p * kb_r) + cur.kb] : 0.0f;
-                        } else {
-                            uint32_t mx = 0;
-#pragma unroll
-                            for (int i = 0; i < kHN; ++i)
-                                mx = max(mx, max(max(h[i].x & 0x7FFFFFFFu, h[i].y & 0x7FFFFFFFu),
-                                                 max(h[i].z & 0x7FFFFFFFu, h[i].w & 0x7FFFFFFFu)));
-                            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                            const float bm = __uint_as_float(fp8_amax_bits(mx));
-                            const float inv = __fdiv_rn(448.0f, bm);
-                            scale = __fdiv_rn(bm, 448.0f);
-                            uint32_t q[8];
-#pragma unroll
-                            for (int i = 0; i < kHN; ++i)
-                                q[i] = fp8_pair(__uint_as_float(h[i].x) * inv, __uint_as_float(h[i].y) * inv) |
-                                       fp8_pair(__uint_as_float(h[i].z) * inv, __uint_as_float(h[i].w) * inv) << 16;
-                            x[0] = make_uint4(q[0], q[1], q[2], q[3]);
-                            x[1] = make_uint4(q[4], q[5], q[6], q[7]);
-                        }
+                    if constexpr (STAGED) {
+                        const int at = 64 * s.hrow[cur.l][gi];
+                        const uint32_t hr = hbase + at + cur.kb * 128;
+                        const uint4 x[2] = {lds16(hr), FP8 && (sh ? a.Is : a.I) - cur.kb * 128 < 128 ? make_uint4(0, 0, 0, 0) : lds16(hr + 64)};
                         tile_mma<FP8>(d, ta, tb, x);
-                        const float sw = lds4(take + scale_at);
-                        f0 *= __shfl_sync(0xffffffffu, scale, 8 * c) * sw;   // row r's scale is in lanes 4 r ..
-                        f1 *= __shfl_sync(0xffffffffu, scale, 8 * c + 4) * sw;
-                    } else if constexpr (STAGED) {
-                        const uint32_t at = hrow + 16 * c;
-                        const uint4 xh[2] = {on ? lds16(at) : z, on ? lds16(at + 64) : z};
-                        tile_mma<FP8>(d, ta, tb, xh);
-                        if (sh) {   // the lo part
-                            const uint32_t lo = at + a.R * sstr;
-                            const uint4 xl[2] = {on ? lds16(lo) : z, on ? lds16(lo + 64) : z};
+                        if constexpr (FP8) {
+                            // the scales of the lane's two columns (of a row that did not choose the expert: any)
+                            const float* sc = reinterpret_cast<const float*>(sx + hp.scales) + (sh ? np * kb_r : 0) + cur.kb;
+                            const int kbn = sh ? kb_s : kb_r, p0 = sh ? 2 * c : 2 * c * a.k + s.slot[cur.l][2 * c];
+                            const int p1 = sh ? 2 * c + 1 : (2 * c + 1) * a.k + s.slot[cur.l][2 * c + 1];
+                            const float sw = wsc[cur.it];
+                            if (m & 1u) f.x *= sc[p0 * kbn] * sw;
+                            if (m & 2u) f.y *= sc[p1 * kbn] * sw;
+                        } else if (sh) {   // the lo part
+                            const uint32_t lo = hr + (at ? a.R * hp.sstr : 0);
+                            const uint4 xl[2] = {lds16(lo), lds16(lo + 64)};
                             tile_mma<FP8>(d, ta, tb, xl);
                         }
+                    } else if constexpr (FP8) {
+                        uint32_t mx = 0;
+#pragma unroll
+                        for (int i = 0; i < kHN; ++i)
+                            mx = max(mx, max(max(h[i].x & 0x7FFFFFFFu, h[i].y & 0x7FFFFFFFu),
+                                             max(h[i].z & 0x7FFFFFFFu, h[i].w & 0x7FFFFFFFu)));
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float bm = __uint_as_float(fp8_amax_bits(mx));
+                        const float inv = __fdiv_rn(448.0f, bm), scale = __fdiv_rn(bm, 448.0f);
+                        uint32_t q[8];
+#pragma unroll
+                        for (int i = 0; i < kHN; ++i)
+                            q[i] = fp8_pair(__uint_as_float(h[i].x) * inv, __uint_as_float(h[i].y) * inv) |
+                                   fp8_pair(__uint_as_float(h[i].z) * inv, __uint_as_float(h[i].w) * inv) << 16;
+                        const uint4 x[2] = {make_uint4(q[0], q[1], q[2], q[3]), make_uint4(q[4], q[5], q[6], q[7])};
+                        tile_mma<FP8>(d, ta, tb, x);
+                        const float sw = scale_of(t, cur.l, cur.kb);
+                        f.x *= __shfl_sync(0xffffffffu, scale, 8 * c) * sw;   // row r's scale is in lanes 4 r ..
+                        f.y *= __shfl_sync(0xffffffffu, scale, 8 * c + 4) * sw;
                     } else {
                         const uint4 xh[2] = {h[0], h[1]}, xl[2] = {h[2], h[3]};
                         tile_mma<FP8>(d, ta, tb, xh);
                         if (sh) tile_mma<FP8>(d, ta, tb, xl);
                     }
                     // columns of rows that did not choose the expert stay out (its weights may not be finite)
-                    if ((m >> (2 * c)) & 1u) { acc[0] = fmaf(f0, d[0], acc[0]); acc[2] = fmaf(f0, d[2], acc[2]); }
-                    if ((m >> (2 * c + 1)) & 1u) { acc[1] = fmaf(f1, d[1], acc[1]); acc[3] = fmaf(f1, d[3], acc[3]); }
+                    if (m & 1u) { acc[0] = fmaf(f.x, d[0], acc[0]); acc[2] = fmaf(f.x, d[2], acc[2]); }
+                    if (m & 2u) { acc[1] = fmaf(f.y, d[1], acc[1]); acc[3] = fmaf(f.y, d[3], acc[3]); }
                 }
                 take = next_slot(take);
                 cur = nxt;
@@ -812,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
                     if (n == 0) status_add(a.status, MOE_STATUS_NONFINITE_OUTPUT, ((nf >> (lane & 16)) & 0xFFFFu) != 0);
                 }
             }
-            pb ^= 1;   // written again behind the next turn's barrier: read by then
+            pb ^= 1;   // written again behind the next turn's barriers: read by then
         }
         cp_async_wait<0>();
     }
@@ -820,19 +883,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
 
 namespace {
 
-// Where x or h lie, and how many tiles are in flight: four where both fit beside them, else
-// three or two; h is staged where two do.
+// Where x or h lie, and how many tiles are in flight: up to five, what fits beside them; h is
+// staged where two do.
 template <bool FP8>
 void plan_smem(TokenArgs& a, bool* staged, int* bytes) {
-    const int64_t x = x_bytes<FP8>(a.H), h = h_bytes<FP8>(a.R, a.k, a.I, a.Is), room = kSmemMax - kSmemHead;
-    *staged = h <= room - 2 * kWarps * kStage<FP8>;
+    const int64_t x = x_bytes<FP8>(a.H), h = h_plan<FP8>(a.R, a.k, a.I, a.Is).bytes, room = kSmemMax - kSmemHead;
+    *staged = h <= room - 2 * kWarps * kStage;
     a.arena = (int)(*staged && h > x ? h : x);
-    const int64_t d = (room - a.arena) / (kWarps * kStage<FP8>);
-    a.depth = d < 4 ? (int)d : 4;
-    *bytes = kSmemHead + a.arena + a.depth * kWarps * kStage<FP8>;
+    const int64_t d = (room - a.arena) / (kWarps * kStage);
+    a.depth = d < 5 ? (int)d : 5;
+    *bytes = kSmemHead + a.arena + a.depth * kWarps * kStage;
 }
-static_assert(x_bytes<false>(kTokenMaxH) + 2 * kWarps * kStage<false> <= kSmemMax - kSmemHead &&
-              x_bytes<true>(kTokenMaxH) + 2 * kWarps * kStage<false> <= kSmemMax - kSmemHead, "two tiles in flight");
+static_assert(x_bytes<false>(kTokenMaxH) + 2 * kWarps * kStage <= kSmemMax - kSmemHead &&
+              x_bytes<true>(kTokenMaxH) + 2 * kWarps * kStage <= kSmemMax - kSmemHead, "two tiles in flight");
 
 }  // namespace
 
