@@ -21,7 +21,7 @@ SOURCES = ["api.cu", "router.cu", "router_tc.cu", "coreset.cu", "scatter.cu",
            "fp8_rows.cu", "fp8_decode.cu", "rows8.cu", "i8_gemm.cu",
            "token.cu"]
 HEADERS = ["common.cuh", "kernels.cuh", "route_common.cuh", "coreset_dev.cuh", "scatter_dev.cuh",
-           "route_scored.cuh", "fp8.cuh", "rows8.cuh", "token.cuh"]
+           "route_scored.cuh", "fp8.cuh", "rows8.cuh", "token.cuh", "pair.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]

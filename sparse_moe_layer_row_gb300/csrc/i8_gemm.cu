@@ -5,6 +5,28 @@
 // rows its N, the sums int32 and exact.  Operands go from global memory to registers, two
 // blocks at a time; K is permuted inside a block, alike in both operands, so that a lane's
 // are 16-byte loads.  The warps' sums are added through shared memory.
+//
+// k_i8_tiles: the tensor core of sm_103a has no fast path for int8.  Codes are exact in fp16,
+// their products and sums below 2^24 exact in fp32, so that kind::f16 computes the sum of whole
+// numbers, at the bf16 rate.  A CTA pair (cta_group::2) takes 256 outputs by up to 256 rows:
+//   A (M = 256)  W, 128 outputs per CTA: raw codes by TMA (8 KB per 64 of K), which the converter
+//                warps turn into fp16 in tensor memory, from where the MMA reads A
+//   B (N <= 256) x in fp16, half of the rows per CTA, by TMA.  k_i8_widen writes it to the
+//                workspace first: every output tile needs it, and converting it there would
+//                double the shared-memory traffic of the loop
+// so that W is read as bytes and never written, and an SM's shared memory carries 48 KB per 64 of
+// K (512 clocks of the tensor core).  Tensor memory holds the accumulators (256 columns) and eight A
+// slots of 32, one per stage.  Roles, 512 threads per CTA:
+//   warp 0 lane 0   TMA producer, ring of 8 stages (W on `wfull`, x on `xfull`)
+//   warp 1          tensor memory; lane 0 of rank 0 issues the MMAs and commits (`empty`
+//                   of both ranks: the stage and its A slot; `tfull`)
+//   warp 2 lane 0   forwarder: the CTA's x of a stage has landed -> rank 0's `ready`
+//   warps 4..7      converters: a row of 64 codes per thread -> rank 0's `ready`
+//   warps 8..15     epilogue: 32 outputs (a lane each) by 128 rows of x per warp.  They take the
+//                   accumulators into registers at once (`tempty` of rank 0), so that the next
+//                   tile's MMAs run while they scale and store
+// Every wait is bounded, and drains follow an abort, as in gemm_pair.cu.
+#include "pair.cuh"
 #include "rows8.cuh"
 
 namespace moe {
@@ -97,6 +119,384 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
         store_one(a.y, (int64_t)(r0 + r) * a.ldy + n0 + n, a.ydtype,
                   (float)v * (__ldg(a.xs + r0 + r) * __ldg(a.ws + n0 + n)));
     }
+}
+
+// ------------------------------------------------------------------------ tiles
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
+constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
+constexpr int kStages = 8, kThreads = 512;
+constexpr int kRaw = 128 * 64, kXTile = 128 * 128;   // bytes per stage: codes of W, fp16 of x
+constexpr int kStageBytes = kRaw + kXTile;
+constexpr int kXOff = kStages * kRaw;                // x tiles behind the codes (1 KB boundaries)
+constexpr int kScaleOff = kStages * kStageBytes;     // float [8][128]: xs of an epilogue warp's rows
+constexpr int kBarOff = kScaleOff + 8 * 128 * 4;
+constexpr int kSmem = kBarOff + 512 + 1024;
+constexpr int kACol = 256;                           // A slots behind the accumulators
+constexpr int kTmemCols = 512;
+static_assert(kACol + 32 * kStages <= kTmemCols, "TMEM columns");
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(8 * (4 * kStages + 3) + 12 <= 512, "barrier region");
+// registers per thread after the split; the pool is what the CTA was launched with (checked on
+// the host)
+constexpr int kLaunchRegs = 128, kFewRegs = 56, kManyRegs = 200;
+static_assert(256 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
+
+// kind::f16 with fp16 A (in tensor memory) and B, fp32 accumulator, both K-major.
+__device__ __forceinline__ void mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Four codes (two's complement, in byte order) -> two words of two fp16: the byte q + 128 is the
+// low byte of fp16 1024 + q + 128, exact; minus 1152 gives q.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+}  // namespace
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+// One output of n (at most 128) rows from row r on: a warp stores 32 outputs of a row at a time.
+template <typename T>
+__device__ __forceinline__ void store_rows(const I8GemmArgs& a, const float (&v)[128], const float* xs, float ws, int r,
+                                           int n, int out) {
+    T* p = static_cast<T*>(a.y) + (int64_t)r * a.ldy + out;
+#pragma unroll
+    for (int c = 0; c < 128; ++c) {
+        if (c < n) *p = rounded<T>(v[c] * (xs[c] * ws));
+        p += a.ldy;
+    }
+}
+
+}  // namespace
+
+// x codes to fp16, 16 per thread and turn.
+__global__ void __launch_bounds__(256) k_i8_widen(const int8_t* q, __half* x, int64_t n16) {
+    pdl_wait();  // see common.cuh: nothing global is touched before
+    pdl_trigger();
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n16; i += gridDim.x * 256ll) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        uint4 a, b;
+        widen4(v.x, a.x, a.y);
+        widen4(v.y, a.z, a.w);
+        widen4(v.z, b.x, b.y);
+        widen4(v.w, b.z, b.w);
+        reinterpret_cast<uint4*>(x)[2 * i] = a;
+        reinterpret_cast<uint4*>(x)[2 * i + 1] = b;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8GemmArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;   // same offset in both CTAs
+    uint8_t* base = smem_raw + (sbase - raw);
+    uint64_t* wfull = reinterpret_cast<uint64_t*>(base + kBarOff);   // [S] codes landed
+    uint64_t* xfull = wfull + kStages;                                // [S] x landed
+    uint64_t* ready = xfull + kStages;                                // [S] both ranks' x and A (rank 0)
+    uint64_t* empty = ready + kStages;                                // [S] stage and A slot free (both)
+    uint64_t* tfull = empty + kStages;                                // accumulators ready (both)
+    uint64_t* tempty = tfull + 1;                                     // accumulators free (rank 0)
+    uint64_t* dbar = tempty + 1;                                      // MMA drain (rank 0)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dbar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* never = abort_flag + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(wfull + s, 1);
+            mbar_init(xfull + s, 1);
+            mbar_init(ready + s, 2 * (1 + 4));   // of each rank: the forwarder, four converter warps
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 2 * 8);   // the epilogue warps of both ranks
+        mbar_init(dbar, 1);
+        *abort_flag = 0;
+        *never = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
+    tc_fence_before();
+    cluster_sync();   // barriers of both CTAs initialised, TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();   // see common.cuh
+    pdl_trigger();
+
+    // unit u: outputs 256 m .., rows 256 c .. (neighbouring units share rows of x)
+    const int mt = (a.N + 255) / 256, nunits = mt * ((a.R + 255) / 256);
+    const int nact = active_workers(nunits, (int)cluster_count());   // balanced rounds
+    const int ufirst = (int)cluster_id() < nact ? (int)cluster_id() : nunits;
+    const int nkb = (a.K + 63) / 64;
+    auto rows_of = [&](int u, int& m, int& r0) {   // the MMA's N: rows of the unit, in 32s
+        const int c = u / mt;
+        m = u - c * mt;
+        r0 = c * 256;
+        return (min(256, a.R - r0) + 31) / 32 * 32;
+    };
+    auto give_up = [&]() {
+        if (!*abort_flag) { *abort_flag = 1; status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1); }
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------------ TMA producer
+            int stage = 0, nfills = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact) {
+                int m, r0;
+                const int n = rows_of(u, m, r0);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitLimitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(wfull + stage, kRaw);
+                    tma_load_2d(sbase + stage * kRaw, &tmW, kb * 64, m * 256 + 128 * rank, wfull + stage);
+                    mbar_expect_tx(xfull + stage, kXTile);
+                    tma_load_2d(sbase + kXOff + stage * kXTile, &tmX, kb * 64, r0 + n / 2 * rank, xfull + stage);
+                    ++nfills;
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // drain: the last fill of every stage has landed (consumed or not)
+            for (int s = 0; s < kStages; ++s) {
+                if (nfills < kStages && s >= nfills) break;
+                const uint32_t par = s < stage ? phase : (phase ^ 1u);
+                if (!mbar_wait_bounded(wfull + s, par, never, kDrainLimitNs) ||
+                    !mbar_wait_bounded(xfull + s, par, never, kDrainLimitNs)) give_up();
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // -------------------------------------------------------------- MMA issuer
+            int stage = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact) {
+                int m, r0;
+                const int n = rows_of(u, m, r0);
+                const uint32_t idesc = 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(256 >> 4) << 24;   // fp16 A and B
+                if (!mbar_wait_cluster_bounded(tempty, tphase ^ 1u, abort_flag, kWaitLimitNs)) {
+                    give_up();
+                    break;
+                }
+                tphase ^= 1u;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_cluster_bounded(ready + stage, phase, abort_flag, kWaitLimitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t bd = smem_desc_sw128(sbase + kXOff + stage * kXTile);
+                    const uint32_t at = tmem + (uint32_t)(kACol + 32 * stage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
+                        mma_f16_pair_ta(tmem, at + 8 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                    tc_commit_pair(empty + stage);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+                if (ok) tc_commit_pair(tfull);
+            }
+            // drain: arrives once every MMA issued above has completed
+            tc_commit_pair_local(dbar);
+            if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs)) give_up();
+        } else if (warp == 2 && lane == 0) {
+            // --------------------------------------------------------------- forwarder
+            const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = ufirst; ok && u < nunits; u += nact)
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_bounded(xfull + stage, phase, abort_flag, kWaitLimitNs)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_cluster(ready0 + stage * 8);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+        }
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        // -------------------------------------------------------------- converters
+        // Output r of the CTA's 128 per thread: 64 codes of its row (chunk c of 16 at
+        // c ^ ((r >> 1) & 3), the copy's 64-byte swizzle) into lane r of the stage's A slot.
+        const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
+        const int r = 32 * (warp & 3) + lane, sw = (r >> 1) & 3;
+        const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)kACol;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = ufirst; ok && u < nunits; u += nact)
+            for (int kb = 0; kb < nkb; ++kb) {
+                // codes landed; they were only asked for once the MMA had read the slot
+                const bool got = mbar_wait_bounded(wfull + stage, phase, abort_flag, kWaitLimitNs);
+                if (__any_sync(0xffffffffu, !got)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint8_t* row = base + stage * kRaw + r * 64;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(row + (((2 * h + i) ^ sw) << 4));
+                        widen4(w.x, o[8 * i], o[8 * i + 1]);
+                        widen4(w.y, o[8 * i + 2], o[8 * i + 3]);
+                        widen4(w.z, o[8 * i + 4], o[8 * i + 5]);
+                        widen4(w.w, o[8 * i + 6], o[8 * i + 7]);
+                    }
+                    tmem_st16(tq + (uint32_t)(32 * stage + 16 * h), o);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(ready0 + stage * 8);
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        // ---------------------------------------------------------------- epilogue
+        const int q = warp & 3, half = (warp - 8) >> 2;   // lane quadrant; rows 128 half ..
+        const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(128 * half);
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        float* xs = reinterpret_cast<float*>(base + kScaleOff) + 128 * (warp - 8);
+        uint32_t tphase = 0;
+        for (int u = ufirst; u < nunits; u += nact) {
+            int m, r0;
+            rows_of(u, m, r0);
+            const int out = m * 256 + 128 * rank + 32 * q + lane;   // this lane's output
+            const float ws = out < a.N ? __ldg(a.ws + out) : 0.0f;
+            __syncwarp();   // the last tile's scales have been read
+#pragma unroll
+            for (int i = lane; i < 128; i += 32) {
+                const int r = r0 + 128 * half + i;
+                xs[i] = r < a.R ? __ldg(a.xs + r) : 0.0f;
+            }
+            __syncwarp();
+            const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitLimitNs);
+            if (__any_sync(0xffffffffu, !got)) { give_up(); break; }
+            tphase ^= 1u;
+            tc_fence_after();
+            const int n = min(128, a.R - r0 - 128 * half);   // rows of this warp
+            float v[128];
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                float lo[16], hi[16];
+                tmem_ld16x2(tq + c, tq + c + 16, lo, hi);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[c + i] = lo[i];
+                    v[c + 16 + i] = hi[i];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0);
+            if (out < a.N) {
+                if (a.ydtype == MOE_F32) store_rows<float>(a, v, xs, ws, r0 + 128 * half, n, out);
+                else if (a.ydtype == MOE_BF16) store_rows<__nv_bfloat16>(a, v, xs, ws, r0 + 128 * half, n, out);
+                else store_rows<__half>(a, v, xs, ws, r0 + 128 * half, n, out);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+namespace {
+cudaLaunchConfig_t tiles_config(cudaLaunchAttribute (&attr)[2], int clusters, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+}  // namespace
+
+// Also the clusters that are resident at once on the current device.
+cudaError_t i8_tiles_set_attributes(int num_sms, int* clusters) {
+    cudaError_t e = cudaFuncSetAttribute(k_i8_tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    // the register split draws on what the CTA is launched with
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, k_i8_tiles)) != cudaSuccess) return e;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = tiles_config(attr, num_sms / 2, nullptr);
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, k_i8_tiles, &cfg)) != cudaSuccess) return e;
+    if (n <= 0) return cudaErrorInvalidConfiguration;
+    *clusters = n < num_sms / 2 ? n : num_sms / 2;
+    return cudaSuccess;
+}
+
+cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& w, const CUtensorMap& x, void* x16, int num_sms,
+                            int clusters, cudaStream_t st) {
+    const int64_t n16 = (int64_t)a.R * a.K / 16;
+    int64_t blocks = (n16 + 255) / 256;
+    if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
+    cudaError_t e = launch_kernel(k_i8_widen, dim3((unsigned)blocks), dim3(256), 0, st, a.xq, static_cast<__half*>(x16), n16);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = tiles_config(attr, clusters, st);
+    return cudaLaunchKernelEx(&cfg, k_i8_tiles, w, x, a);
+}
+
+bool i8_rows_applies(int R, int N, int K) {
+    (void)N;
+    (void)K;
+    return R <= kRowsPerCta;
 }
 
 cudaError_t launch_i8_rows(const I8GemmArgs& a, cudaStream_t st) {

@@ -59,6 +59,20 @@ moe_status device_ready(bool gemm, int* sms) {
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
 }
 
+// CTA pairs of k_i8_tiles that are resident at once on the current device, looked up once per
+// device, with the kernel's attributes.
+std::atomic<int> g_pairs[kMaxDevices];
+
+moe_status pairs_ready(int sms, int* clusters) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);   // device_ready has checked its range
+    if (e == cudaSuccess && !(*clusters = g_pairs[dev].load(std::memory_order_acquire))) {
+        e = i8_tiles_set_attributes(sms, clusters);
+        if (e == cudaSuccess) g_pairs[dev].store(*clusters, std::memory_order_release);
+    }
+    return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+}
+
 moe_status launched(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return set_error(MOE_OK, "");
@@ -213,7 +227,7 @@ size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K) {
         fail(MOE_ERR_INVALID_ARG, "R=%d, N=%d, K=%d: R >= 0, N >= 1, K a positive multiple of 16 below 2^17", R, N, K);
         return 0;
     }
-    return kGemmWorkspace;
+    return kGemmWorkspace + (i8_rows_applies(R, N, K) ? 0 : 2 * (size_t)R * (size_t)K);
 }
 
 moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_t* wq,
@@ -235,8 +249,15 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
         return fail(MOE_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype};
-    return launched(launch_i8_rows(a, reinterpret_cast<cudaStream_t>(stream)), "gemm launch");
+    I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype, static_cast<uint32_t*>(workspace)};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (i8_rows_applies(R, N, K)) return launched(launch_i8_rows(a, st), "gemm launch");
+    int sms = 0, clusters = 0;
+    if ((s = device_ready(false, &sms)) != MOE_OK || (s = pairs_ready(sms, &clusters)) != MOE_OK) return s;
+    void* x16 = static_cast<uint8_t*>(workspace) + kGemmWorkspace;
+    CUtensorMap w, x;
+    if (!encode_i8_tiles(&w, &x, wq, x16, R, N, K)) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    return launched(launch_i8_tiles(a, w, x, x16, sms, clusters, st), "gemm launch");
 }
 
 moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int32_t R,
