@@ -250,6 +250,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     }
 }
 
+// One lane of the converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ---- cp.async (16-byte global -> shared copies, L2 only) ----------------------
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

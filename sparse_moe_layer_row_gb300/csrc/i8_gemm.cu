@@ -1,14 +1,18 @@
 // moe_i8_gemm: y[r, n] = xs[r] ws[n] sum_k xq[r, k] wq[n, k] on int8 codes.
 //
-// k_i8_rows: a CTA takes 16 outputs and 32 rows, and its eight warps share K: warp w
-// takes the blocks of 128 w, w + 8, ...  The weights are the M of mma.sync m16n8k32, the
-// rows its N, the sums int32 and exact.  Operands go from global memory to registers, two
-// blocks at a time; K is permuted inside a block, alike in both operands, so that a lane's
-// are 16-byte loads.  The warps' sums are added through shared memory.
+// sm_103a has no fast path for int8 products: mma.sync on int8 takes an SM some 20 clocks for 16 x
+// 8 x 32, which up to 8 rows hide behind the weights' loads.  With more, codes become fp16 in
+// registers (exact, as their products and sums below 2^24 are in fp32), and the sum of whole
+// numbers is the fp16 tensor core's.
 //
-// k_i8_tiles: the tensor core of sm_103a has no fast path for int8.  Codes are exact in fp16,
-// their products and sums below 2^24 exact in fp32, so that kind::f16 computes the sum of whole
-// numbers, at the bf16 rate.  A CTA pair (cta_group::2) takes 256 outputs by up to 256 rows:
+// k_i8_rows: a CTA takes 16 outputs and 32 rows, and its eight warps share K: warp w
+// takes the blocks of 128 w, w + 8, ...  The weights are the M of mma.sync m16n8k16 (up to 8
+// rows: m16n8k32 on int8), the rows its N.  Operands go from global memory to registers, two blocks at a time; K is
+// permuted inside a block, alike in both operands, so that a lane's are 16-byte loads and
+// four codes of a row make one MMA's operand.  The warps' sums are added through shared memory.
+//
+// k_i8_tiles: tcgen05 kind::f16 (the bf16 rate).  A CTA pair (cta_group::2) takes 256 outputs by up
+// to 256 rows:
 //   A (M = 256)  W, 128 outputs per CTA: raw codes by TMA (8 KB per 64 of K), which the converter
 //                warps turn into fp16 in tensor memory, from where the MMA reads A
 //   B (N <= 256) x in fp16, half of the rows per CTA, by TMA.  k_i8_widen writes it to the
@@ -17,7 +21,7 @@
 // so that W is read as bytes and never written, and an SM's shared memory carries 48 KB per 64 of
 // K (512 clocks of the tensor core).  Tensor memory holds the accumulators (256 columns) and eight A
 // slots of 32, one per stage.  Roles, 512 threads per CTA:
-//   warp 0 lane 0   TMA producer, ring of 8 stages (W on `wfull`, x on `xfull`)
+//   warps 0, 3      lane 0: TMA producers of W (`wfull`) and of x (`xfull`), ring of 8 stages
 //   warp 1          tensor memory; lane 0 of rank 0 issues the MMAs and commits (`empty`
 //                   of both ranks: the stage and its A slot; `tfull`)
 //   warp 2 lane 0   forwarder: the CTA's x of a stage has landed -> rank 0's `ready`
@@ -26,6 +30,8 @@
 //                   accumulators into registers at once (`tempty` of rank 0), so that the next
 //                   tile's MMAs run while they scale and store
 // Every wait is bounded, and drains follow an abort, as in gemm_pair.cu.
+#include <type_traits>
+
 #include "pair.cuh"
 #include "rows8.cuh"
 
@@ -44,7 +50,26 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
+// Four codes (two's complement, in byte order) -> two words of two fp16: the byte q + 128 is the
+// low byte of fp16 1024 + q + 128, exact; minus 1152 gives q.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
 __device__ __forceinline__ void store_one(void* y, int64_t i, int dtype, float v) {
     if (dtype == MOE_F32) static_cast<float*>(y)[i] = v;
     else if (dtype == MOE_BF16) static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
@@ -56,9 +81,10 @@ __device__ __forceinline__ void store_one(void* y, int64_t i, int dtype, float v
 // NT tiles of 8 rows per CTA
 template <int NT>
 __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
+    using Acc = std::conditional_t<NT == 1, int, float>;
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
-    __shared__ int part[kWarps][NT * 8][kCols + 1];
+    __shared__ Acc part[kWarps][NT * 8][kCols + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gi = lane >> 2, c = lane & 3;
     const int r0 = blockIdx.y * kRowsPerCta;
@@ -70,7 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
     const int8_t* xr[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) xr[t] = a.xq + (int64_t)min(r0 + 8 * t + gi, a.R - 1) * a.K + 32 * c;
-    int acc[NT][4];
+    Acc acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -95,12 +121,30 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (NT == 1) {
+                    const uint4 x = vx[h][0][i];
+                    mma_s8(acc[0], va[h][i].x, vb[h][i].x, va[h][i].y, vb[h][i].y, x.x, x.y);
+                    mma_s8(acc[0], va[h][i].z, vb[h][i].z, va[h][i].w, vb[h][i].w, x.z, x.w);
+                    continue;
+                } else {
+                const uint32_t wa4[4] = {va[h][i].x, va[h][i].y, va[h][i].z, va[h][i].w};
+                const uint32_t wb4[4] = {vb[h][i].x, vb[h][i].y, vb[h][i].z, vb[h][i].w};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mma_s8(acc[t], va[h][i].x, vb[h][i].x, va[h][i].y, vb[h][i].y, vx[h][t][i].x, vx[h][t][i].y);
-                    mma_s8(acc[t], va[h][i].z, vb[h][i].z, va[h][i].w, vb[h][i].w, vx[h][t][i].z, vx[h][t][i].w);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a0, a1, a2, a3;
+                    widen4(wa4[j], a0, a2);
+                    widen4(wb4[j], a1, a3);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint4 x = vx[h][t][i];
+                        uint32_t b0, b1;
+                        widen4(j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w, b0, b1);
+                        mma_f16(acc[t], a0, a1, a2, a3, b0, b1);
+                    }
                 }
+                }
+            }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {   // D: outputs gi and gi + 8 of rows 2c and 2c + 1
@@ -113,7 +157,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
     for (int i = threadIdx.x; i < NT * 8 * kCols; i += 32 * kWarps) {
         const int r = i / kCols, n = i % kCols;
         if (r0 + r >= a.R || n0 + n >= a.N) continue;
-        int v = part[0][r][n];
+        Acc v = part[0][r][n];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) v += part[w][r][n];
         store_one(a.y, (int64_t)(r0 + r) * a.ldy + n0 + n, a.ydtype,
@@ -153,18 +197,6 @@ __device__ __forceinline__ void mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// Four codes (two's complement, in byte order) -> two words of two fp16: the byte q + 128 is the
-// low byte of fp16 1024 + q + 128, exact; minus 1152 gives q.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 k = __half2half2(__ushort_as_half(0x6480));
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 }  // namespace
@@ -248,8 +280,8 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     cluster_sync();   // barriers of both CTAs initialised, TMEM allocated
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();   // see common.cuh
-    pdl_trigger();
+    // The kernel before this one is k_i8_widen, which let it start after its own wait: all but the
+    // widened x was complete by then, so that only x's producer waits (common.cuh).
 
     // unit u: outputs 256 m .., rows 256 c .. (neighbouring units share rows of x)
     const int mt = (a.N + 255) / 256, nunits = mt * ((a.R + 255) / 256);
@@ -268,8 +300,16 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        if (warp == 0 && lane == 0) {
-            // ------------------------------------------------------------ TMA producer
+        if ((warp == 0 || warp == 3) && lane == 0) {
+            // ----------------------------------------------------------- TMA producers
+            // (a copy takes its thread some 250 clocks to issue: both by one thread made the
+            // 64 of K 560 clocks long, whatever the tile's width)
+            const bool x = warp == 3;
+            if (x) {
+                pdl_wait();
+                pdl_trigger();
+            }
+            uint64_t* full = x ? xfull : wfull;
             int stage = 0, nfills = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -282,10 +322,9 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(wfull + stage, kRaw);
-                    tma_load_2d(sbase + stage * kRaw, &tmW, kb * 64, m * 256 + 128 * rank, wfull + stage);
-                    mbar_expect_tx(xfull + stage, kXTile);
-                    tma_load_2d(sbase + kXOff + stage * kXTile, &tmX, kb * 64, r0 + n / 2 * rank, xfull + stage);
+                    mbar_expect_tx(full + stage, x ? kXTile : kRaw);
+                    if (x) tma_load_2d(sbase + kXOff + stage * kXTile, &tmX, kb * 64, r0 + n / 2 * rank, full + stage);
+                    else tma_load_2d(sbase + stage * kRaw, &tmW, kb * 64, m * 256 + 128 * rank, full + stage);
                     ++nfills;
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -294,43 +333,52 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             for (int s = 0; s < kStages; ++s) {
                 if (nfills < kStages && s >= nfills) break;
                 const uint32_t par = s < stage ? phase : (phase ^ 1u);
-                if (!mbar_wait_bounded(wfull + s, par, never, kDrainLimitNs) ||
-                    !mbar_wait_bounded(xfull + s, par, never, kDrainLimitNs)) give_up();
+                if (!mbar_wait_bounded(full + s, par, never, kDrainLimitNs)) give_up();
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------------- MMA issuer
+            // The whole warp runs the loop, so that its values are uniform, and one elected lane
+            // issues.
+            const bool leader = elect_one();
             int stage = 0;
             uint32_t phase = 0, tphase = 0;
             bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (__all_sync(0xffffffffu, mbar_test_wait_cluster(smem_u32(bar), parity))) return true;
+                const bool got = mbar_wait_cluster_bounded(bar, parity, abort_flag, kWaitLimitNs);
+                if (!__any_sync(0xffffffffu, !got)) return true;
+                if (lane == 0) give_up();
+                return false;
+            };
             for (int u = ufirst; ok && u < nunits; u += nact) {
                 int m, r0;
                 const int n = rows_of(u, m, r0);
                 const uint32_t idesc = 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(256 >> 4) << 24;   // fp16 A and B
-                if (!mbar_wait_cluster_bounded(tempty, tphase ^ 1u, abort_flag, kWaitLimitNs)) {
-                    give_up();
-                    break;
-                }
+                if (!wait(tempty, tphase ^ 1u)) break;
                 tphase ^= 1u;
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_cluster_bounded(ready + stage, phase, abort_flag, kWaitLimitNs)) {
-                        give_up();
+                    if (!wait(ready + stage, phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t bd = smem_desc_sw128(sbase + kXOff + stage * kXTile);
                     const uint32_t at = tmem + (uint32_t)(kACol + 32 * stage);
+                    if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
-                        mma_f16_pair_ta(tmem, at + 8 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
-                    tc_commit_pair(empty + stage);
+                        for (int kk = 0; kk < 4; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
+                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                        tc_commit_pair(empty + stage);
+                        if (kb == nkb - 1) tc_commit_pair(tfull);
+                    }
+                    __syncwarp();
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
-                if (ok) tc_commit_pair(tfull);
             }
             // drain: arrives once every MMA issued above has completed
-            tc_commit_pair_local(dbar);
-            if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs)) give_up();
+            if (leader) tc_commit_pair_local(dbar);
+            __syncwarp();
+            if (!mbar_wait_bounded(dbar, 0, never, kDrainLimitNs) && lane == 0) give_up();
         } else if (warp == 2 && lane == 0) {
             // --------------------------------------------------------------- forwarder
             const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
@@ -485,7 +533,7 @@ cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& w, const CUt
                             int clusters, cudaStream_t st) {
     const int64_t n16 = (int64_t)a.R * a.K / 16;
     int64_t blocks = (n16 + 255) / 256;
-    if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
+    if (blocks > (int64_t)num_sms * 32) blocks = (int64_t)num_sms * 32;
     cudaError_t e = launch_kernel(k_i8_widen, dim3((unsigned)blocks), dim3(256), 0, st, a.xq, static_cast<__half*>(x16), n16);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
@@ -493,10 +541,15 @@ cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& w, const CUt
     return cudaLaunchKernelEx(&cfg, k_i8_tiles, w, x, a);
 }
 
+// By what the two kernels were measured to take (ns): the rows kernel 1800 + CTAs (3.5 + 0.0046 K)
+// with 17 to 32 rows per CTA, the tiles 7800 + 265 per 64 of K and round of units.
 bool i8_rows_applies(int R, int N, int K) {
-    (void)N;
-    (void)K;
-    return R <= kRowsPerCta;
+    if (R <= 16) return true;
+    if (R > 65535 * kRowsPerCta) return false;   // the grid's y: row tiles
+    const int64_t ctas = (int64_t)((N + kCols - 1) / kCols) * ((R + kRowsPerCta - 1) / kRowsPerCta);
+    const int64_t units = (int64_t)((R + 255) / 256) * ((N + 255) / 256);
+    const int64_t rounds = (units + 75) / 76;   // 76 CTA pairs
+    return 1800 + ctas * (35000 + 46 * (int64_t)K) / 10000 <= 7800 + rounds * ((K + 63) / 64) * 265;
 }
 
 cudaError_t launch_i8_rows(const I8GemmArgs& a, cudaStream_t st) {
