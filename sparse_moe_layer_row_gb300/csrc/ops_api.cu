@@ -308,7 +308,7 @@ moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int
     const bool f32 = dtype == MOE_F32;
     RmsNormArgs a{x, x_stride, residual, residual_stride, total, total_stride, weight,
                   !f32 && residual && residual_dtype == MOE_F32, !f32 && weight && weight_dtype == MOE_F32, R, H, eps,
-                  y, y_stride, static_cast<uint8_t*>(codes), scales};
+                  1.0f / (float)H, y, y_stride, static_cast<uint8_t*>(codes), scales};
     const int what = code_type == MOE_CODES_E4M3 ? kNormE4m3 : code_type == MOE_CODES_I8 ? kNormI8 : kNormOnly;
     return launched(launch_rows8(what, a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)), "rmsnorm launch");
 }

@@ -15,8 +15,13 @@
 // of one CTA (one warp for short rows), eight consecutive values per thread and
 // vector, so that a block of 128 is a half-warp's vector; the sum of squares and the
 // row's largest |p| are combined in one exchange.  Rows beyond 32,768 values are read twice.
+// Between a row's loads and its stores lie the exchange and two passes of arithmetic, some
+// 2 us in which a CTA that comes and goes with its row asks memory for nothing: CTAs stay, and
+// load their next row before the exchange of this one.
 // Sums are fp32: 8 NV squares per thread, then a tree.  A row whose sum of squares
 // overflows is scaled by 2^-80 and summed again.
+#include <type_traits>
+
 #include "rows8.cuh"
 
 namespace moe {
@@ -25,55 +30,104 @@ namespace {
 
 constexpr float kTiny = 1.0f / (1 << 20) / (1 << 20) / (1 << 20) / (1 << 20);   // 2^-80
 
+// Two values in 16 bits each.
 template <typename T>
-__device__ __forceinline__ T from_f32(float v);
+__device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+__device__ __forceinline__ uint32_t pack2<float>(float, float) { return 0; }   // never called
 
-// Eight consecutive values: 16-byte accesses, or one at a time up to `n`.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
-    if (VEC) {
-        if (sizeof(T) == 4) {
-            const float4 lo = *reinterpret_cast<const float4*>(p), hi = *(reinterpret_cast<const float4*>(p) + 1);
-            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-            v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-        } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
-        }
+// Eight consecutive values as they lie in memory (16-bit types: lo alone).
+struct Raw8 {
+    uint4 lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Raw8 load_raw(const T* p) {
+    Raw8 r;
+    r.lo = *reinterpret_cast<const uint4*>(p);
+    r.hi = sizeof(T) == 4 ? *(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0, 0, 0, 0);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void values(const Raw8& r, float (&v)[8]) {
+    if (sizeof(T) == 4) {
+        v[0] = __uint_as_float(r.lo.x); v[1] = __uint_as_float(r.lo.y);
+        v[2] = __uint_as_float(r.lo.z); v[3] = __uint_as_float(r.lo.w);
+        v[4] = __uint_as_float(r.hi.x); v[5] = __uint_as_float(r.hi.y);
+        v[6] = __uint_as_float(r.hi.z); v[7] = __uint_as_float(r.hi.w);
     } else {
+        const T* e = reinterpret_cast<const T*>(&r.lo);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
     }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
-    if (VEC) {
-        if (sizeof(T) == 4) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            uint4 w;
-            T* e = reinterpret_cast<T*>(&w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(v[i]);
-            *reinterpret_cast<uint4*>(p) = w;
-        }
+template <typename T>
+__device__ __forceinline__ Raw8 raw_of(const float (&v)[8]) {   // rounded
+    Raw8 r;
+    if (sizeof(T) == 4) {
+        r.lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        r.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = from_f32<T>(v[i]);
+        r.lo = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        r.hi = make_uint4(0, 0, 0, 0);
     }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_raw(T* p, const Raw8& r) {
+    *reinterpret_cast<uint4*>(p) = r.lo;
+    if (sizeof(T) == 4) *(reinterpret_cast<uint4*>(p) + 1) = r.hi;
 }
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The same, one value at a time up to `n`, where addresses or H do not allow 16 bytes.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8 load8(const T* p, int n) {
+    if (VEC) return load_raw(p);
+    Raw8 r{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) e[i] = p[i];
+    return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, int n, const Raw8& r) {
+    if (VEC) {
+        store_raw(p, r);
+        return;
+    }
+    const T* e = reinterpret_cast<const T*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = e[i];
+}
+
+// The largest of |a|, |b| and c >= 0 (a NaN if there is one, whose bits follow infinity's).
+__device__ __forceinline__ float max_magnitude(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float largest(const float (&p)[8], float m) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) m = max_magnitude(p[i], p[i + 1], m);
+    return m;
+}
+
+// a / m, rounded once, by Markstein's correction (fp8.cuh); r: 1 / m rounded
+__device__ __forceinline__ float over(float a, float m, float r) {
+    const float q = a * r;
+    return a < INFINITY ? __fmaf_rn(__fmaf_rn(-q, m, a), r, q) : a;
+}
 
 // int8 codes of eight values whose row's largest magnitude has the bits m.
 __device__ __forceinline__ uint2 i8_codes(const float (&p)[8], uint32_t m) {
@@ -115,171 +169,411 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&p)[8], uint32_t m) {
 }
 
 // The row's sum of squares and largest magnitude over the threads that hold it (`warps`
-// warps: the whole CTA, or one warp of several rows'), the same in each of them.
-__device__ __forceinline__ void combine_row(float& ss, uint32_t& m, int warps) {
-    __shared__ float s_ss[32];
-    __shared__ uint32_t s_m[32];
+// warps: the whole CTA, or one warp of several rows'), the same in each of them.  Two buffers,
+// taken in turn: one is written again behind the barrier of the other.
+struct Exchange {
+    float ss[2][32];
+    uint32_t m[2][32];
+};
+template <bool SS, bool M>
+__device__ __forceinline__ void combine_row(Exchange& x, int& buf, float& ss, uint32_t& m, int warps) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (SS) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (M) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
     if (warps == 1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    __syncthreads();   // an earlier exchange has been read
-    if (lane == 0) { s_ss[warp] = ss; s_m[warp] = m; }
+    if (lane == 0) {
+        if (SS) x.ss[buf][warp] = ss;
+        if (M) x.m[buf][warp] = m;
+    }
     __syncthreads();
-    ss = lane < warps ? s_ss[lane] : 0.0f;
-    m = lane < warps ? s_m[lane] : 0u;
+    if (SS) ss = lane < warps ? x.ss[buf][lane] : 0.0f;
+    if (M) m = lane < warps ? x.m[buf][lane] : 0u;
+    buf ^= 1;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (SS) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (M) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
 }
 
 }  // namespace
 
-// A row per `warps` warps; a CTA has several rows only where that is one.  NV vectors of
-// eight values per thread; ONE: they hold the row, else it is gone through twice.
-template <int WHAT, typename T, bool VEC, int NV, bool ONE>
-__global__ void __launch_bounds__(1024) k_rows8(RmsNormArgs a, int warps) {
+namespace {
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul22(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma22(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// Many rows of at most 8192 values on 16-byte addresses.  RES: no residual, one of x's type, an
+// fp32 one; FULL: the threads' vectors end with the row.  w lies in shared memory, in fp32.
+template <int WHAT, typename T, int RES, bool FULL, int NV>
+__device__ __forceinline__ void rows_many(const RmsNormArgs& a, int warps, const float* s_w, Exchange& s_x) {
+    constexpr bool kNorm = WHAT != kQuantI8, kRowMax = WHAT == kNormI8 || WHAT == kQuantI8;
+    using RT = std::conditional_t<RES == 2, float, T>;
+    int buf = 0;
+    const int lane = threadIdx.x & 31;
+    const int t = warps == 1 ? lane : threadIdx.x;
+    const int step = 256 * warps;
+    const int per_cta = warps == 1 ? blockDim.x >> 5 : 1;
+    const int stride = (int)gridDim.x * per_cta;
+    int row = (int)blockIdx.x * per_cta + (warps == 1 ? threadIdx.x >> 5 : 0);
+    const int c0 = 8 * t;
+    auto inside = [&](int v) { return FULL || c0 + v * step < a.H; };
+    Raw8 nx[NV], nr[RES ? NV : 1];
+    auto load_row = [&](int row) {
+        const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.ldx + c0;
+        const RT* res = static_cast<const RT*>(a.residual) + (int64_t)row * a.ldr + c0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            nx[v].lo = nx[v].hi = make_uint4(0, 0, 0, 0);
+            if (inside(v)) nx[v] = load_raw(x + v * step);
+            if (RES) {
+                nr[v].lo = nr[v].hi = make_uint4(0, 0, 0, 0);
+                if (inside(v)) nr[v] = load_raw(res + v * step);
+            }
+        }
+    };
+    auto pairs = [](const float (&f)[8], float2 (&p)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    };
+    auto singles = [](const float2 (&p)[4], float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = p[i].x;
+            f[2 * i + 1] = p[i].y;
+        }
+    };
+    auto times_w = [&](int v, float2 (&p)[4]) {
+        if (!kNorm) return;
+        const float4 w0 = *reinterpret_cast<const float4*>(s_w + c0 + v * step);
+        const float4 w1 = *reinterpret_cast<const float4*>(s_w + c0 + v * step + 4);
+        p[0] = mul22(p[0], make_float2(w0.x, w0.y));
+        p[1] = mul22(p[1], make_float2(w0.z, w0.w));
+        p[2] = mul22(p[2], make_float2(w1.x, w1.y));
+        p[3] = mul22(p[3], make_float2(w1.z, w1.w));
+    };
+    auto largest4 = [](const float2 (&p)[4], float m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max_magnitude(p[i].x, p[i].y, m);
+        return m;
+    };
+    if (row < a.R) load_row(row);
+    for (; row < a.R; row += stride) {   // the same rows in every thread of a barrier
+        float2 r[NV][4], s2 = make_float2(0.0f, 0.0f);
+        float ss = 0.0f, mf = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float f[8];
+            values<T>(nx[v], f);
+            pairs(f, r[v]);
+            if (RES) {
+                values<RT>(nr[v], f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[v][i] = add2(r[v][i], make_float2(f[2 * i], f[2 * i + 1]));
+                singles(r[v], f);
+                const Raw8 sum = raw_of<RT>(f);
+                if (sizeof(RT) == 2) {
+                    values<RT>(sum, f);
+                    pairs(f, r[v]);
+                }
+                if (a.total && inside(v)) store_raw(static_cast<RT*>(a.total) + (int64_t)row * a.ldt + c0 + v * step, sum);
+            }
+        }
+        if (row + stride < a.R) load_row(row + stride);   // before the exchange
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (kNorm)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = fma22(r[v][i], r[v][i], s2);
+            if (kRowMax) {
+                float2 p[4] = {r[v][0], r[v][1], r[v][2], r[v][3]};
+                if (inside(v)) times_w(v, p);
+                mf = largest4(p, mf);
+            }
+        }
+        ss = s2.x + s2.y;
+        uint32_t m = __float_as_uint(mf);
+        combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
+        const bool huge = kNorm && !(ss < INFINITY);   // as in k_rows8
+        if (huge) {
+            ss = mf = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    r[v][i] = make_float2(r[v][i].x * kTiny, r[v][i].y * kTiny);
+                    ss = fmaf(r[v][i].x, r[v][i].x, fmaf(r[v][i].y, r[v][i].y, ss));
+                }
+                if (kRowMax) {
+                    float2 p[4] = {r[v][0], r[v][1], r[v][2], r[v][3]};
+                    if (inside(v)) times_w(v, p);
+                    mf = largest4(p, mf);
+                }
+            }
+            m = __float_as_uint(mf);
+            combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
+        }
+        const float rstd = kNorm ? rsqrtf(fmaf(ss, a.inv_h, huge ? 0.0f : a.eps)) : 1.0f;
+        if (kRowMax) {
+            m = fp8_amax_bits(m);
+            if (t == 0) a.scales[row] = over(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f, 1.0f / 127.0f);
+        }
+        uint32_t bm[NV];   // e4m3: the blocks' largest magnitudes, their exchanges side by side
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (inside(v)) times_w(v, r[v]);
+            if (WHAT == kNormE4m3) bm[v] = __float_as_uint(largest4(r[v], 0.0f));
+        }
+        if (WHAT == kNormE4m3)
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) bm[v] = max(bm[v], __shfl_xor_sync(0xffffffffu, bm[v], o));
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float p[8];
+            singles(r[v], p);
+            if (WHAT == kNormE4m3) {
+                const uint32_t b = fp8_amax_bits(bm[v]);
+                const uint2 q = e4m3_codes(p, b);
+                if (inside(v)) {
+                    *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.H + c0 + v * step) = q;
+                    if ((lane & 15) == 0)
+                        a.scales[(int64_t)((c0 + v * step) / kFp8Block) * a.R + row] =
+                            over(__uint_as_float(b) * rstd, 448.0f, 1.0f / 448.0f);
+                }
+            }
+            if (kRowMax) {
+                const uint2 q = i8_codes(p, m);
+                if (inside(v)) *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.H + c0 + v * step) = q;
+            }
+            if (kNorm && (WHAT == kNormOnly || a.y) && inside(v)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[v][i] = mul2(r[v][i], rstd);
+                singles(r[v], p);
+                store_raw(static_cast<T*>(a.y) + (int64_t)row * a.ldy + c0 + v * step, raw_of<T>(p));
+            }
+        }
+    }
+}
+
+}  // namespace
+
+template <int WHAT, typename T, int NV, int MINB>
+__global__ void __launch_bounds__(256, MINB) k_rows8_many(RmsNormArgs a, int warps) {
+    pdl_wait();  // see common.cuh: nothing global is touched before
+    pdl_trigger();
+    extern __shared__ __align__(16) float s_w[];
+    __shared__ Exchange s_x;
+    if (WHAT != kQuantI8) {
+        for (int c = 8 * threadIdx.x; c < a.H; c += 8 * blockDim.x) {
+            float f[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+            if (a.w) {
+                if (a.w_f32) values<float>(load_raw(static_cast<const float*>(a.w) + c), f);
+                else values<T>(load_raw(static_cast<const T*>(a.w) + c), f);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s_w[c + i] = f[i];
+        }
+        __syncthreads();
+    }
+    const bool full = a.H == 256 * NV * warps;
+    if (WHAT == kQuantI8 || !a.residual) {
+        if (full) rows_many<WHAT, T, 0, true, NV>(a, warps, s_w, s_x);
+        else rows_many<WHAT, T, 0, false, NV>(a, warps, s_w, s_x);
+    } else if (!a.res_f32 || sizeof(T) == 4) {
+        if (full) rows_many<WHAT, T, 1, true, NV>(a, warps, s_w, s_x);
+        else rows_many<WHAT, T, 1, false, NV>(a, warps, s_w, s_x);
+    } else {
+        if (full) rows_many<WHAT, T, 2, true, NV>(a, warps, s_w, s_x);
+        else rows_many<WHAT, T, 2, false, NV>(a, warps, s_w, s_x);
+    }
+}
+
+// Rows blockIdx.x, + gridDim.x, ...: a row per `warps` warps; a CTA has several at once only where
+// that is one.  NV vectors of eight values per thread; ONE: they hold the row, else it is gone
+// through twice.  MAXT, MINB: threads of a CTA at most, CTAs per SM at least.
+template <int WHAT, typename T, bool VEC, int NV, bool ONE, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_rows8(RmsNormArgs a, int warps) {
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
     constexpr bool kNorm = WHAT != kQuantI8, kRowMax = WHAT == kNormI8 || WHAT == kQuantI8;
+    __shared__ Exchange s_x;
+    int buf = 0;
     const int lane = threadIdx.x & 31;
     const int t = warps == 1 ? lane : threadIdx.x;
     const int step = 256 * warps;   // values per vector of the row's threads
-    const int64_t row = warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    if (row >= a.R) return;   // whole warps, and no CTA-wide barrier where warps == 1
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const int per_cta = warps == 1 ? blockDim.x >> 5 : 1;
+    const int64_t stride = (int64_t)gridDim.x * per_cta;
+    int64_t row = (int64_t)blockIdx.x * per_cta + (warps == 1 ? threadIdx.x >> 5 : 0);
 
-    // r of the eight values from c on; `stored`: the sum has been written
-    auto load_r = [&](int c, bool stored, float (&r)[8]) {
+    // x and the residual of eight values from c on; `stored`: their sum, which has been written
+    struct In { Raw8 x, res; };
+    auto load_in = [&](int64_t row, int c, bool stored) {
+        In in{};
         const int n = a.H - c;
-        if (n <= 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-            return;
-        }
+        if (n <= 0 || row >= a.R) return in;
         if (kNorm && stored && a.residual && a.total) {
-            if (a.res_f32) load8<float, VEC>(static_cast<const float*>(a.total) + row * a.ldt + c, n, r);
-            else load8<T, VEC>(static_cast<const T*>(a.total) + row * a.ldt + c, n, r);
+            if (a.res_f32) in.res = load8<float, VEC>(static_cast<const float*>(a.total) + row * a.ldt + c, n);
+            else in.x = load8<T, VEC>(static_cast<const T*>(a.total) + row * a.ldt + c, n);
+            return in;
+        }
+        in.x = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + c, n);
+        if (kNorm && a.residual) {
+            if (a.res_f32) in.res = load8<float, VEC>(static_cast<const float*>(a.residual) + row * a.ldr + c, n);
+            else in.res = load8<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr + c, n);
+        }
+        return in;
+    };
+    // r, and its store
+    auto sum_in = [&](int64_t row, const In& in, int c, bool stored, float (&r)[8]) {
+        values<T>(in.x, r);
+        if (!kNorm || !a.residual) return;
+        const int n = a.H - c;
+        if (stored && a.total) {
+            if (a.res_f32) values<float>(in.res, r);
             return;
         }
-        load8<T, VEC>(x + c, n, r);
-        if (!kNorm || !a.residual) return;
         float b[8];
-        if (a.res_f32) load8<float, VEC>(static_cast<const float*>(a.residual) + row * a.ldr + c, n, b);
-        else load8<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr + c, n, b);
+        if (a.res_f32) {
+            values<float>(in.res, b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            r[i] += b[i];
-            if (!a.res_f32) r[i] = to_f32(from_f32<T>(r[i]));
+            for (int i = 0; i < 8; ++i) r[i] += b[i];
+            if (!stored && a.total && n > 0)
+                store8<float, VEC>(static_cast<float*>(a.total) + row * a.ldt + c, n, raw_of<float>(r));
+        } else {
+            values<T>(in.res, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] += b[i];
+            const Raw8 sum = raw_of<T>(r);
+            values<T>(sum, r);
+            if (!stored && a.total && n > 0) store8<T, VEC>(static_cast<T*>(a.total) + row * a.ldt + c, n, sum);
         }
-    };
-    auto store_total = [&](int c, const float (&r)[8]) {
-        const int n = a.H - c;
-        if (!kNorm || !a.total || n <= 0) return;
-        if (a.res_f32) store8<float, VEC>(static_cast<float*>(a.total) + row * a.ldt + c, n, r);
-        else store8<T, VEC>(static_cast<T*>(a.total) + row * a.ldt + c, n, r);
     };
     auto times_w = [&](int c, float (&p)[8]) {
         const int n = a.H - c;
         if (!kNorm || !a.w || n <= 0) return;
         float w[8];
-        if (a.w_f32) load8<float, VEC>(static_cast<const float*>(a.w) + c, n, w);
-        else load8<T, VEC>(static_cast<const T*>(a.w) + c, n, w);
+        if (a.w_f32) values<float>(load8<float, VEC>(static_cast<const float*>(a.w) + c, n), w);
+        else values<T>(load8<T, VEC>(static_cast<const T*>(a.w) + c, n), w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] *= w[i];
     };
-    auto add_in = [&](int c, const float (&r)[8], float f, float& ss, uint32_t& m) {
-        float p[8];
+    auto add_in = [&](int c, const float (&r)[8], float& ss, float& m) {
+        if (kNorm)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            p[i] = r[i] * f;
-            if (kNorm) ss = fmaf(p[i], p[i], ss);
-        }
+            for (int i = 0; i < 8; ++i) ss = fmaf(r[i], r[i], ss);
         if (kRowMax) {
-            times_w(c, p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, magnitude(p[i]));
-        }
-    };
-
-    float r[NV][8], ss = 0.0f;
-    uint32_t m = 0;
-    for (int c0 = 0; c0 < a.H; c0 += NV * step) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) load_r(c0 + v * step + 8 * t, false, r[v]);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = c0 + v * step + 8 * t;
-            store_total(c, r[v]);
-            add_in(c, r[v], 1.0f, ss, m);
-        }
-        if (ONE) break;
-    }
-    combine_row(ss, m, warps);
-    float f = 1.0f;
-    if (kNorm && !(ss < INFINITY)) {   // beyond fp32's range, or not finite at all; the same in each thread
-        f = kTiny;
-        ss = 0.0f;
-        m = 0;
-        for (int c0 = 0; c0 < a.H; c0 += NV * step)
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = c0 + v * step + 8 * t;
-                if (!ONE) load_r(c, true, r[v]);
-                add_in(c, r[v], f, ss, m);
-            }
-        combine_row(ss, m, warps);
-    }
-    const float rstd = kNorm ? __frcp_rn(__fsqrt_rn(__fdiv_rn(ss, (float)a.H) + (f == 1.0f ? a.eps : 0.0f))) : 1.0f;
-    if (kRowMax) {
-        m = fp8_amax_bits(m);
-        if (t == 0) a.scales[row] = __fdiv_rn(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f);
-    }
-    for (int c0 = 0; c0 < a.H; c0 += NV * step) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = c0 + v * step + 8 * t, n = a.H - c;
-            if (!ONE) load_r(c, true, r[v]);
             float p[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = kNorm ? r[v][i] * f : r[v][i];
+            for (int i = 0; i < 8; ++i) p[i] = r[i];
             times_w(c, p);
-            uint2 q = make_uint2(0, 0);
-            if (WHAT == kNormE4m3) {   // every lane takes part in the block's maximum
-                uint32_t bm = 0;
+            m = largest(p, m);
+        }
+    };
+    auto shrink = [&](float (&r)[8]) {   // rows beyond fp32's range
 #pragma unroll
-                for (int i = 0; i < 8; ++i) bm = max(bm, magnitude(p[i]));
+        for (int i = 0; i < 8; ++i) r[i] *= kTiny;
+    };
+
+    for (; row < a.R; row += stride) {   // the same rows in every thread of a barrier
+        float r[NV][8], ss = 0.0f, mf = 0.0f;
+        for (int c0 = 0; c0 < a.H; c0 += NV * step) {
+            In in[NV];
 #pragma unroll
-                for (int o = 8; o >= 1; o >>= 1) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-                bm = fp8_amax_bits(bm);
-                q = e4m3_codes(p, bm);
-                if ((lane & 15) == 0 && n > 0)
-                    a.scales[(int64_t)(c / kFp8Block) * a.R + row] = __fdiv_rn(__uint_as_float(bm) * rstd, 448.0f);
-            }
-            if (kRowMax) q = i8_codes(p, m);
-            if (n <= 0) continue;
-            if (WHAT != kNormOnly) {
-                uint8_t* dst = a.codes + row * a.H + c;
-                if (VEC) {
-                    *reinterpret_cast<uint2*>(dst) = q;
-                } else {
+            for (int v = 0; v < NV; ++v) in[v] = load_in(row, c0 + v * step + 8 * t, false);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < n) dst[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+            for (int v = 0; v < NV; ++v) sum_in(row, in[v], c0 + v * step + 8 * t, false, r[v]);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) add_in(c0 + v * step + 8 * t, r[v], ss, mf);
+            if (ONE) break;
+        }
+        uint32_t m = __float_as_uint(mf);
+        combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
+        // beyond fp32's range, or not finite at all; the same in each thread
+        const bool huge = kNorm && !(ss < INFINITY);
+        if (huge) {
+            ss = mf = 0.0f;
+            for (int c0 = 0; c0 < a.H; c0 += NV * step)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int c = c0 + v * step + 8 * t;
+                    if (!ONE) sum_in(row, load_in(row, c, true), c, true, r[v]);
+                    shrink(r[v]);
+                    add_in(c, r[v], ss, mf);
+                }
+            m = __float_as_uint(mf);
+            combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
+        }
+        const float rstd = kNorm ? rsqrtf(fmaf(ss, a.inv_h, huge ? 0.0f : a.eps)) : 1.0f;
+        if (kRowMax) {
+            m = fp8_amax_bits(m);
+            if (t == 0) a.scales[row] = over(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f, 1.0f / 127.0f);
+        }
+        for (int c0 = 0; c0 < a.H; c0 += NV * step) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = c0 + v * step + 8 * t, n = a.H - c;
+                if (!ONE) {
+                    sum_in(row, load_in(row, c, true), c, true, r[v]);
+                    if (huge) shrink(r[v]);
+                }
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = r[v][i];
+                times_w(c, p);
+                uint2 q = make_uint2(0, 0);
+                if (WHAT == kNormE4m3) {   // every lane takes part in the block's maximum
+                    uint32_t bm = __float_as_uint(largest(p, 0.0f));
+#pragma unroll
+                    for (int o = 8; o >= 1; o >>= 1) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+                    bm = fp8_amax_bits(bm);
+                    q = e4m3_codes(p, bm);
+                    if ((lane & 15) == 0 && n > 0)
+                        a.scales[(int64_t)(c / kFp8Block) * a.R + row] = over(__uint_as_float(bm) * rstd, 448.0f, 1.0f / 448.0f);
+                }
+                if (kRowMax) q = i8_codes(p, m);
+                if (n <= 0) continue;
+                if (WHAT != kNormOnly) {
+                    uint8_t* dst = a.codes + row * a.H + c;
+                    if (VEC) {
+                        *reinterpret_cast<uint2*>(dst) = q;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < n) dst[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+                    }
+                }
+                if (kNorm && (WHAT == kNormOnly || a.y)) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i] *= rstd;
+                    store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy + c, n, raw_of<T>(p));
                 }
             }
-            if (kNorm && (WHAT == kNormOnly || a.y)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] *= rstd;
-                store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy + c, n, p);
-            }
+            if (ONE) break;
         }
-        if (ONE) break;
     }
 }
 
@@ -289,11 +583,23 @@ bool rows_aligned(const void* p, int64_t ld, size_t size, int64_t R) {
     return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (R <= 1 || ld * (int64_t)size % 16 == 0));
 }
 
-template <int WHAT, typename T, bool VEC, int NV, bool ONE>
-cudaError_t launch_as(const RmsNormArgs& a, int warps, cudaStream_t st) {
-    const int rows = warps == 1 ? 4 : 1;   // per CTA
-    return launch_kernel(k_rows8<WHAT, T, VEC, NV, ONE>, dim3((unsigned)(((int64_t)a.R + rows - 1) / rows)),
-                         dim3(32 * warps * rows), 0, st, a, warps);
+template <int WHAT, typename T, bool VEC, int NV, bool ONE, int MAXT, int MINB>
+cudaError_t launch_as(const RmsNormArgs& a, int warps, int num_sms, cudaStream_t st) {
+    const int per_cta = warps == 1 ? 4 : 1, threads = 32 * warps * per_cta;
+    int64_t grid = ((int64_t)a.R + per_cta - 1) / per_cta;
+    const int64_t resident = (int64_t)num_sms * (MAXT * MINB / threads);
+    if (grid > resident) grid = resident;
+    return launch_kernel(k_rows8<WHAT, T, VEC, NV, ONE, MAXT, MINB>, dim3((unsigned)grid), dim3(threads), 0, st, a, warps);
+}
+
+template <int WHAT, typename T, int NV, int MINB>
+cudaError_t launch_many(const RmsNormArgs& a, int warps, int num_sms, cudaStream_t st) {
+    const int per_cta = warps == 1 ? 4 : 1, threads = 32 * warps * per_cta;
+    int64_t grid = ((int64_t)a.R + per_cta - 1) / per_cta;
+    const int64_t resident = (int64_t)num_sms * (256 * MINB / threads);
+    if (grid > resident) grid = resident;
+    return launch_kernel(k_rows8_many<WHAT, T, NV, MINB>, dim3((unsigned)grid), dim3(threads),
+                         WHAT == kQuantI8 ? 0 : (size_t)a.H * 4, st, a, warps);
 }
 
 template <int WHAT, typename T>
@@ -304,12 +610,18 @@ cudaError_t launch_t(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
                      reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
     const int per_warp = (a.H + 255) / 256;   // vectors that one warp would hold
     auto warps = [&](int nv) { return (per_warp + nv - 1) / nv; };
-    if (warps(4) > 32) return vec ? launch_as<WHAT, T, true, 4, false>(a, 32, st) : launch_as<WHAT, T, false, 4, false>(a, 32, st);
-    if (!vec) return launch_as<WHAT, T, false, 4, true>(a, warps(4), st);
+    if (warps(4) > 32)
+        return vec ? launch_as<WHAT, T, true, 4, false, 1024, 1>(a, 32, num_sms, st)
+                   : launch_as<WHAT, T, false, 4, false, 1024, 1>(a, 32, num_sms, st);
+    if (!vec) return warps(4) <= 8 ? launch_as<WHAT, T, false, 4, true, 256, 3>(a, warps(4), num_sms, st)
+                                   : launch_as<WHAT, T, false, 4, true, 1024, 1>(a, warps(4), num_sms, st);
     // few rows: a row over many threads, for the latency
-    if (a.R <= 4 * num_sms && warps(1) <= 32) return launch_as<WHAT, T, true, 1, true>(a, warps(1), st);
-    if (warps(2) <= 32) return launch_as<WHAT, T, true, 2, true>(a, warps(2), st);
-    return launch_as<WHAT, T, true, 4, true>(a, warps(4), st);
+    if (a.R <= 2 * num_sms && warps(1) <= 32) return launch_as<WHAT, T, true, 1, true, 1024, 1>(a, warps(1), num_sms, st);
+    // many: much of a row per thread, since the exchange costs each warp as much as eight values a lane
+    if (per_warp == 1) return launch_many<WHAT, T, 1, 4>(a, 1, num_sms, st);
+    if (per_warp == 2) return launch_many<WHAT, T, 2, 3>(a, 1, num_sms, st);
+    if (warps(4) <= 8) return launch_many<WHAT, T, 4, 2>(a, warps(4), num_sms, st);
+    return launch_as<WHAT, T, true, 4, true, 1024, 1>(a, warps(4), num_sms, st);
 }
 
 template <typename T>

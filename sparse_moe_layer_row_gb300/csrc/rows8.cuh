@@ -16,7 +16,7 @@ struct RmsNormArgs {
     const void* w;            // [H], or NULL: ones
     int res_f32, w_f32;       // residual and total, w: fp32 instead of the type of x
     int R, H;
-    float eps;
+    float eps, inv_h;         // inv_h: 1 / H
     void* y;                  // the type of x, or NULL
     int64_t ldy;
     uint8_t* codes;           // [R, H], or NULL
