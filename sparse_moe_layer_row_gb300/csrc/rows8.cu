@@ -584,11 +584,9 @@ bool rows_aligned(const void* p, int64_t ld, size_t size, int64_t R) {
 }
 
 template <int WHAT, typename T, bool VEC, int NV, bool ONE, int MAXT, int MINB>
-cudaError_t launch_as(const RmsNormArgs& a, int warps, int num_sms, cudaStream_t st) {
+cudaError_t launch_as(const RmsNormArgs& a, int warps, cudaStream_t st) {
     const int per_cta = warps == 1 ? 4 : 1, threads = 32 * warps * per_cta;
-    int64_t grid = ((int64_t)a.R + per_cta - 1) / per_cta;
-    const int64_t resident = (int64_t)num_sms * (MAXT * MINB / threads);
-    if (grid > resident) grid = resident;
+    const int64_t grid = ((int64_t)a.R + per_cta - 1) / per_cta;
     return launch_kernel(k_rows8<WHAT, T, VEC, NV, ONE, MAXT, MINB>, dim3((unsigned)grid), dim3(threads), 0, st, a, warps);
 }
 
@@ -611,17 +609,22 @@ cudaError_t launch_t(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
     const int per_warp = (a.H + 255) / 256;   // vectors that one warp would hold
     auto warps = [&](int nv) { return (per_warp + nv - 1) / nv; };
     if (warps(4) > 32)
-        return vec ? launch_as<WHAT, T, true, 4, false, 1024, 1>(a, 32, num_sms, st)
-                   : launch_as<WHAT, T, false, 4, false, 1024, 1>(a, 32, num_sms, st);
-    if (!vec) return warps(4) <= 8 ? launch_as<WHAT, T, false, 4, true, 256, 3>(a, warps(4), num_sms, st)
-                                   : launch_as<WHAT, T, false, 4, true, 1024, 1>(a, warps(4), num_sms, st);
+        return vec ? launch_as<WHAT, T, true, 4, false, 1024, 1>(a, 32, st)
+                   : launch_as<WHAT, T, false, 4, false, 1024, 1>(a, 32, st);
+    if (!vec) return warps(4) <= 8 ? launch_as<WHAT, T, false, 4, true, 256, 3>(a, warps(4), st)
+                                   : launch_as<WHAT, T, false, 4, true, 1024, 1>(a, warps(4), st);
     // few rows: a row over many threads, for the latency
-    if (a.R <= 2 * num_sms && warps(1) <= 32) return launch_as<WHAT, T, true, 1, true, 1024, 1>(a, warps(1), num_sms, st);
+    if (a.R <= 2 * num_sms && warps(1) <= 32) return launch_as<WHAT, T, true, 1, true, 1024, 1>(a, warps(1), st);
     // many: much of a row per thread, since the exchange costs each warp as much as eight values a lane
     if (per_warp == 1) return launch_many<WHAT, T, 1, 4>(a, 1, num_sms, st);
     if (per_warp == 2) return launch_many<WHAT, T, 2, 3>(a, 1, num_sms, st);
+    // (an fp32 residual of 16-bit rows takes HBM longer than the arithmetic anyway, and CTAs that
+    // stay were slower there: 8192 x 4096 73.6 us against 63.7)
+    if (WHAT != kQuantI8 && a.res_f32 && warps(2) <= 32) return launch_as<WHAT, T, true, 2, true, 1024, 1>(a, warps(2), st);
+    // (8192 x 2048 with e4m3 codes: two vectors 20.8 us, four 22.4; int8 quantising 13.1 and 11.1)
+    if (WHAT != kQuantI8 && warps(2) <= 8) return launch_many<WHAT, T, 2, 3>(a, warps(2), num_sms, st);
     if (warps(4) <= 8) return launch_many<WHAT, T, 4, 2>(a, warps(4), num_sms, st);
-    return launch_as<WHAT, T, true, 4, true, 1024, 1>(a, warps(4), num_sms, st);
+    return launch_as<WHAT, T, true, 4, true, 1024, 1>(a, warps(4), st);
 }
 
 template <typename T>
