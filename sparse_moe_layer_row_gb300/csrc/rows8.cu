@@ -129,6 +129,13 @@ __device__ __forceinline__ float over(float a, float m, float r) {
     return a < INFINITY ? __fmaf_rn(__fmaf_rn(-q, m, a), r, q) : a;
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
 // int8 codes of eight values whose row's largest magnitude has the bits m.
 __device__ __forceinline__ uint2 i8_codes(const float (&p)[8], uint32_t m) {
     const float d = __uint_as_float(m) * (1.0f / 128.0f);
@@ -139,8 +146,9 @@ __device__ __forceinline__ uint2 i8_codes(const float (&p)[8], uint32_t m) {
         for (int i = 0; i < 4; ++i) {
             const float2 w = quotient2(mul2(make_float2(p[2 * i], p[2 * i + 1]), 127.0f / 128.0f), d, r);
             // |w| <= 127 and 1.5 * 2^23: the sum is rounded to an integer, which is its low byte
-            q[2 * i] = __float_as_int(w.x + 12582912.0f);
-            q[2 * i + 1] = __float_as_int(w.y + 12582912.0f);
+            const float2 s = add2(w, make_float2(12582912.0f, 12582912.0f));
+            q[2 * i] = __float_as_int(s.x);
+            q[2 * i + 1] = __float_as_int(s.y);
         }
     } else {   // an infinity or a NaN: codes 0, so that code times scale is NaN
 #pragma unroll
@@ -203,13 +211,6 @@ __device__ __forceinline__ void combine_row(Exchange& x, int& buf, float& ss, ui
 
 namespace {
 
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 __device__ __forceinline__ float2 mul22(float2 a, float2 b) {
     float2 r;
     asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -623,7 +624,7 @@ cudaError_t launch_t(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
     if (WHAT != kQuantI8 && a.res_f32 && warps(2) <= 32) return launch_as<WHAT, T, true, 2, true, 1024, 1>(a, warps(2), st);
     // (8192 x 2048 with e4m3 codes: two vectors 20.8 us, four 22.4; int8 quantising 13.1 and 11.1)
     if (WHAT != kQuantI8 && warps(2) <= 8) return launch_many<WHAT, T, 2, 3>(a, warps(2), num_sms, st);
-    if (warps(4) <= 8) return launch_many<WHAT, T, 4, 2>(a, warps(4), num_sms, st);
+    if (warps(4) <= 8) return launch_many<WHAT, T, 4, WHAT == kQuantI8 ? 3 : 2>(a, warps(4), num_sms, st);
     return launch_as<WHAT, T, true, 4, true, 1024, 1>(a, warps(4), st);
 }
 
