@@ -301,18 +301,19 @@ moe_status moe_block_forward_live(const moe_plan* plan, const void* x, int32_t R
  * Does what moe_block_pass does with one block and tau = 1 (every chosen expert
  * kept): topk_idx and topk_w are moe_block_route's, bit for bit; y is the same sum
  *   y[r] = S(x[r]) + sum over the slots j of row r of topk_w[r, j] * E_{topk_idx[r, j]}(x[r])
- * with h rounded as there, and the experts' outputs summed in fp32 without being stored, the
- * shared expert's first, in ascending order of the experts.
- * The result is reproducible, and does not depend on the other rows of a call but for the
- * order of fp32 sums.
+ * with h rounded as there, and the experts' outputs summed in fp32, in a fixed order, without
+ * being stored: reproducible, and a row depends on the other rows of a call in the order of
+ * its fp32 sums alone.
  *   R           0 .. min(8, max_rows)
  *   logit_bias  [E] fp32 added to every row's logits, or NULL
  *   topk_idx, topk_w  [R, k] out;  y [R, H] bf16 out;  y_f32 [R, H] fp32 out, or NULL
- * Plans of bf16 or e4m3 experts (moe_plan_create, moe_plan_create_fp8) with H up to 8192
- * and I and Is up to 16384; others: MOE_ERR_UNSUPPORTED.  The kernel's CTAs wait for one another (it is launched
- * cooperatively, one CTA per SM); their waits have the limit of moe_plan_set_wait_limit.
- * The workspace must have been zeroed once before its first use here.  MOE_STATUS_NONFINITE_OUTPUT
- * counts 16-column pieces. */
+ * y may be x.  Plans of bf16 or e4m3 experts (moe_plan_create, moe_plan_create_fp8) with H up
+ * to 8192 and I and Is up to 16384; others: MOE_ERR_UNSUPPORTED.  The kernel's CTAs wait for
+ * one another (it is launched cooperatively, one CTA per SM); their waits have the limit of
+ * moe_plan_set_wait_limit.
+ * The workspace must have been zeroed once before its first use here; the calls of this
+ * header, of any plan, may use it in between.  MOE_STATUS_NONFINITE_OUTPUT counts 16-column
+ * pieces. */
 moe_status moe_token_pass(const moe_plan* plan, const void* x, int32_t R, const float* logit_bias,
                           int32_t* topk_idx, float* topk_w, void* y, float* y_f32,
                           void* workspace, size_t workspace_bytes, moe_stream_t stream);
@@ -497,7 +498,8 @@ moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, i
                            int32_t K, int8_t* codes, float* scales, moe_stream_t stream);
 
 /* Bytes of device workspace (256-byte aligned; it begins with the status
- * counters, as in moe_workspace_bytes) of a moe_i8_gemm; 0 on bad sizes. */
+ * counters, as in moe_workspace_bytes) of a moe_i8_gemm: 1 KB, or with more rows (it
+ * depends on all three sizes) 2 KB and two bytes per code of x; 0 on bad sizes. */
 size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K);
 
 /* y = x W^T on int8 codes, x with a scale for each row (token), W for each output channel.
@@ -536,7 +538,8 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
  *   y         [R, H] of `dtype` out, or NULL; without a total in its place it may be x
  *   codes     [R, H] out, scales [ceil(H / 128), R] (e4m3) or [R] (int8) out, fp32;
  *             both NULL with MOE_CODES_NONE
- * At least one of y and codes.  Pointers are aligned to their element. */
+ * At least one of y and codes.  Pointers are aligned to their element.  No output overlaps
+ * an input or another output but as said above. */
 enum { MOE_CODES_NONE = 0, MOE_CODES_E4M3 = 1, MOE_CODES_I8 = 2 };
 moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int32_t R,
                            int32_t H, const void* residual, moe_dtype residual_dtype,

@@ -222,12 +222,16 @@ moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, i
                     "quantise launch");
 }
 
+// x as fp16 lies behind what a plan's workspace keeps between calls (Layout's status and barriers):
+// a workspace may serve both.
+constexpr size_t kX16Offset = 2048;
+
 size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K) {
     if (R < 0 || R > kMaxRows || N < 1 || N > kMaxRows || K < 16 || K % 16 || K > kI8MaxK) {
         fail(MOE_ERR_INVALID_ARG, "R=%d, N=%d, K=%d: R >= 0, N >= 1, K a positive multiple of 16 below 2^17", R, N, K);
         return 0;
     }
-    return kGemmWorkspace + (i8_rows_applies(R, N, K) ? 0 : 2 * (size_t)R * (size_t)K);
+    return i8_rows_applies(R, N, K) ? kGemmWorkspace : kX16Offset + 2 * (size_t)R * (size_t)K;
 }
 
 moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_t* wq,
@@ -254,7 +258,7 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
     if (i8_rows_applies(R, N, K)) return launched(launch_i8_rows(a, st), "gemm launch");
     int sms = 0, clusters = 0;
     if ((s = device_ready(false, &sms)) != MOE_OK || (s = pairs_ready(sms, &clusters)) != MOE_OK) return s;
-    void* x16 = static_cast<uint8_t*>(workspace) + kGemmWorkspace;
+    void* x16 = static_cast<uint8_t*>(workspace) + kX16Offset;
     CUtensorMap w, x;
     if (!encode_i8_tiles(&w, &x, wq, x16, R, N, K)) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     return launched(launch_i8_tiles(a, w, x, x16, sms, clusters, st), "gemm launch");

@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     }
     __syncthreads();
     // The down step's tiles follow gate/up's without a gap: turn by turn 16 hidden outputs; the
-    // tiles of all experts (the shared one's first) go round the warps.
-    // the lane's slots of the tiles in flight, taken in turn
+    // tiles of all experts (the shared one's last) go round the warps.
+    // The lane's slots of the tiles in flight, taken in turn:
     const int depth = a.depth;
     const uint32_t ring = smem_u32(sx) + a.arena + warp * (depth * kStage) + lane * 16;
     const uint32_t ring_end = ring + depth * kStage;

@@ -126,6 +126,34 @@ def test_norm_in_place_of_x(H):
     assert torch.equal(xt, total) and torch.equal(y2, y) and torch.equal(xy, y)
 
 
+@pytest.mark.parametrize("H", [8, 248, 256, 264, 512, 776, 2048, 4096, 4104, 8192, 8200, 32768, 32776])
+@pytest.mark.parametrize("dt,rt", [(BF, BF), (BF, FP), (HF, HF), (FP, FP)], ids=str)
+def test_norm_many_rows_in_place(dt, rt, H):
+    """More rows than CTAs, whose next row is loaded while one is worked on: in place gives what
+    separate buffers give, at the edges of the kernels' widths; rows and columns beyond stay."""
+    R = 1400 if H <= 8200 else 320
+    x, res = randn(R, H, seed=H).to(dt), randn(R, H, seed=H + 1).to(rt)
+    w = (1 + 0.2 * randn(H, seed=H + 2)).to(rt)
+    total = torch.empty_like(res)
+    y, q, s = outputs(R, H, dt, "y+i8")
+    mb.moe_add_rmsnorm(x, w, 1e-6, residual=res, total=total, y=y, codes=q, scales=s)
+    residual_sum(x, res, total)
+    check(total, w, 1e-6, dt, y, q, s)
+    _, q2, s2 = outputs(R, H, dt, "y+i8")
+    rbuf = torch.full((R + 2, H), 9.0, dtype=rt, device="cuda")
+    rbuf[:R] = res
+    xbuf = torch.full((R + 2, H), 9.0, dtype=dt, device="cuda")
+    xbuf[:R] = x
+    mb.moe_add_rmsnorm(xbuf[:R], w, 1e-6, residual=rbuf[:R], total=rbuf[:R], y=xbuf[:R], codes=q2, scales=s2)
+    assert torch.equal(rbuf[:R], total) and torch.equal(xbuf[:R], y) and torch.equal(q2, q) and torch.equal(s2, s)
+    assert torch.all(rbuf[R:] == 9) and torch.all(xbuf[R:] == 9)
+    if rt == dt:   # the sum in x's place
+        xt = x.clone()
+        y3, _, _ = outputs(R, H, dt, "y")
+        mb.moe_add_rmsnorm(xt, w, 1e-6, residual=res, total=xt, y=y3)
+        assert torch.equal(xt, total) and torch.equal(y3, y)
+
+
 def test_norm_codes_are_those_of_the_plain_formula():
     """Bit for bit: codes are formed from the stored sum by the stated fp32 operations."""
     for dt, H in ((BF, 2048), (FP, 1000), (HF, 640)):
@@ -371,6 +399,50 @@ def test_product_strided_output_and_nonfinite_scales(R, N, K):
     rest = torch.ones(R, N, dtype=torch.bool, device="cuda")
     rest[1], rest[:, 2] = False, False
     assert torch.equal(y[rest], product(xq, torch.ones_like(xs), wq, torch.ones_like(ws))[rest])
+
+
+@pytest.mark.parametrize("R,N,K", [(6, 500, 528), (30, 500, 528), (600, 2000, 528)])
+def test_product_stream_and_graph(R, N, K):
+    """On another stream, and captured and replayed on new codes; the workspace's contents and
+    what ran before in it do not show."""
+    xq, wq = codes(R, K, seed=11), codes(N, K, seed=12)
+    xs, ws = torch.exp(randn(R, seed=13)) * 0.01, torch.exp(randn(N, seed=14)) * 0.003
+    want = product(xq, xs, wq, ws, BF)
+    mem = torch.zeros(mb.moe_i8_gemm_workspace_bytes(R, N, K), dtype=torch.uint8, device="cuda")
+    mem[1024:] = 0xFF
+    y = torch.full((R + 1, N), 5.0, dtype=BF, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    mb.moe_i8_gemm(xq, xs, wq, ws, y[:R], mem, stream=st)
+    st.synchronize()
+    assert torch.equal(y[:R], want) and torch.all(y[R:] == 5)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        mb.moe_i8_gemm(xq, xs, wq, ws, y[:R], mem)
+    for i in range(5):
+        xq.copy_(codes(R, K, seed=20 + i))
+        xs.mul_(1.25)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y[:R], product(xq, xs, wq, ws, BF)) and torch.all(y[R:] == 5)
+    assert not any(mb.moe_read_device_status(mem).values())
+
+
+def test_quantize_then_product_back_to_back():
+    """Codes and scales written by one call and read by the next, with no wait of the host
+    between: a kernel may start before the one ahead of it ends."""
+    for R, N, K in ((4, 1000, 2048), (24, 1000, 2048), (1000, 1000, 2048)):
+        W, x = randn(N, K, seed=1), [randn(R, K, seed=2 + i).to(BF) for i in range(8)]
+        wq, ws = quantize(W)
+        mem = torch.zeros(mb.moe_i8_gemm_workspace_bytes(R, N, K), dtype=torch.uint8, device="cuda")
+        q, s = torch.empty(R, K, dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+        ys = [torch.empty(R, N, device="cuda") for _ in x]
+        for xi, yi in zip(x, ys):
+            mb.moe_i8_quantize(xi, q, s)
+            mb.moe_i8_gemm(q, s, wq, ws, yi, mem)
+        torch.cuda.synchronize()
+        for xi, yi in zip(x, ys):
+            assert torch.equal(yi, product(*quantize(xi), wq, ws))
 
 
 def test_norm_codes_feed_both_products():

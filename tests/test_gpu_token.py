@@ -8,6 +8,10 @@ expert's to 2^-16; the sum over experts adds a rounding of 2^-24 per addend.
 """
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -336,6 +340,109 @@ def test_wait_limit(kind):
         assert all(torch.equal(a, b) for a, b in zip(base, again))
         assert torch.equal(given[1], g2[1])
         c.status_clean()
+
+
+def test_two_layers_on_two_streams():
+    """Calls of two layers, each with its workspace, on two streams at once."""
+    cs = [Case("bf16", 8, E=32, k=4, H=1024, I=512, Is=512, seed=71), Case("e4m3", 3, E=64, k=6, H=512, seed=72)]
+    want = [c.routed() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [[], []]
+    for _ in range(50):
+        for c, st, o in zip(cs, streams, outs):
+            with torch.cuda.stream(st):   # its outputs' memory is of the stream too
+                o.append(c.routed())
+    torch.cuda.synchronize()
+    for c, w, o in zip(cs, want, outs):
+        for got in o:
+            assert all(torch.equal(a, b) for a, b in zip(w, got))
+        c.status_clean()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_one_workspace_for_the_layer_and_the_products(kind):
+    """The int8 and e4m3 products use the layer's workspace between its calls."""
+    c = Case(kind, 4, E=32, k=4, H=512, seed=73, max_rows=2048)
+    R, N, K = 520, 2048, 1024   # large enough for the tiles, whose x lies in the workspace
+    need = mb.moe_i8_gemm_workspace_bytes(R, N, K)
+    mem = c.layer.workspace
+    assert 2 * R * K < need <= mem.numel()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    xq = torch.randint(-127, 128, (R, K), generator=g, device="cuda").to(torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+    xs, ws = torch.ones(R, device="cuda"), torch.ones(N, device="cuda")
+    y = torch.empty(R, N, device="cuda")
+    want = c.routed()
+    for _ in range(5):
+        mb.moe_i8_gemm(xq, xs, wq, ws, y, mem)
+        got = c.routed()
+        given = c.given(want[2], want[3])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(given[1], want[1])
+        assert torch.equal(y.double(), xq.double() @ wq.double().t())
+    c.status_clean()
+
+
+def test_one_row_at_a_time_and_together():
+    """Rows alone give what they give together, up to the order of fp32 sums; also a view of a
+    larger batch, and R = 0."""
+    c = Case("bf16", 8, E=48, k=6, H=768, seed=74)
+    y, y32, idx, wt = c.routed()
+    _, bound = c.reference(idx, wt)
+    for r in range(8):
+        a = torch.empty(1, c.H, dtype=BF, device="cuda")
+        a32 = torch.empty(1, c.H, device="cuda")
+        i1, w1 = torch.empty(1, 6, dtype=torch.int32, device="cuda"), torch.empty(1, 6, device="cuda")
+        c.layer.token_pass(c.x[r:r + 1], topk_idx=i1, topk_w=w1, y=a, y_f32=a32)
+        assert torch.equal(i1[0], idx[r]) and torch.equal(w1[0], wt[r])
+        assert torch.all((a32[0] - y32[r]).abs() <= 2 * bound[r])
+    none = c.layer.token_forward(c.x[:0], idx[:0], wt[:0])
+    assert none.shape == (0, c.H)
+
+
+FIRST = """
+import torch
+from sparse_moe_layer_row_gb300 import moe_block as mb
+torch.manual_seed(0)
+dev, BF = "cuda", torch.bfloat16
+def w(*s): return (torch.randn(*s, device=dev) * 0.05).to(BF)
+H, E, I, R, N = 256, 16, 128, 700, 2048
+layer = mb.MoeBlockLayer(w(E, H), w(E, I, H), w(E, I, H), w(E, H, I), w(I, H), w(I, H), w(H, I), k=4, max_rows=8, max_blocks=1)
+x, big, W = w(4, H), w(R, H), w(N, H)
+n, y = torch.empty_like(x), torch.empty_like(x)
+q, s = torch.empty(R, H, dtype=torch.int8, device=dev), torch.empty(R, device=dev)
+wq, ws = torch.empty(N, H, dtype=torch.int8, device=dev), torch.empty(N, device=dev)
+out = torch.empty(R, N, device=dev)
+mem = torch.zeros(mb.moe_i8_gemm_workspace_bytes(R, N, H), dtype=torch.uint8, device=dev)
+assert mem.numel() > 2 * R * H
+def run():
+    mb.moe_add_rmsnorm(x, None, 1e-6, residual=x, y=n)
+    layer.token_pass(n, y=y)
+    mb.moe_i8_quantize(big, q, s)
+    mb.moe_i8_quantize(W, wq, ws)
+    mb.moe_i8_gemm(q, s, wq, ws, out, mem)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (n, y, q, wq, out)]
+for t in (n, y, q, wq, out): t.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (n, y, q, wq, out)))
+assert out.abs().max() > 0 and not any(layer.status().values()) and not any(mb.moe_read_device_status(mem).values())
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """What a first call sets up (attributes, occupancy) is allowed inside a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_scored_routing_into_the_layer():
