@@ -172,11 +172,11 @@ bool moe::encode_fp8(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, 
                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-bool moe::encode_i8_tiles(CUtensorMap* w, CUtensorMap* x, const void* wq, const void* x16, int R, int N, int K) {
-    const uint64_t dw[2] = {(uint64_t)K, (uint64_t)N}, dx[2] = {(uint64_t)K, (uint64_t)R};
+bool moe::encode_i8_tiles(CUtensorMap* a, CUtensorMap* b, const void* codes, const void* wide, int M, int C, int K) {
+    const uint64_t da[2] = {(uint64_t)K, (uint64_t)M}, db[2] = {(uint64_t)K, (uint64_t)C};
     const uint32_t box[2] = {64, 128};
-    return encode_plain(w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq, 2, dw, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
-           encode_plain(x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, 2, dx, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_plain(a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, 2, da, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
+           encode_plain(b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, wide, 2, db, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 moe_status moe::set_error(moe_status s, const char* msg) {

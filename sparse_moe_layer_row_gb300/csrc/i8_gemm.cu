@@ -11,25 +11,26 @@
 // permuted inside a block, alike in both operands, so that a lane's are 16-byte loads and
 // four codes of a row make one MMA's operand.  The warps' sums are added through shared memory.
 //
-// k_i8_tiles: tcgen05 kind::f16 (the bf16 rate).  A CTA pair (cta_group::2) takes 256 outputs by up
-// to 256 rows:
-//   A (M = 256)  W, 128 outputs per CTA: raw codes by TMA (8 KB per 64 of K), which the converter
-//                warps turn into fp16 in tensor memory, from where the MMA reads A
-//   B (N <= 256) x in fp16, half of the rows per CTA, by TMA.  k_i8_widen writes it to the
-//                workspace first: every output tile needs it, and converting it there would
-//                double the shared-memory traffic of the loop
-// so that W is read as bytes and never written, and an SM's shared memory carries 48 KB per 64 of
+// k_i8_tiles: tcgen05 kind::f16 (the bf16 rate).  A CTA pair (cta_group::2) takes 256 rows of A by up
+// to 256 of B, where B is the operand with fewer rows:
+//   A (M = 256)  128 rows per CTA: raw codes by TMA (8 KB per 64 of K), which the converter warps
+//                turn into fp16 in tensor memory, from where the MMA reads A
+//   B (N <= 256) fp16, half of the rows per CTA, by TMA.  k_i8_widen writes it to the workspace
+//                first: every tile of A needs it, and converting it there would double the
+//                shared-memory traffic of the loop
+// so that A is read as bytes and never written, and an SM's shared memory carries 48 KB per 64 of
 // K (512 clocks of the tensor core).  Tensor memory holds the accumulators (256 columns) and eight A
 // slots of 32, one per stage.  Roles, 512 threads per CTA:
-//   warps 0, 3      lane 0: TMA producers of W (`wfull`) and of x (`xfull`), ring of 8 stages
-//   warp 1          tensor memory; lane 0 of rank 0 issues the MMAs and commits (`empty`
-//                   of both ranks: the stage and its A slot; `tfull`)
-//   warp 2 lane 0   forwarder: the CTA's x of a stage has landed -> rank 0's `ready`
+//   warps 0, 3      lane 0: TMA producers of A (`afull`) and of B (`bfull`), ring of 8 stages
+//   warp 1          tensor memory; in rank 0, issues the MMAs and commits (`empty` of both ranks:
+//                   the stage and its A slot; `tfull`)
+//   warp 2 lane 0   forwarder: the CTA's B of a stage has landed -> rank 0's `ready`
 //   warps 4..7      converters: a row of 64 codes per thread -> rank 0's `ready`
-//   warps 8..15     epilogue: 32 outputs (a lane each) by 128 rows of x per warp.  They take the
+//   warps 8..15     epilogue: 32 rows of A (a lane each) by 128 of B per warp.  They take the
 //                   accumulators into registers at once (`tempty` of rank 0), so that the next
 //                   tile's MMAs run while they scale and store
 // Every wait is bounded, and drains follow an abort, as in gemm_pair.cu.
+#include <cstring>
 #include <type_traits>
 
 #include "pair.cuh"
@@ -126,23 +127,22 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
                     const uint4 x = vx[h][0][i];
                     mma_s8(acc[0], va[h][i].x, vb[h][i].x, va[h][i].y, vb[h][i].y, x.x, x.y);
                     mma_s8(acc[0], va[h][i].z, vb[h][i].z, va[h][i].w, vb[h][i].w, x.z, x.w);
-                    continue;
                 } else {
-                const uint32_t wa4[4] = {va[h][i].x, va[h][i].y, va[h][i].z, va[h][i].w};
-                const uint32_t wb4[4] = {vb[h][i].x, vb[h][i].y, vb[h][i].z, vb[h][i].w};
+                    const uint32_t wa4[4] = {va[h][i].x, va[h][i].y, va[h][i].z, va[h][i].w};
+                    const uint32_t wb4[4] = {vb[h][i].x, vb[h][i].y, vb[h][i].z, vb[h][i].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t a0, a1, a2, a3;
-                    widen4(wa4[j], a0, a2);
-                    widen4(wb4[j], a1, a3);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a0, a1, a2, a3;
+                        widen4(wa4[j], a0, a2);
+                        widen4(wb4[j], a1, a3);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const uint4 x = vx[h][t][i];
-                        uint32_t b0, b1;
-                        widen4(j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w, b0, b1);
-                        mma_f16(acc[t], a0, a1, a2, a3, b0, b1);
+                        for (int t = 0; t < NT; ++t) {
+                            const uint4 x = vx[h][t][i];
+                            uint32_t b0, b1;
+                            widen4(j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w, b0, b1);
+                            mma_f16(acc[t], a0, a1, a2, a3, b0, b1);
+                        }
                     }
-                }
                 }
             }
     }
@@ -172,9 +172,9 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
 constexpr int kStages = 8, kThreads = 512;
-constexpr int kRaw = 128 * 64, kXTile = 128 * 128;   // bytes per stage: codes of W, fp16 of x
-constexpr int kStageBytes = kRaw + kXTile;
-constexpr int kXOff = kStages * kRaw;                // x tiles behind the codes (1 KB boundaries)
+constexpr int kRaw = 128 * 64, kBTile = 128 * 128;   // bytes per stage: codes of A, fp16 of B
+constexpr int kStageBytes = kRaw + kBTile;
+constexpr int kBOff = kStages * kRaw;                // tiles of B behind the codes (1 KB boundaries)
 constexpr int kScaleOff = kStages * kStageBytes;     // float [8][128]: xs of an epilogue warp's rows
 constexpr int kBarOff = kScaleOff + 8 * 128 * 4;
 constexpr int kSmem = kBarOff + 512 + 1024;
@@ -212,21 +212,42 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { retur
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
-// One output of n (at most 128) rows from row r on: a warp stores 32 outputs of a row at a time.
+// What a lane holds of y: v[c] (xs[c] ws), c < n.  Along the rows (one output of n rows from p on): a
+// warp stores 32 outputs of a row at a time.
 template <typename T>
-__device__ __forceinline__ void store_rows(const I8GemmArgs& a, const float (&v)[128], const float* xs, float ws, int r,
-                                           int n, int out) {
-    T* p = static_cast<T*>(a.y) + (int64_t)r * a.ldy + out;
+__device__ __forceinline__ void store_rows(T* p, int64_t ld, const float (&v)[128], const float* xs, float ws, int n) {
 #pragma unroll
     for (int c = 0; c < 128; ++c) {
         if (c < n) *p = rounded<T>(v[c] * (xs[c] * ws));
-        p += a.ldy;
+        p += ld;
+    }
+}
+// Along a row (n outputs of one row from p on): 32 bytes a lane and store, where rows lie on them.
+template <typename T>
+__device__ __forceinline__ void store_along(T* p, bool vec, const float (&v)[128], const float* xs, float ws, int n) {
+    constexpr int kN = 32 / (int)sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 128; c += kN) {
+        T o[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) o[i] = rounded<T>(v[c + i] * (xs[c + i] * ws));
+        if (vec && c + kN <= n) {
+            uint32_t w[8];
+            memcpy(w, o, 32);
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + c), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (c + i < n) p[c + i] = o[i];
+        }
     }
 }
 
 }  // namespace
 
-// x codes to fp16, 16 per thread and turn.
+// Codes to fp16, 16 per thread and turn.
 __global__ void __launch_bounds__(256) k_i8_widen(const int8_t* q, __half* x, int64_t n16) {
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
@@ -242,15 +263,18 @@ __global__ void __launch_bounds__(256) k_i8_widen(const int8_t* q, __half* x, in
     }
 }
 
+template <bool SWAP>
 __global__ void __launch_bounds__(kThreads, 1)
-k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8GemmArgs a) {
+k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, I8GemmArgs a) {
+    const int M = SWAP ? a.R : a.N, C = SWAP ? a.N : a.R;   // rows of A and of B
+    const float *sa = SWAP ? a.xs : a.ws, *sb = SWAP ? a.ws : a.xs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;   // same offset in both CTAs
     uint8_t* base = smem_raw + (sbase - raw);
-    uint64_t* wfull = reinterpret_cast<uint64_t*>(base + kBarOff);   // [S] codes landed
-    uint64_t* xfull = wfull + kStages;                                // [S] x landed
-    uint64_t* ready = xfull + kStages;                                // [S] both ranks' x and A (rank 0)
+    uint64_t* afull = reinterpret_cast<uint64_t*>(base + kBarOff);   // [S] codes landed
+    uint64_t* bfull = afull + kStages;                                // [S] x landed
+    uint64_t* ready = bfull + kStages;                                // [S] both ranks' x and A (rank 0)
     uint64_t* empty = ready + kStages;                                // [S] stage and A slot free (both)
     uint64_t* tfull = empty + kStages;                                // accumulators ready (both)
     uint64_t* tempty = tfull + 1;                                     // accumulators free (rank 0)
@@ -263,8 +287,8 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(wfull + s, 1);
-            mbar_init(xfull + s, 1);
+            mbar_init(afull + s, 1);
+            mbar_init(bfull + s, 1);
             mbar_init(ready + s, 2 * (1 + 4));   // of each rank: the forwarder, four converter warps
             mbar_init(empty + s, 1);
         }
@@ -281,18 +305,18 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // The kernel before this one is k_i8_widen, which let it start after its own wait: all but the
-    // widened x was complete by then, so that only x's producer waits (common.cuh).
+    // widened operand was complete by then, so that only B's producer waits (common.cuh).
 
-    // unit u: outputs 256 m .., rows 256 c .. (neighbouring units share rows of x)
-    const int mt = (a.N + 255) / 256, nunits = mt * ((a.R + 255) / 256);
+    // unit u: rows 256 m .. of A, 256 c .. of B (neighbouring units share rows of B)
+    const int mt = (M + 255) / 256, nunits = mt * ((C + 255) / 256);
     const int nact = active_workers(nunits, (int)cluster_count());   // balanced rounds
     const int ufirst = (int)cluster_id() < nact ? (int)cluster_id() : nunits;
     const int nkb = (a.K + 63) / 64;
-    auto rows_of = [&](int u, int& m, int& r0) {   // the MMA's N: rows of the unit, in 32s
+    auto rows_of = [&](int u, int& m, int& r0) {   // the MMA's N: rows of B of the unit, in 32s
         const int c = u / mt;
         m = u - c * mt;
         r0 = c * 256;
-        return (min(256, a.R - r0) + 31) / 32 * 32;
+        return (min(256, C - r0) + 31) / 32 * 32;
     };
     auto give_up = [&]() {
         if (!*abort_flag) { *abort_flag = 1; status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1); }
@@ -302,14 +326,12 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if ((warp == 0 || warp == 3) && lane == 0) {
             // ----------------------------------------------------------- TMA producers
-            // (a copy takes its thread some 250 clocks to issue: both by one thread made the
-            // 64 of K 560 clocks long, whatever the tile's width)
-            const bool x = warp == 3;
-            if (x) {
+            const bool b = warp == 3;
+            if (b) {
                 pdl_wait();
                 pdl_trigger();
             }
-            uint64_t* full = x ? xfull : wfull;
+            uint64_t* full = b ? bfull : afull;
             int stage = 0, nfills = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -322,9 +344,9 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(full + stage, x ? kXTile : kRaw);
-                    if (x) tma_load_2d(sbase + kXOff + stage * kXTile, &tmX, kb * 64, r0 + n / 2 * rank, full + stage);
-                    else tma_load_2d(sbase + stage * kRaw, &tmW, kb * 64, m * 256 + 128 * rank, full + stage);
+                    mbar_expect_tx(full + stage, b ? kBTile : kRaw);
+                    if (b) tma_load_2d(sbase + kBOff + stage * kBTile, &tmB, kb * 64, r0 + n / 2 * rank, full + stage);
+                    else tma_load_2d(sbase + stage * kRaw, &tmA, kb * 64, m * 256 + 128 * rank, full + stage);
                     ++nfills;
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -362,7 +384,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t bd = smem_desc_sw128(sbase + kXOff + stage * kXTile);
+                    const uint64_t bd = smem_desc_sw128(sbase + kBOff + stage * kBTile);
                     const uint32_t at = tmem + (uint32_t)(kACol + 32 * stage);
                     if (leader) {
 #pragma unroll
@@ -387,7 +409,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             bool ok = true;
             for (int u = ufirst; ok && u < nunits; u += nact)
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_bounded(xfull + stage, phase, abort_flag, kWaitLimitNs)) {
+                    if (!mbar_wait_bounded(bfull + stage, phase, abort_flag, kWaitLimitNs)) {
                         give_up();
                         ok = false;
                         break;
@@ -410,7 +432,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         for (int u = ufirst; ok && u < nunits; u += nact)
             for (int kb = 0; kb < nkb; ++kb) {
                 // codes landed; they were only asked for once the MMA had read the slot
-                const bool got = mbar_wait_bounded(wfull + stage, phase, abort_flag, kWaitLimitNs);
+                const bool got = mbar_wait_bounded(afull + stage, phase, abort_flag, kWaitLimitNs);
                 if (__any_sync(0xffffffffu, !got)) {
                     give_up();
                     ok = false;
@@ -448,20 +470,17 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         for (int u = ufirst; u < nunits; u += nact) {
             int m, r0;
             rows_of(u, m, r0);
-            const int out = m * 256 + 128 * rank + 32 * q + lane;   // this lane's output
-            const float ws = out < a.N ? __ldg(a.ws + out) : 0.0f;
+            const int ra = m * 256 + 128 * rank + 32 * q + lane, rb = r0 + 128 * half;   // this lane's of A; B's first
+            const float ls = ra < M ? __ldg(sa + ra) : 0.0f;
             __syncwarp();   // the last tile's scales have been read
 #pragma unroll
-            for (int i = lane; i < 128; i += 32) {
-                const int r = r0 + 128 * half + i;
-                xs[i] = r < a.R ? __ldg(a.xs + r) : 0.0f;
-            }
+            for (int i = lane; i < 128; i += 32) xs[i] = rb + i < C ? __ldg(sb + rb + i) : 0.0f;
             __syncwarp();
             const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitLimitNs);
             if (__any_sync(0xffffffffu, !got)) { give_up(); break; }
             tphase ^= 1u;
             tc_fence_after();
-            const int n = min(128, a.R - r0 - 128 * half);   // rows of this warp
+            const int n = min(128, C - rb);   // of B, of this warp
             float v[128];
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
@@ -476,10 +495,14 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0);
-            if (out < a.N) {
-                if (a.ydtype == MOE_F32) store_rows<float>(a, v, xs, ws, r0 + 128 * half, n, out);
-                else if (a.ydtype == MOE_BF16) store_rows<__nv_bfloat16>(a, v, xs, ws, r0 + 128 * half, n, out);
-                else store_rows<__half>(a, v, xs, ws, r0 + 128 * half, n, out);
+            if (ra < M) {
+                auto store = [&](auto* y) {
+                    if (SWAP) store_along(y + (int64_t)ra * a.ldy + rb, a.y_vec, v, xs, ls, n);
+                    else store_rows(y + (int64_t)rb * a.ldy + ra, a.ldy, v, xs, ls, n);
+                };
+                if (a.ydtype == MOE_F32) store(static_cast<float*>(a.y));
+                else if (a.ydtype == MOE_BF16) store(static_cast<__nv_bfloat16*>(a.y));
+                else store(static_cast<__half*>(a.y));
             }
         }
     }
@@ -513,32 +536,39 @@ cudaLaunchConfig_t tiles_config(cudaLaunchAttribute (&attr)[2], int clusters, cu
 
 // Also the clusters that are resident at once on the current device.
 cudaError_t i8_tiles_set_attributes(int num_sms, int* clusters) {
-    cudaError_t e = cudaFuncSetAttribute(k_i8_tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    // the register split draws on what the CTA is launched with
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, k_i8_tiles)) != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = tiles_config(attr, num_sms / 2, nullptr);
-    cfg.numAttrs = 1;
-    int n = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&n, k_i8_tiles, &cfg)) != cudaSuccess) return e;
-    if (n <= 0) return cudaErrorInvalidConfiguration;
-    *clusters = n < num_sms / 2 ? n : num_sms / 2;
-    return cudaSuccess;
+    *clusters = num_sms / 2;
+    auto set = [&](auto k) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        // the register split draws on what the CTA is launched with
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = tiles_config(attr, num_sms / 2, nullptr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) != cudaSuccess) return e;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        *clusters = n < *clusters ? n : *clusters;
+        return cudaSuccess;
+    };
+    const cudaError_t e = set(k_i8_tiles<false>);
+    return e == cudaSuccess ? set(k_i8_tiles<true>) : e;
 }
 
-cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& w, const CUtensorMap& x, void* x16, int num_sms,
+cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, void* wide, int num_sms,
                             int clusters, cudaStream_t st) {
-    const int64_t n16 = (int64_t)a.R * a.K / 16;
+    const bool swap = i8_swapped(a.R, a.N);
+    const int64_t n16 = (int64_t)(swap ? a.N : a.R) * a.K / 16;
     int64_t blocks = (n16 + 255) / 256;
     if (blocks > (int64_t)num_sms * 32) blocks = (int64_t)num_sms * 32;
-    cudaError_t e = launch_kernel(k_i8_widen, dim3((unsigned)blocks), dim3(256), 0, st, a.xq, static_cast<__half*>(x16), n16);
+    cudaError_t e = launch_kernel(k_i8_widen, dim3((unsigned)blocks), dim3(256), 0, st, swap ? a.wq : a.xq,
+                                  static_cast<__half*>(wide), n16);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = tiles_config(attr, clusters, st);
-    return cudaLaunchKernelEx(&cfg, k_i8_tiles, w, x, a);
+    return cudaLaunchKernelEx(&cfg, swap ? k_i8_tiles<true> : k_i8_tiles<false>, ma, mb, a);
 }
 
 // By what the two kernels were measured to take (ns): the rows kernel 1800 + CTAs (3.5 + 0.0046 K)

@@ -222,16 +222,16 @@ moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, i
                     "quantise launch");
 }
 
-// x as fp16 lies behind what a plan's workspace keeps between calls (Layout's status and barriers):
-// a workspace may serve both.
-constexpr size_t kX16Offset = 2048;
+// The operand that is widened lies behind what a plan's workspace keeps between calls (Layout's
+// status and barriers): a workspace may serve both.
+constexpr size_t kWideOffset = 2048;
 
 size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K) {
     if (R < 0 || R > kMaxRows || N < 1 || N > kMaxRows || K < 16 || K % 16 || K > kI8MaxK) {
         fail(MOE_ERR_INVALID_ARG, "R=%d, N=%d, K=%d: R >= 0, N >= 1, K a positive multiple of 16 below 2^17", R, N, K);
         return 0;
     }
-    return i8_rows_applies(R, N, K) ? kGemmWorkspace : kX16Offset + 2 * (size_t)R * (size_t)K;
+    return i8_rows_applies(R, N, K) ? kGemmWorkspace : kWideOffset + 2 * (size_t)(R < N ? R : N) * (size_t)K;
 }
 
 moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_t* wq,
@@ -253,15 +253,18 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
         return fail(MOE_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype, static_cast<uint32_t*>(workspace)};
+    I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype, static_cast<uint32_t*>(workspace),
+                 aligned(y, 32) && row_stride * (int64_t)dtype_size(dtype) % 32 == 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (i8_rows_applies(R, N, K)) return launched(launch_i8_rows(a, st), "gemm launch");
     int sms = 0, clusters = 0;
     if ((s = device_ready(false, &sms)) != MOE_OK || (s = pairs_ready(sms, &clusters)) != MOE_OK) return s;
-    void* x16 = static_cast<uint8_t*>(workspace) + kX16Offset;
-    CUtensorMap w, x;
-    if (!encode_i8_tiles(&w, &x, wq, x16, R, N, K)) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    return launched(launch_i8_tiles(a, w, x, x16, sms, clusters, st), "gemm launch");
+    const bool swap = i8_swapped(R, N);
+    void* wide = static_cast<uint8_t*>(workspace) + kWideOffset;
+    CUtensorMap ma, mb;
+    if (!encode_i8_tiles(&ma, &mb, swap ? xq : wq, wide, swap ? R : N, swap ? N : R, K))
+        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    return launched(launch_i8_tiles(a, ma, mb, wide, sms, clusters, st), "gemm launch");
 }
 
 moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int32_t R,

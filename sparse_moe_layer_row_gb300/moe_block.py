@@ -261,6 +261,28 @@ def _same_device(*tensors) -> int:
     return dev
 
 
+def _need_at(t: torch.Tensor, name: str, device: int, dtype, shape):
+    """_need and _same_device in one: a contiguous tensor of that device, type and shape."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype == dtype
+            and t.shape == shape and t.is_contiguous()):
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"tensors on different devices: {name} on {t.device}, others on cuda:{device}")
+
+
+def _need_rows_at(t: torch.Tensor, name: str, device: int, dtype, shape) -> int:
+    """_need_rows and _same_device in one, of one type; returns the row stride."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype == dtype
+            and t.shape == shape and t.is_contiguous()):
+        return shape[1]
+    ld = _need_rows(t, name, shape)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"tensors on different devices: {name} on {t.device}, others on cuda:{device}")
+    return ld
+
+
 def _on(device: int, fn, *args):
     """Call the library with ``device`` current."""
     if torch._C._cuda_getDevice() == device:
@@ -665,10 +687,10 @@ def moe_i8_quantize(x, codes, scales, stream=None):
     """Rows x [R, K] (bf16, fp16 or fp32; rows may be strided) to int8 ``codes`` [R, K] and
     fp32 ``scales`` [R], one per row (for weights [N, K]: one per output channel)."""
     ld = _need_rows(x, "x")
-    R, K = x.shape
-    _need(codes, "codes", torch.int8, (R, K))
-    _need(scales, "scales", torch.float32, (R,))
-    dev = _same_device(x, codes, scales)
+    dev, shape = x.get_device(), x.shape
+    R, K = shape
+    _need_at(codes, "codes", dev, torch.int8, shape)
+    _need_at(scales, "scales", dev, torch.float32, (R,))
     _on(dev, load().moe_i8_quantize, _ptr(x), _DTYPES[x.dtype], ld, R, K, _ptr(codes),
         _ptr(scales), _stream(stream, dev))
 
@@ -686,23 +708,21 @@ def moe_i8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
     moe_i8_quantize writes them), wq [N, K] with a scale per output ws [N].
     y: bf16, fp16 or fp32, rows may be strided."""
     ld = _need_rows(y, "y")
+    dev = y.get_device()
     R, N = y.shape
-    _need(xq, "xq", torch.int8)
-    if xq.dim() != 2 or xq.shape[0] != R:
-        raise ValueError(f"xq must have shape ({R}, K), got {tuple(xq.shape)}")
-    K = xq.shape[1]
-    _need(xs, "xs", torch.float32, (R,))
-    _need(wq, "wq", torch.int8, (N, K))
-    _need(ws, "ws", torch.float32, (N,))
-    _need(workspace, "workspace", torch.uint8)
-    dev = _same_device(xq, xs, wq, ws, y, workspace)
+    K = xq.shape[-1] if isinstance(xq, torch.Tensor) and xq.dim() else 0
+    _need_at(xq, "xq", dev, torch.int8, (R, K))
+    _need_at(xs, "xs", dev, torch.float32, (R,))
+    _need_at(wq, "wq", dev, torch.int8, (N, K))
+    _need_at(ws, "ws", dev, torch.float32, (N,))
+    _need_at(workspace, "workspace", dev, torch.uint8, getattr(workspace, "shape", None))
     _on(dev, load().moe_i8_gemm, _ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
         _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(), _stream(stream, dev))
 
 
-def _of_type(t, name, dtype):
-    if t.dtype != dtype and t.dtype != torch.float32:
-        raise ValueError(f"{name} must be {dtype} (the type of x) or torch.float32, got {t.dtype}")
+def _or_fp32(t, dtype):
+    """The type that ``t`` has to have: ``dtype``, or fp32 where it is that."""
+    return torch.float32 if isinstance(t, torch.Tensor) and t.dtype == torch.float32 else dtype
 
 
 def moe_add_rmsnorm(x, weight, eps, residual=None, total=None, y=None, codes=None, scales=None,
@@ -715,36 +735,29 @@ def moe_add_rmsnorm(x, weight, eps, residual=None, total=None, y=None, codes=Non
     of moe_fp8_gemm) or int8 with [R] (those of moe_i8_gemm).  Rows of x, residual, total and
     y may be strided."""
     ldx = _need_rows(x, "x")
-    shape = x.shape
+    dev, dt, shape = x.get_device(), x.dtype, x.shape
     R, H = shape
-    dt = x.dtype
     ldr = ldt = ldy = 0
     rt = wt = dt
     if residual is not None:
-        ldr = _need_rows(residual, "residual", shape)
-        rt = residual.dtype
-        _of_type(residual, "residual", dt)
+        rt = _or_fp32(residual, dt)
+        ldr = _need_rows_at(residual, "residual", dev, rt, shape)
     if total is not None:
         if residual is None:
             raise ValueError("total needs a residual")
-        ldt = _need_rows(total, "total", shape)
-        if total.dtype != rt:
-            raise ValueError(f"total must be {rt}, got {total.dtype}")
+        ldt = _need_rows_at(total, "total", dev, rt, shape)
     if weight is not None:
-        wt = weight.dtype if isinstance(weight, torch.Tensor) else None
-        _need(weight, "weight", dt if wt == dt else torch.float32, (H,))
+        wt = _or_fp32(weight, dt)
+        _need_at(weight, "weight", dev, wt, (H,))
     if y is not None:
-        ldy = _need_rows(y, "y", shape)
-        if y.dtype != dt:
-            raise ValueError(f"y must be {dt}, got {y.dtype}")
+        ldy = _need_rows_at(y, "y", dev, dt, shape)
     kind = 0
     if codes is not None:
         kind = 2 if codes.dtype == torch.int8 else 1
-        _need(codes, "codes", torch.int8 if kind == 2 else torch.float8_e4m3fn, shape)
-        _need(scales, "scales", torch.float32, (R,) if kind == 2 else (-(-H // 128), R))
+        _need_at(codes, "codes", dev, torch.int8 if kind == 2 else torch.float8_e4m3fn, shape)
+        _need_at(scales, "scales", dev, torch.float32, (R,) if kind == 2 else (-(-H // 128), R))
     elif scales is not None:
         raise ValueError("scales go with codes")
-    dev = _same_device(x, weight, residual, total, y, codes, scales)
     _on(dev, load().moe_add_rmsnorm, _ptr(x), _DTYPES[dt], ldx, R, H, _ptr(residual), _DTYPES[rt],
         ldr, _ptr(total), ldt, _ptr(weight), _DTYPES[wt], eps, _ptr(y), ldy, kind, _ptr(codes),
         _ptr(scales), _stream(stream, dev))
