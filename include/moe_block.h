@@ -499,7 +499,7 @@ moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, i
 
 /* Bytes of device workspace (256-byte aligned; it begins with the status
  * counters, as in moe_workspace_bytes) of a moe_i8_gemm: 1 KB, or with more rows (it
- * depends on all three sizes) 2 KB + 2 K min(R, N); 0 on bad sizes. */
+ * depends on all three sizes) 66 KB + 2 K min(R, N); 0 on bad sizes. */
 size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K);
 
 /* y = x W^T on int8 codes, x with a scale for each row (token), W for each output channel.

@@ -384,7 +384,8 @@ moe_status enqueue_token(const moe_plan* p, const void* x, int32_t R, bool given
     a.topk_idx = topk_idx;
     a.topk_w = topk_w;
     a.h = at<void>(workspace, L.h32);
-    a.counters = at<uint32_t>(workspace, L.barriers);
+    a.counters = at<uint64_t>(workspace, L.token);
+    a.tagged = a.counters + 128;
     a.status = at<uint32_t>(workspace, L.status);
     a.y = static_cast<__nv_bfloat16*>(y);
     a.y_f32 = y_f32;

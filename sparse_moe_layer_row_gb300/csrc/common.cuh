@@ -19,8 +19,9 @@ namespace moe {
 
 struct Layout {
     size_t status;       // uint32[MOE_STATUS_WORDS]
-    size_t barriers;     // uint32[2]                  grid barriers of token.cu; at the same place in
-                         // every layout, so that plans of any shape may share a workspace
+    size_t token;        // uint64[128 + 8 * 1024]     counters and numbered logits of token.cu, kept
+                         // between calls: at the same place (up to kTokenEnd) in every layout, so
+                         // that plans of any shape may share a workspace
     size_t route_cnt;    // uint32[max_rows]          router row / row-group tickets
     size_t logits;       // fp32 [max_rows, E]        router logits (before bias)
     size_t wnorm;        // fp32 [E]                  |w_e|_2
@@ -76,6 +77,8 @@ inline int64_t logit_rows(int64_t max_rows) {
     return r8 < kTcSplitRows ? r8 : (max_rows > kTcSplitRows ? max_rows : kTcSplitRows);
 }
 
+constexpr size_t kTokenEnd = 2048 + 8 * 8 * 1024;
+
 inline Layout make_layout(const moe_dims& d) {
     Layout L{};
     const int64_t R = d.max_rows, E = d.E, H = d.H;
@@ -89,7 +92,7 @@ inline Layout make_layout(const moe_dims& d) {
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 1024); return at; };
     L.status = take(sizeof(uint32_t) * 64);
-    L.barriers = take(sizeof(uint32_t) * 2);
+    L.token = take(kTokenEnd - o);
     L.route_cnt = take(sizeof(uint32_t) * (size_t)R);
     L.logits = take(sizeof(float) * (size_t)(logit_rows(R) * E));
     L.wnorm = take(sizeof(float) * (size_t)E);

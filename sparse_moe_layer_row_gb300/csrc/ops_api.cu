@@ -222,9 +222,9 @@ moe_status moe_i8_quantize(const void* x, moe_dtype dtype, int64_t row_stride, i
                     "quantise launch");
 }
 
-// The operand that is widened lies behind what a plan's workspace keeps between calls (Layout's
-// status and barriers): a workspace may serve both.
-constexpr size_t kWideOffset = 2048;
+// The operand that is widened lies behind what a plan's workspace keeps between calls: a workspace
+// may serve both.
+constexpr size_t kWideOffset = kTokenEnd;
 
 size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K) {
     if (R < 0 || R > kMaxRows || N < 1 || N > kMaxRows || K < 16 || K % 16 || K > kI8MaxK) {

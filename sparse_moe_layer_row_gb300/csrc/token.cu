@@ -49,7 +49,7 @@ constexpr int kGroup = 4;                       // warps that share a gate/up un
 constexpr int kGroups = kWarps / kGroup;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxPairs = kTokenRows * 32;      // k <= 32
-constexpr int64_t kPrefetchBytes = 32 << 20;    // of the down weights, a quarter of L2
+constexpr int64_t kPrefetchBytes = 40 << 20;    // of gate/up, and of the down weights: a third of L2 each
 
 // A tile: 16 weight rows by 128 bytes of K; a lane holds 32 bytes of two rows.
 template <bool FP8>
@@ -73,6 +73,7 @@ struct Smem {
     uint32_t used[kMaxExperts / 32];            // experts touched, a bit each
     uint32_t scratch[MOE_STATUS_WORDS];         // for status counts that another CTA makes
     int ok;
+    uint32_t call;
 };
 
 // x in shared memory: rows an odd multiple of 64 bytes apart, so that a quarter-warp's reads (two
@@ -183,20 +184,20 @@ __device__ __forceinline__ void tile_mma(float (&d)[4], const uint4 (&a)[2], con
     }
 }
 
-constexpr uint32_t kRound = 1024;
-__device__ __forceinline__ uint32_t ld_round(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+constexpr uint64_t kRound = 1024;
+__device__ __forceinline__ uint64_t ld_round(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v & ~(kRound - 1);
 }
 // Releases what the CTA wrote before the __syncthreads ahead of it.
-__device__ __forceinline__ void arrive(uint32_t* p) {
-    const uint32_t n = blockIdx.x == 0 ? kRound - (gridDim.x - 1) : 1;
-    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(n) : "memory");
+__device__ __forceinline__ void arrive(uint64_t* p) {
+    const uint64_t n = blockIdx.x == 0 ? kRound - (gridDim.x - 1) : 1;
+    asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p), "l"(n) : "memory");
 }
 // A grid barrier; the whole CTA calls it.  round: the counter's at the start of the kernel (in
 // thread 0).  False: gave up, the same in every thread.
-__device__ __forceinline__ bool grid_barrier(uint32_t* counter, uint32_t round, uint64_t limit_ns, int* ok) {
+__device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t round, uint64_t limit_ns, int* ok) {
     __syncthreads();
     if (threadIdx.x == 0) {
         arrive(counter);
@@ -209,6 +210,19 @@ __device__ __forceinline__ bool grid_barrier(uint32_t* counter, uint32_t round, 
     return *ok;
 }
 
+// A logit and the call that it is of, in one word: who reads the call's number reads its logit, and
+// neither a fence nor a barrier stands between.  Numbers: the low 32 bits of the rounds that the down
+// step's counter has ended, plus 1 (0: a workspace that was never used).
+__device__ __forceinline__ uint32_t call_number(uint64_t round) { return (uint32_t)(round / kRound) + 1; }
+__device__ __forceinline__ void store_tagged(uint64_t* p, float z, uint32_t call) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"((uint64_t)call << 32 | __float_as_uint(z)) : "memory");
+}
+__device__ __forceinline__ uint64_t ld_tagged(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {   // the xor butterfly of route_common.cuh
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -216,7 +230,7 @@ __device__ __forceinline__ float warp_sum(float v) {   // the xor butterfly of r
 }
 
 // The logit of one expert and row, one warp.
-__device__ __forceinline__ void expert_logit(const TokenArgs& a, int e, int r, int lane) {
+__device__ __forceinline__ void expert_logit(const TokenArgs& a, int e, int r, int lane, uint32_t call) {
     constexpr int kS = 8;   // stripes of 256 at a time
     float acc = 0.0f;
     const __nv_bfloat16* w = a.wr + (int64_t)e * a.H + lane * 8;
@@ -234,11 +248,16 @@ __device__ __forceinline__ void expert_logit(const TokenArgs& a, int e, int r, i
             if (s0 + 256 * i < a.H) acc = dot8_bf16(xv[i], wv[i], acc);
     }
     const float z = warp_sum(acc);
-    if (lane == 0) a.logits[(int64_t)r * a.E + e] = z;
+    if (lane == 0) store_tagged(a.tagged + r * kMaxExperts + e, z, call);
 }
 
 // Rows with many equal logits: the top-k of route_common.cuh.  Not inlined: rarely called code.
-__device__ __noinline__ void topk_slow(const RouteArgs& ra, int row, int lane) { route_topk(ra, row, row + 1, lane); }
+// It reads logits alone: every CTA writes the same ones.
+__device__ __noinline__ void topk_slow(const RouteArgs& ra, const uint64_t* tagged, int row, int lane) {
+    for (int e = lane; e < ra.E; e += 32) ra.logits[(int64_t)row * ra.E + e] = __uint_as_float((uint32_t)ld_tagged(tagged + e));
+    __syncwarp();
+    route_topk(ra, row, row + 1, lane);
+}
 
 // How many of the 32 keys at `keys` come before this lane's: larger ones, and equal ones in lower lanes.
 __device__ __forceinline__ int rank_of(const uint32_t* keys, uint32_t mine, int lane) {
@@ -254,19 +273,38 @@ __device__ __forceinline__ int rank_of(const uint32_t* keys, uint32_t mine, int 
 
 // Top-k of one row and the weights, one warp: what route_topk writes, in fewer steps and less code.
 // The k-th largest of the lanes' own largest keys is a lower bound of the k-th largest key; few keys
-// reach it, and their ranks among each other are counted.  buf: 96 words, then E keys.
+// reach it, and their ranks among each other are counted.  tagged: the row's logits, waited for.
+// buf: 96 words, then E keys.  False: gave up, the same in every lane.
 constexpr int kTopkWords = 96;
-__device__ __forceinline__ void topk_row(const RouteArgs& ra, int row, int lane, uint32_t* buf) {
+__device__ __forceinline__ bool topk_row(const RouteArgs& ra, const uint64_t* tagged, uint32_t call, uint64_t limit_ns,
+                                         int row, int lane, uint32_t* buf) {
     uint32_t* keys = buf + kTopkWords;
     uint32_t top = 0, nonfinite = 0;
-#pragma unroll 8
-    for (int e = lane; e < ra.E; e += 32) {
-        const float z = finish_logit_v(__ldcg(ra.logits + (int64_t)row * ra.E + e), ra.bias != nullptr,
-                                       ra.bias ? __ldg(ra.bias + e) : 0.0f);
-        nonfinite += !isfinite(z);
-        const uint32_t key = order_key(z);
-        keys[e] = key;
-        top = max(top, key);
+    const uint64_t t0 = globaltimer_ns();
+    constexpr int kN = 8;
+    for (int e0 = lane; e0 - lane < ra.E; e0 += 32 * kN) {
+        float bias[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) bias[i] = ra.bias && e0 + 32 * i < ra.E ? __ldg(ra.bias + e0 + 32 * i) : 0.0f;
+        uint64_t v[kN];
+        for (;;) {
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = e0 + 32 * i < ra.E ? ld_tagged(tagged + e0 + 32 * i) : (uint64_t)call << 32;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) all = all && (uint32_t)(v[i] >> 32) == call;
+            if (__all_sync(0xffffffffu, all)) break;
+            if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            if (e0 + 32 * i >= ra.E) continue;
+            const float z = finish_logit_v(__uint_as_float((uint32_t)v[i]), ra.bias != nullptr, bias[i]);
+            nonfinite += !isfinite(z);
+            const uint32_t key = order_key(z);
+            keys[e0 + 32 * i] = key;
+            top = max(top, key);
+        }
     }
     buf[lane] = top;
     buf[32 + lane] = 0;   // candidates' keys
@@ -292,8 +330,8 @@ __device__ __forceinline__ void topk_row(const RouteArgs& ra, int row, int lane,
         }
     }
     if (count > 32) {
-        topk_slow(ra, row, lane);
-        return;
+        topk_slow(ra, tagged, row, lane);
+        return true;
     }
     __syncwarp();
     const uint32_t key = buf[32 + lane], id = buf[64 + lane];
@@ -309,6 +347,7 @@ __device__ __forceinline__ void topk_row(const RouteArgs& ra, int row, int lane,
                on ? buf[lane] : 0u);
     nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
     if (lane == 0) status_add(ra.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
+    return true;
 }
 
 // x into shared memory: as it is, or as e4m3 codes and scales per block of 128 (fp8.cuh).
@@ -355,35 +394,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, c = lane & 3;
     const int G = gridDim.x, cta = blockIdx.x;
     const uint64_t limit = a.wait_ns ? a.wait_ns : kWaitLimitNs;
-    uint32_t round1 = 0, round2 = 0;   // thread 0's
-    if (tid == 0) {   // this CTA's own arrivals are missing: neither round can have ended
-        round1 = ld_round(a.counters);
-        round2 = ld_round(a.counters + 1);
-    }
+    // Rounds of the down step's barrier: a counter each for the two calls, as only one of them numbers its
+    // logits.  This CTA's own arrival is missing: the round cannot have ended.
+    uint64_t* counter = a.counters + (a.given ? 0 : 1);
+    const int tasks = a.given ? 0 : ((a.E - cta + G - 1) / G) * a.R;   // logits of this CTA
+    const uint64_t round = tid == 0 || (lane == 0 && kWarps - 1 - warp < tasks) ? ld_round(counter) : 0;
     const uint8_t *wg = static_cast<const uint8_t*>(a.wg), *wu = static_cast<const uint8_t*>(a.wu),
                   *wd = static_cast<const uint8_t*>(a.wd), *sg = static_cast<const uint8_t*>(a.sg),
                   *su = static_cast<const uint8_t*>(a.su), *sd = static_cast<const uint8_t*>(a.sd);
     const int utiles = a.I / 8, stiles = a.Is / 8, dtiles = a.H / 16, np = a.R * a.k;
 
-    // ---- step 1: logits; the shared expert's weights, which do not depend on them, to L2
+    // ---- step 1: logits
     int my_e = -1;         // given: lane j of warp r holds slot j of row r
     float my_w = 0.0f;
     if (a.given && warp < a.R && lane < a.k) {
         my_e = __ldg(a.topk_idx + warp * a.k + lane);
         my_w = __ldg(a.topk_w + warp * a.k + lane);
     }
-    if (tid == 0) {
-        const uint32_t gb = 8u * a.H * kES, db = 16u * a.Is * kES;
-        for (int t = cta; t < stiles; t += G) {
-            prefetch_l2(sg + (int64_t)t * gb, gb);
-            prefetch_l2(su + (int64_t)t * gb, gb);
-        }
-        for (int t = cta; t < dtiles; t += G) prefetch_l2(sd + (int64_t)t * db, db);
-    }
-    if (!a.given) {   // the last warps first: the first ones stage x meanwhile
-        const int tasks = ((a.E - cta + G - 1) / G) * a.R;
-        for (int i = kWarps - 1 - warp; i < tasks; i += kWarps) expert_logit(a, cta + i / a.R * G, i % a.R, lane);
-    }
+    // the last warps first: the first ones stage x meanwhile
+    for (int i = kWarps - 1 - warp; i < tasks; i += kWarps)
+        expert_logit(a, cta + i / a.R * G, i % a.R, lane, call_number(round));
     stage_x<FP8>(a, sx);
     for (int i = tid; i < a.E; i += kThreads) s.mask[i] = 0;
     const HPlan hp = h_plan<FP8>(a.R, a.k, a.I, a.Is);
@@ -391,14 +421,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         for (int i = tid; i < (kMaxPairs + 1) * kTokenRows; i += kThreads) (&s.hrow[0][0])[i] = 0;
     if (tid < kMaxExperts / 32) s.used[tid] = 0;
     if (tid < MOE_STATUS_WORDS) s.scratch[tid] = 0;
-    if (a.given) {
-        __syncthreads();
-    } else if (!grid_barrier(a.counters, round1, limit, &s.ok)) {
-        if (tid == 0) {
-            status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
-            arrive(a.counters + 1);   // the barrier that this CTA will not reach
+    if (tid == 0) {
+        s.ok = 1;
+        s.call = call_number(round);
+    }
+    __syncthreads();
+
+    // the shared expert's weights to L2
+    if (tid == kThreads - 1) {
+        const uint32_t gb = 8u * a.H * kES, db = 16u * a.Is * kES;
+        for (int t = cta; t < stiles; t += G) {
+            prefetch_l2(sg + (int64_t)t * gb, gb);
+            prefetch_l2(su + (int64_t)t * gb, gb);
         }
-        return;
+        for (int t = cta; t < dtiles; t += G) prefetch_l2(sd + (int64_t)t * db, db);
     }
 
     // ---- step 2: the experts of each row and the list of all of them
@@ -415,9 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             ra.topk_idx = s.idx;
             ra.topk_w = s.w;
             ra.status = cta == 0 ? a.status : s.scratch;
-            topk_row(ra, warp, lane, reinterpret_cast<uint32_t*>(sx + a.arena) + warp * (((a.E + 3) & ~3) + kTopkWords));   // the ring is idle
+            uint32_t* buf = reinterpret_cast<uint32_t*>(sx + a.arena) + warp * (((a.E + 3) & ~3) + kTopkWords);   // the ring is idle
+            const bool got = topk_row(ra, a.tagged + warp * kMaxExperts, s.call, limit, warp, lane, buf);
             __syncwarp();
-            if (lane < a.k) {
+            if (!got) {
+                s.ok = 0;
+            } else if (lane < a.k) {
                 my_e = s.idx[warp * a.k + lane];
                 my_w = s.w[warp * a.k + lane];
                 if (cta == 0) {
@@ -428,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         }
         const bool good = lane < a.k && my_e >= 0 && my_e < a.E;
         const uint32_t ok = __ballot_sync(0xffffffffu, good);
-        same = __match_any_sync(0xffffffffu, good ? my_e : -1 - lane);
+        same = 1u << lane;
+        if (a.given) same = __match_any_sync(0xffffffffu, good ? my_e : -1 - lane);
         if (good && lane == __ffs(same) - 1) {
             atomicOr(&s.mask[my_e], 1u << warp);
             atomicOr(&s.used[my_e >> 5], 1u << (my_e & 31));
@@ -450,6 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         }
     }
     __syncthreads();
+    if (!s.ok) {
+        if (tid == 0) {
+            status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
+            arrive(counter);   // the barrier that this CTA will not reach
+        }
+        return;
+    }
     // an expert's place in the list: touched experts below it.  Lane i has word i of `used`.
     const uint32_t word = s.used[lane];
     int upto = __popc(word);
@@ -695,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     float* wsc = reinterpret_cast<float*>(sx + hp.wscales);
     const bool early = FP8 && STAGED && cta < dtiles && tid < items;   // the first turn's are loaded before the barrier
     const float first_sc = early ? scale_at(cta, tid) : 0.0f;
-    if (!grid_barrier(a.counters + (a.given ? 0 : 1), a.given ? round1 : round2, limit, &s.ok)) {
+    if (!grid_barrier(counter, round, limit, &s.ok)) {
         cp_async_wait<0>();
         if (tid == 0) status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1);
         return;

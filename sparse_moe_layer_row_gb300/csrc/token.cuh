@@ -19,11 +19,12 @@ struct TokenArgs {
     const void *wg, *wu, *wd, *sg, *su, *sd;
     // e4m3: their scales per 128 x 128 block
     const float *cg, *cu, *cd, *csg, *csu, *csd;
-    float* logits;                // [R, E]
+    float* logits;                // [R, E], for rows of many equal ones
     int32_t* topk_idx;            // [R, k]
     float* topk_w;
     void* h;                      // 4 bytes for each of R (k I + Is) values
-    uint32_t* counters;           // of the two grid barriers
+    uint64_t* counters;           // of the grid barrier: given routing, whole pass
+    uint64_t* tagged;             // [8, kMaxExperts] logits with the number of their call
     uint32_t* status;
     __nv_bfloat16* y;             // [R, H]
     float* y_f32;                 // or NULL
