@@ -156,17 +156,21 @@ __device__ __forceinline__ void warp_topk(const uint32_t (&key)[NI], const uint3
     }
 }
 
-// Softmax over the k selected logits (lane j < k holds rank j) and the store.
-__device__ __forceinline__ void write_topk(int32_t* idx_out, float* w_out, int k, int lane,
-                                           uint32_t my_id, uint32_t my_key) {
+// Softmax over the k selected logits (lane j < k holds rank j): this lane's weight.
+__device__ __forceinline__ float topk_weight(int k, int lane, uint32_t my_key) {
     const float zj = key_value(my_key);
     const float m = __shfl_sync(0xffffffffu, zj, 0);
     const float aj = lane < k ? exp_c(__fsub_rn(zj, m)) : 0.0f;
     float S = 0.0f;
     for (int j = 0; j < k; ++j) S = __fadd_rn(S, __shfl_sync(0xffffffffu, aj, j));
+    return __fdiv_rn(aj, S);
+}
+__device__ __forceinline__ void write_topk(int32_t* idx_out, float* w_out, int k, int lane,
+                                           uint32_t my_id, uint32_t my_key) {
+    const float w = topk_weight(k, lane, my_key);
     if (lane < k) {
         idx_out[lane] = (int32_t)my_id;
-        w_out[lane] = __fdiv_rn(aj, S);
+        w_out[lane] = w;
     }
 }
 

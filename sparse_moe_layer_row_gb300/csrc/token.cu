@@ -259,27 +259,43 @@ __device__ __noinline__ void topk_slow(const RouteArgs& ra, const uint64_t* tagg
     route_topk(ra, row, row + 1, lane);
 }
 
-// How many of the 32 keys at `keys` come before this lane's: larger ones, and equal ones in lower lanes.
-__device__ __forceinline__ int rank_of(const uint32_t* keys, uint32_t mine, int lane) {
+// How many of the first n keys at `keys` (a multiple of 4 is read) come before this lane's: larger
+// ones, and equal ones in lower lanes.
+__device__ __forceinline__ int rank_of(const uint32_t* keys, uint32_t mine, int lane, int n) {
     int rank = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint4 o = *reinterpret_cast<const uint4*>(keys + 4 * i);
-        rank += (o.x > mine || (o.x == mine && 4 * i < lane)) + (o.y > mine || (o.y == mine && 4 * i + 1 < lane)) +
-                (o.z > mine || (o.z == mine && 4 * i + 2 < lane)) + (o.w > mine || (o.w == mine && 4 * i + 3 < lane));
+#pragma unroll 2
+    for (int i = 0; i < n; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(keys + i);
+        rank += (o.x > mine || (o.x == mine && i < lane)) + (o.y > mine || (o.y == mine && i + 1 < lane)) +
+                (o.z > mine || (o.z == mine && i + 2 < lane)) + (o.w > mine || (o.w == mine && i + 3 < lane));
     }
     return rank;
 }
+// How many of the 32 keys at `keys` are at least this lane's.
+__device__ __forceinline__ int at_least(const uint32_t* keys, uint32_t mine) {
+    int n[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 o = *reinterpret_cast<const uint4*>(keys + 4 * i);
+        n[0] += o.x >= mine;
+        n[1] += o.y >= mine;
+        n[2] += o.z >= mine;
+        n[3] += o.w >= mine;
+    }
+    return n[0] + n[1] + (n[2] + n[3]);
+}
 
-// Top-k of one row and the weights, one warp: what route_topk writes, in fewer steps and less code.
+// Top-k of one row, one warp: the order of route_topk, in fewer steps and less code.  Lane j gets the
+// j-th chosen expert and its key; the weights can wait (topk_weight).
 // The k-th largest of the lanes' own largest keys is a lower bound of the k-th largest key; few keys
 // reach it, and their ranks among each other are counted.  tagged: the row's logits, waited for.
-// buf: 96 words, then E keys.  False: gave up, the same in every lane.
+// buf: 96 words, then E keys.
+enum { kGaveUp = 0, kChosen = 1, kWritten = 2 };   // kWritten: route_topk did it, to ra's outputs
 constexpr int kTopkWords = 96;
-__device__ __forceinline__ bool topk_row(const RouteArgs& ra, const uint64_t* tagged, uint32_t call, uint64_t limit_ns,
-                                         int row, int lane, uint32_t* buf) {
+__device__ __forceinline__ int topk_row(const RouteArgs& ra, const uint64_t* tagged, uint32_t call, uint64_t limit_ns,
+                                        int row, int lane, uint32_t* buf, uint32_t& id, uint32_t& key, uint32_t& nonfinite) {
     uint32_t* keys = buf + kTopkWords;
-    uint32_t top = 0, nonfinite = 0;
+    uint32_t top = 0;
     const uint64_t t0 = globaltimer_ns();
     constexpr int kN = 8;
     for (int e0 = lane; e0 - lane < ra.E; e0 += 32 * kN) {
@@ -294,36 +310,35 @@ __device__ __forceinline__ bool topk_row(const RouteArgs& ra, const uint64_t* ta
 #pragma unroll
             for (int i = 0; i < kN; ++i) all = all && (uint32_t)(v[i] >> 32) == call;
             if (__all_sync(0xffffffffu, all)) break;
-            if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return false;
+            if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) return kGaveUp;
         }
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             if (e0 + 32 * i >= ra.E) continue;
             const float z = finish_logit_v(__uint_as_float((uint32_t)v[i]), ra.bias != nullptr, bias[i]);
             nonfinite += !isfinite(z);
-            const uint32_t key = order_key(z);
-            keys[e0 + 32 * i] = key;
-            top = max(top, key);
+            const uint32_t o = order_key(z);
+            keys[e0 + 32 * i] = o;
+            top = max(top, o);
         }
     }
     buf[lane] = top;
     buf[32 + lane] = 0;   // candidates' keys
     __syncwarp();
-    const uint32_t kth = __ballot_sync(0xffffffffu, rank_of(buf, top, lane) == ra.k - 1);
-    const uint32_t bound = __shfl_sync(0xffffffffu, top, __ffs(kth) - 1);
+    const uint32_t bound = __reduce_max_sync(0xffffffffu, at_least(buf, top) >= ra.k ? top : 0u);
     int count = 0;
     for (int e0 = 0; e0 < ra.E; e0 += 128) {   // in ascending order of the experts
-        uint32_t key[4];
+        uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) key[i] = e0 + 32 * i + lane < ra.E ? keys[e0 + 32 * i + lane] : 0u;
+        for (int i = 0; i < 4; ++i) o[i] = e0 + 32 * i + lane < ra.E ? keys[e0 + 32 * i + lane] : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = e0 + 32 * i + lane;
-            const bool in = e < ra.E && key[i] >= bound;
+            const bool in = e < ra.E && o[i] >= bound;
             const uint32_t b = __ballot_sync(0xffffffffu, in);
             const int at = count + __popc(b & ((1u << lane) - 1));
             if (in && at < 32) {
-                buf[32 + at] = key[i];
+                buf[32 + at] = o[i];
                 buf[64 + at] = (uint32_t)e;
             }
             count += __popc(b);
@@ -331,23 +346,20 @@ __device__ __forceinline__ bool topk_row(const RouteArgs& ra, const uint64_t* ta
     }
     if (count > 32) {
         topk_slow(ra, tagged, row, lane);
-        return true;
+        return kWritten;
     }
     __syncwarp();
-    const uint32_t key = buf[32 + lane], id = buf[64 + lane];
-    const int rank = rank_of(buf + 32, key, lane);
+    const uint32_t k1 = buf[32 + lane], e1 = buf[64 + lane];
+    const int rank = rank_of(buf + 32, k1, lane, count);
     __syncwarp();
-    if (lane < count) {
-        buf[rank] = key;
-        buf[64 + rank] = id;   // each lane has read its own
+    if (lane < count) {   // each lane has read its own
+        buf[rank] = k1;
+        buf[64 + rank] = e1;
     }
     __syncwarp();
-    const bool on = lane < ra.k;
-    write_topk(ra.topk_idx + (int64_t)row * ra.k, ra.topk_w + (int64_t)row * ra.k, ra.k, lane, on ? buf[64 + lane] : 0u,
-               on ? buf[lane] : 0u);
-    nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
-    if (lane == 0) status_add(ra.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
-    return true;
+    id = buf[64 + lane];
+    key = lane < ra.k ? buf[lane] : 0u;
+    return kChosen;
 }
 
 // x into shared memory: as it is, or as e4m3 codes and scales per block of 128 (fp8.cuh).
@@ -439,6 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
 
     // ---- step 2: the experts of each row and the list of all of them
     uint32_t same = 0;     // slots of the row with the same expert
+    uint32_t my_key = 0, nonfinite = 0;
+    bool weigh = false;    // the row's weights are still to be formed
+    int my_l = 0;          // place in the list of experts
     if (warp < a.R) {
         if (!a.given) {
             RouteArgs ra{};
@@ -452,18 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             ra.topk_w = s.w;
             ra.status = cta == 0 ? a.status : s.scratch;
             uint32_t* buf = reinterpret_cast<uint32_t*>(sx + a.arena) + warp * (((a.E + 3) & ~3) + kTopkWords);   // the ring is idle
-            const bool got = topk_row(ra, a.tagged + warp * kMaxExperts, s.call, limit, warp, lane, buf);
+            uint32_t id;
+            const int got = topk_row(ra, a.tagged + warp * kMaxExperts, s.call, limit, warp, lane, buf, id, my_key, nonfinite);
             __syncwarp();
-            if (!got) {
+            if (got == kGaveUp) {
                 s.ok = 0;
             } else if (lane < a.k) {
-                my_e = s.idx[warp * a.k + lane];
-                my_w = s.w[warp * a.k + lane];
-                if (cta == 0) {
-                    a.topk_idx[warp * a.k + lane] = my_e;
-                    a.topk_w[warp * a.k + lane] = my_w;
-                }
+                my_e = got == kChosen ? (int)id : s.idx[warp * a.k + lane];
+                my_w = got == kChosen ? 0.0f : s.w[warp * a.k + lane];
             }
+            weigh = got == kChosen;
         }
         const bool good = lane < a.k && my_e >= 0 && my_e < a.E;
         const uint32_t ok = __ballot_sync(0xffffffffu, good);
@@ -473,14 +486,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
             atomicOr(&s.mask[my_e], 1u << warp);
             atomicOr(&s.used[my_e >> 5], 1u << (my_e & 31));
         }
-        if (cta == 0 && lane == 0) {
+        if (a.given && cta == 0 && lane == 0) {
             status_add(a.status, MOE_STATUS_BAD_EXPERT_ID, a.k - __popc(ok));
             status_add(a.status, MOE_STATUS_EMPTY_ROWS, ok == 0);
         }
         if (!good) my_e = -1;
         // an expert in several slots: their weights in slot order, in the first of them
         uint32_t rest = same & (same - 1);
-        if (__any_sync(0xffffffffu, rest != 0)) {
+        if (a.given && __any_sync(0xffffffffu, rest != 0)) {
             float sum = my_w;
             for (int j = 0; j < 32; ++j) {
                 const float o = __shfl_sync(0xffffffffu, my_w, j);
@@ -520,11 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         }
     }
     if (warp < a.R) {
-        const int l = place(my_e >= 0 ? my_e : 0);
+        my_l = place(my_e >= 0 ? my_e : 0);
         if (my_e >= 0 && lane == __ffs(same) - 1) {
-            s.wt[l][warp] = my_w;
-            s.slot[l][warp] = (uint8_t)lane;
-            s.hrow[l][warp] = (uint16_t)((hp.routed + (warp * a.k + lane) * hp.rstr) / 64);
+            s.wt[my_l][warp] = my_w;
+            s.slot[my_l][warp] = (uint8_t)lane;
+            s.hrow[my_l][warp] = (uint16_t)((hp.routed + (warp * a.k + lane) * hp.rstr) / 64);
         }
     }
     if (tid < kTokenRows) {   // the shared expert follows
@@ -665,6 +678,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
         float sc_next = scales_of(lu);
 #pragma unroll 1
         for (int i = 0; i < depth - 1; ++i) copy_next();
+        // with tiles on their way: the rows' weights, which the down step needs
+        if (!a.given && warp < a.R) {
+            const float w = weigh ? topk_weight(a.k, lane, my_key) : my_w;
+            if (lane < a.k) {
+                s.wt[my_l][warp] = w;
+                if (cta == 0) {
+                    a.topk_idx[warp * a.k + lane] = my_e;
+                    a.topk_w[warp * a.k + lane] = w;
+                }
+            }
+            nonfinite = __reduce_add_sync(0xffffffffu, nonfinite);
+            if (weigh && cta == 0 && lane == 0) status_add(a.status, MOE_STATUS_NONFINITE_LOGITS, nonfinite);
+        }
         const uint32_t xrow = smem_u32(sx) + gi * x_stride<FP8>(a.H) + 16 * c;
         const bool on = gi < a.R;
         int pb = 0;
