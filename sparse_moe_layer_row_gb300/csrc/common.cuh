@@ -136,7 +136,8 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     return t;
 }
 
-// Programmatic dependent launch.  Every kernel of this library is launched
+// Programmatic dependent launch.  Every kernel of this library (but k_token, which is
+// launched cooperatively: the attribute changed nothing there) is launched
 // with programmatic stream serialization, so it may be scheduled while the
 // kernel before it on the stream is still running.  The rule that keeps this
 // safe: a thread calls pdl_wait() -- which returns once the preceding kernel
@@ -148,7 +149,9 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // scatter; it may be read early because the kernel between, the gate/up GEMM,
 // does not write it and triggers only after its own wait, by when the scatter has
 // completed.  A gate/up kernel's trigger must therefore stay behind its wait, and
-// no kernel that writes the list may come between.  pdl_trigger()
+// no kernel that writes the list may come between.  k_i8_tiles reads the codes and
+// scales that its call was given early for the same reason: the kernel between is
+// k_i8_widen.  pdl_trigger()
 // lets the next kernel be scheduled; it is called right after the wait, so at
 // most two kernels of a stream overlap.  The down GEMM on CTA pairs
 // (k_down_pair, bf16 calls over kStreamDownRows rows) does not call it: the

@@ -10,6 +10,9 @@
 // rows: m16n8k32 on int8), the rows its N.  Operands go from global memory to registers, two blocks at a time; K is
 // permuted inside a block, alike in both operands, so that a lane's are 16-byte loads and
 // four codes of a row make one MMA's operand.  The warps' sums are added through shared memory.
+// Bound by the round trip to memory (1 x 2048 x 2048 2.1 us, floor 0.6; 8 x 32768 x 2048 13.7 us,
+// 4.9 TB/s of W), with more rows by the conversions and mma.sync (32 x 4096 x 2048 4.5 us,
+// 77 x 1000 x 1104 4.6); mma.sync on int8 there took 911 us for 8192 x 4096 x 2048.
 //
 // k_i8_tiles: tcgen05 kind::f16 (the bf16 rate).  A CTA pair (cta_group::2) takes 256 rows of A by up
 // to 256 of B, where B is the operand with fewer rows:
@@ -30,6 +33,15 @@
 //                   accumulators into registers at once (`tempty` of rank 0), so that the next
 //                   tile's MMAs run while they scale and store
 // Every wait is bounded, and drains follow an abort, as in gemm_pair.cu.
+//
+// 8192 x 4096 x 2048: 77 us, 1.79 PFLOP/s (floor 73 at the measured burst rate; called back to back
+// for long, at the power limit's clock, 88: 81 there).  Of it some 3 us are k_i8_widen's, which reads
+// 8 MB and writes 17 (x, the larger operand, took 6; to start on what is widened already, the tiles would
+// need flags that a call clears first), 512 clocks per 64 of K the tensor core's, and the last
+// tile's epilogue.  Issued by one lane in a branch of its own the 64 of K took 560: the whole warp runs
+// the loop.  Two converter warpgroups instead of one (98 us against 97 at that stage), the wait for the
+// tensor memory stores deferred by a stage (95) and four conversions in flight (2048 x 2048 x 2048 26
+// us against 20) gained nothing.  2048 x 2048 x 2048: 19.4 us, one round of 64 units on 76 pairs.
 #include <cstring>
 #include <type_traits>
 
@@ -572,7 +584,9 @@ cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CU
 }
 
 // By what the two kernels were measured to take (ns): the rows kernel 1800 + CTAs (3.5 + 0.0046 K)
-// with 17 to 32 rows per CTA, the tiles 7800 + 265 per 64 of K and round of units.
+// with 17 to 32 rows per CTA, the tiles 7800 + 265 per 64 of K and round of units.  (Both sides, us:
+// 64 x 4096 x 2048 8.4 and 17.1; 256 x 2048 x 2048 13.6 and 16.7; 256 x 4096 x 2048 26 and 17.3;
+// 32 x 4096 x 7168 13.3 and 38.  Within 10% of the border either may be the faster one.)
 bool i8_rows_applies(int R, int N, int K) {
     if (R <= 16) return true;
     if (R > 65535 * kRowsPerCta) return false;   // the grid's y: row tiles

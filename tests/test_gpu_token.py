@@ -280,6 +280,26 @@ def test_new_rows_every_call():
         assert torch.equal(y, w.to(BF))
 
 
+def test_call_numbers_wrap():
+    """The counter behind the logits' call numbers, set to shortly before their 32 bits wrap (a
+    day's calls): rows that were never used before, and other rows each call."""
+    c = Case("bf16", 8, E=32, k=4, H=512, seed=75)
+    xs = [randn(8, 512, seed=300 + i).to(BF) for i in range(8)]
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    for start in ((1 << 32) - 4, (1 << 33) - 5, (1 << 53) - 4):
+        c.layer.workspace.zero_()
+        c.layer.workspace[1024:2048].view(torch.int64)[1] = start * 1024
+        for i, x in enumerate(xs):
+            R = 1 if i < 3 else 8
+            c.x, c.R = x[:R].contiguous(), R
+            y, y32, idx, wt = c.routed()
+            ri, rw = c.layer.route(c.x, off if R == 8 else torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+            torch.cuda.synchronize()
+            assert torch.equal(idx, ri) and torch.equal(wt, rw)
+            c.check(y, y32, c.reference(idx, wt))
+        c.status_clean()
+
+
 def test_in_place_and_rows_behind():
     c = Case("bf16", 3, seed=58)
     want = c.routed()[0]
