@@ -172,11 +172,12 @@ bool moe::encode_fp8(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, 
                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-bool moe::encode_i8_tiles(CUtensorMap* a, CUtensorMap* b, const void* codes, const void* wide, int M, int C, int K) {
+bool moe::encode_i8_tiles(CUtensorMap* a, CUtensorMap* b, const void* codes, const void* wide, int M, int C, int K,
+                          int width) {
     const uint64_t da[2] = {(uint64_t)K, (uint64_t)M}, db[2] = {(uint64_t)K, (uint64_t)C};
-    const uint32_t box[2] = {64, 128};
-    return encode_plain(a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, 2, da, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
-           encode_plain(b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, wide, 2, db, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint32_t box_a[2] = {128, 128}, box_b[2] = {64, (uint32_t)width / 2};
+    return encode_plain(a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, 2, da, box_a, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_plain(b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, wide, 2, db, box_b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 moe_status moe::set_error(moe_status s, const char* msg) {

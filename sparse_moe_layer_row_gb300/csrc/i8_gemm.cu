@@ -16,32 +16,33 @@
 //
 // k_i8_tiles: tcgen05 kind::f16 (the bf16 rate).  A CTA pair (cta_group::2) takes 256 rows of A by up
 // to 256 of B, where B is the operand with fewer rows:
-//   A (M = 256)  128 rows per CTA: raw codes by TMA (8 KB per 64 of K), which the converter warps
+//   A (M = 256)  128 rows per CTA: raw codes by TMA (16 KB per 128 of K), which the converter warps
 //                turn into fp16 in tensor memory, from where the MMA reads A
 //   B (N <= 256) fp16, half of the rows per CTA, by TMA.  k_i8_widen writes it to the workspace
 //                first: every tile of A needs it, and converting it there would double the
 //                shared-memory traffic of the loop
-// so that A is read as bytes and never written, and an SM's shared memory carries 48 KB per 64 of
-// K (512 clocks of the tensor core).  Tensor memory holds the accumulators (256 columns) and eight A
-// slots of 32, one per stage.  Roles, 512 threads per CTA:
-//   warps 0, 3      lane 0: TMA producers of A (`afull`) and of B (`bfull`), ring of 8 stages
+// so that A is read as bytes and never written, and an SM's shared memory carries 96 KB per 128 of
+// K (1024 clocks of the tensor core).  Tensor memory holds the accumulators (256 columns) and four A
+// slots of 64, one per stage.  Roles, 512 threads per CTA:
+//   warps 0, 3      lane 0: TMA producers of A (`afull`) and of B (`bfull`), ring of 4 stages
 //   warp 1          tensor memory; in rank 0, issues the MMAs and commits (`empty` of both ranks:
 //                   the stage and its A slot; `tfull`)
 //   warp 2 lane 0   forwarder: the CTA's B of a stage has landed -> rank 0's `ready`
-//   warps 4..7      converters: a row of 64 codes per thread -> rank 0's `ready`
+//   warps 4..7      converters: 128 codes of a row per thread -> rank 0's `ready`
 //   warps 8..15     epilogue: 32 rows of A (a lane each) by 128 of B per warp.  They take the
 //                   accumulators into registers at once (`tempty` of rank 0), so that the next
-//                   tile's MMAs run while they scale and store
+//                   tile's MMAs run while they scale and store.
 // Every wait is bounded, and drains follow an abort, as in gemm_pair.cu.
 //
-// 8192 x 4096 x 2048: 77 us, 1.79 PFLOP/s (floor 73 at the measured burst rate; called back to back
+// 8192 x 4096 x 2048: 78 us, 1.75 PFLOP/s (floor 73 at the measured burst rate; called back to back
 // for long, at the power limit's clock, 88: 81 there).  Of it some 3 us are k_i8_widen's, which reads
-// 8 MB and writes 17 (x, the larger operand, took 6; to start on what is widened already, the tiles would
-// need flags that a call clears first), 512 clocks per 64 of K the tensor core's, and the last
-// tile's epilogue.  Issued by one lane in a branch of its own the 64 of K took 560: the whole warp runs
-// the loop.  Two converter warpgroups instead of one (98 us against 97 at that stage), the wait for the
-// tensor memory stores deferred by a stage (95) and four conversions in flight (2048 x 2048 x 2048 26
-// us against 20) gained nothing.  2048 x 2048 x 2048: 19.4 us, one round of 64 units on 76 pairs.
+// 8 MB and writes 17 (x, the larger operand, took 6; to start on what is widened already, the tiles
+// would need flags that a call clears first), 512 clocks per 64 of K the tensor core's, and the last
+// tile's epilogue.  Issued by one lane in a branch of its own the 64 of K took 560: the whole warp
+// runs the loop.  Stages of 64 of K cost 230 ns each whatever the tile's width (rows of 64 bytes are
+// slow to copy), those of 128 some 270.  Two converter warpgroups, the wait for the tensor memory
+// stores deferred by a stage, four conversions in flight and prefetches of A to L2 gained nothing
+// where stages were of 64.  2048 x 2048 x 2048: 20 us, one round of 64 units on 76 pairs.
 #include <cstring>
 #include <type_traits>
 
@@ -183,8 +184,8 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
-constexpr int kStages = 8, kThreads = 512;
-constexpr int kRaw = 128 * 64, kBTile = 128 * 128;   // bytes per stage: codes of A, fp16 of B
+constexpr int kStages = 4, kThreads = 512;
+constexpr int kStepK = 128, kRaw = 128 * 128, kBHalf = 128 * 128, kBTile = 2 * kBHalf;   // bytes per stage: codes of A, fp16 of B
 constexpr int kStageBytes = kRaw + kBTile;
 constexpr int kBOff = kStages * kRaw;                // tiles of B behind the codes (1 KB boundaries)
 constexpr int kScaleOff = kStages * kStageBytes;     // float [8][128]: xs of an epilogue warp's rows
@@ -192,7 +193,7 @@ constexpr int kBarOff = kScaleOff + 8 * 128 * 4;
 constexpr int kSmem = kBarOff + 512 + 1024;
 constexpr int kACol = 256;                           // A slots behind the accumulators
 constexpr int kTmemCols = 512;
-static_assert(kACol + 32 * kStages <= kTmemCols, "TMEM columns");
+static_assert(kACol + 64 * kStages <= kTmemCols, "TMEM columns");
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(8 * (4 * kStages + 3) + 12 <= 512, "barrier region");
 // registers per thread after the split; the pool is what the CTA was launched with (checked on
@@ -305,7 +306,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
             mbar_init(empty + s, 1);
         }
         mbar_init(tfull, 1);
-        mbar_init(tempty, 2 * 8);   // the epilogue warps of both ranks
+        mbar_init(tempty, 2 * (a.width > 128 ? 8 : 4));   // the epilogue warps of both ranks
         mbar_init(dbar, 1);
         *abort_flag = 0;
         *never = 0;
@@ -319,16 +320,16 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
     // The kernel before this one is k_i8_widen, which let it start after its own wait: all but the
     // widened operand was complete by then, so that only B's producer waits (common.cuh).
 
-    // unit u: rows 256 m .. of A, 256 c .. of B (neighbouring units share rows of B)
-    const int mt = (M + 255) / 256, nunits = mt * ((C + 255) / 256);
+    // unit u: rows 256 m .. of A, `width` c .. of B (neighbouring units share rows of B)
+    const int mt = (M + 255) / 256, nunits = mt * ((C + a.width - 1) / a.width);
     const int nact = active_workers(nunits, (int)cluster_count());   // balanced rounds
     const int ufirst = (int)cluster_id() < nact ? (int)cluster_id() : nunits;
-    const int nkb = (a.K + 63) / 64;
+    const int nkb = (a.K + kStepK - 1) / kStepK;
     auto rows_of = [&](int u, int& m, int& r0) {   // the MMA's N: rows of B of the unit, in 32s
         const int c = u / mt;
         m = u - c * mt;
-        r0 = c * 256;
-        return (min(256, C - r0) + 31) / 32 * 32;
+        r0 = c * a.width;
+        return (min(a.width, C - r0) + 31) / 32 * 32;
     };
     auto give_up = [&]() {
         if (!*abort_flag) { *abort_flag = 1; status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1); }
@@ -356,9 +357,14 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(full + stage, b ? kBTile : kRaw);
-                    if (b) tma_load_2d(sbase + kBOff + stage * kBTile, &tmB, kb * 64, r0 + n / 2 * rank, full + stage);
-                    else tma_load_2d(sbase + stage * kRaw, &tmA, kb * 64, m * 256 + 128 * rank, full + stage);
+                    mbar_expect_tx(full + stage, b ? 128 * a.width : kRaw);
+                    if (b) {
+                        const uint32_t to = sbase + kBOff + stage * kBTile;
+                        tma_load_2d(to, &tmB, kb * kStepK, r0 + n / 2 * rank, full + stage);
+                        tma_load_2d(to + kBHalf, &tmB, kb * kStepK + 64, r0 + n / 2 * rank, full + stage);
+                    } else {
+                        tma_load_2d(sbase + stage * kRaw, &tmA, kb * kStepK, m * 256 + 128 * rank, full + stage);
+                    }
                     ++nfills;
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -397,11 +403,11 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                     }
                     tc_fence_after();
                     const uint64_t bd = smem_desc_sw128(sbase + kBOff + stage * kBTile);
-                    const uint32_t at = tmem + (uint32_t)(kACol + 32 * stage);
+                    const uint32_t at = tmem + (uint32_t)(kACol + 64 * stage);
                     if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
-                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                        for (int kk = 0; kk < 8; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
+                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + (kk >> 2) * (kBHalf >> 4) + 2 * (kk & 3), idesc, (kb | kk) != 0);
                         tc_commit_pair(empty + stage);
                         if (kb == nkb - 1) tc_commit_pair(tfull);
                     }
@@ -433,10 +439,10 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         // -------------------------------------------------------------- converters
-        // Output r of the CTA's 128 per thread: 64 codes of its row (chunk c of 16 at
-        // c ^ ((r >> 1) & 3), the copy's 64-byte swizzle) into lane r of the stage's A slot.
+        // Row r of the CTA's 128 of A per thread: 128 codes (chunk c of 16 at c ^ (r & 7), the copy's
+        // 128-byte swizzle) into lane r of the stage's A slot.
         const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
-        const int r = 32 * (warp & 3) + lane, sw = (r >> 1) & 3;
+        const int r = 32 * (warp & 3) + lane, sw = r & 7;
         const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)kACol;
         int stage = 0;
         uint32_t phase = 0;
@@ -451,9 +457,9 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                     break;
                 }
                 tc_fence_after();
-                const uint8_t* row = base + stage * kRaw + r * 64;
+                const uint8_t* row = base + stage * kRaw + r * 128;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -463,7 +469,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                         widen4(w.z, o[8 * i + 4], o[8 * i + 5]);
                         widen4(w.w, o[8 * i + 6], o[8 * i + 7]);
                     }
-                    tmem_st16(tq + (uint32_t)(32 * stage + 16 * h), o);
+                    tmem_st16(tq + (uint32_t)(64 * stage + 16 * h), o);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -479,20 +485,20 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
         float* xs = reinterpret_cast<float*>(base + kScaleOff) + 128 * (warp - 8);
         uint32_t tphase = 0;
-        for (int u = ufirst; u < nunits; u += nact) {
+        for (int u = half && a.width <= 128 ? nunits : ufirst; u < nunits; u += nact) {
             int m, r0;
             rows_of(u, m, r0);
             const int ra = m * 256 + 128 * rank + 32 * q + lane, rb = r0 + 128 * half;   // this lane's of A; B's first
+            const int n = min(min(a.width - 128 * half, 128), C - rb);   // rows of B of this warp
             const float ls = ra < M ? __ldg(sa + ra) : 0.0f;
             __syncwarp();   // the last tile's scales have been read
 #pragma unroll
-            for (int i = lane; i < 128; i += 32) xs[i] = rb + i < C ? __ldg(sb + rb + i) : 0.0f;
+            for (int i = lane; i < 128; i += 32) xs[i] = i < n ? __ldg(sb + rb + i) : 0.0f;
             __syncwarp();
             const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitLimitNs);
             if (__any_sync(0xffffffffu, !got)) { give_up(); break; }
             tphase ^= 1u;
             tc_fence_after();
-            const int n = min(128, C - rb);   // of B, of this warp
             float v[128];
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
@@ -571,6 +577,7 @@ cudaError_t i8_tiles_set_attributes(int num_sms, int* clusters) {
 
 cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, void* wide, int num_sms,
                             int clusters, cudaStream_t st) {
+    // a.width: set by the caller, which encoded the maps for it
     const bool swap = i8_swapped(a.R, a.N);
     const int64_t n16 = (int64_t)(swap ? a.N : a.R) * a.K / 16;
     int64_t blocks = (n16 + 255) / 256;
@@ -583,17 +590,43 @@ cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CU
     return cudaLaunchKernelEx(&cfg, swap ? k_i8_tiles<true> : k_i8_tiles<false>, ma, mb, a);
 }
 
-// By what the two kernels were measured to take (ns): the rows kernel 1800 + CTAs (3.5 + 0.0046 K)
-// with 17 to 32 rows per CTA, the tiles 7800 + 265 per 64 of K and round of units.  (Both sides, us:
-// 64 x 4096 x 2048 8.4 and 17.1; 256 x 2048 x 2048 13.6 and 16.7; 256 x 4096 x 2048 26 and 17.3;
-// 32 x 4096 x 7168 13.3 and 38.  Within 10% of the border either may be the faster one.)
+// By what the kernels were measured to take (ns): the rows kernel 1800 + CTAs (5.9 + 0.0031 K) with 17
+// to 32 rows per CTA; the tiles 7800 (6500 where a lane holds a row of y) + kStep per 64 of K and round
+// of units.  Narrow tiles leave the tensor core waiting for the converters, but give few rows more
+// pairs.  Measured, us, rows kernel / tiles of 256, 128, 64:
+//    256 x 2048 x 2048   13.5 / 16.6 12.5 11.9       512 x 2048 x 2048   25.2 / 17.3 14.3 14.1
+//    128 x 4096 x 2048   14.6 / 14.1 13.8 13.1      1024 x 4096 x 4096      - / 28.3 32.8 49.1
+//   1000 x 1000 x  992   24.7 / 12.6 10.4 11.3 (the rule's 64 is not the best)
+//   1000 x  512 x  512    9.5 /  9.1  7.1  6.9        64 x 4096 x 7168   23.8 / 30.0 29.1 29.0
+namespace {
+int64_t tiles_ns(int R, int N, int K, int* width) {
+    constexpr int kStep[3] = {265, 200, 195};   // widths 256, 128, 64
+    const int64_t M = R > N ? R : N, C = R > N ? N : R, steps = (K + 63) / 64;
+    int64_t best = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t w = 256 >> i, rounds = ((M + 255) / 256 * ((C + w - 1) / w) + 75) / 76;   // 76 CTA pairs
+        const int64_t ns = (i8_swapped(R, N) ? 6500 : 7800) + rounds * steps * kStep[i];
+        if (i == 0 || ns < best) {
+            best = ns;
+            *width = (int)w;
+        }
+    }
+    return best;
+}
+}  // namespace
+
+int i8_width(int R, int N, int K) {
+    int width = 0;
+    tiles_ns(R, N, K, &width);
+    return width;
+}
+
 bool i8_rows_applies(int R, int N, int K) {
     if (R <= 16) return true;
     if (R > 65535 * kRowsPerCta) return false;   // the grid's y: row tiles
     const int64_t ctas = (int64_t)((N + kCols - 1) / kCols) * ((R + kRowsPerCta - 1) / kRowsPerCta);
-    const int64_t units = (int64_t)((R + 255) / 256) * ((N + 255) / 256);
-    const int64_t rounds = (units + 75) / 76;   // 76 CTA pairs
-    return 1800 + ctas * (35000 + 46 * (int64_t)K) / 10000 <= 7800 + rounds * ((K + 63) / 64) * 265;
+    int width;
+    return 1800 + ctas * (59000 + 31 * (int64_t)K) / 10000 <= tiles_ns(R, N, K, &width);
 }
 
 cudaError_t launch_i8_rows(const I8GemmArgs& a, cudaStream_t st) {

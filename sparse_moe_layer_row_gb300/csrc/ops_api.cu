@@ -254,7 +254,7 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
     if (workspace_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype, static_cast<uint32_t*>(workspace),
-                 aligned(y, 32) && row_stride * (int64_t)dtype_size(dtype) % 32 == 0};
+                 aligned(y, 32) && row_stride * (int64_t)dtype_size(dtype) % 32 == 0, i8_width(R, N, K)};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (i8_rows_applies(R, N, K)) return launched(launch_i8_rows(a, st), "gemm launch");
     int sms = 0, clusters = 0;
@@ -262,7 +262,7 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
     const bool swap = i8_swapped(R, N);
     void* wide = static_cast<uint8_t*>(workspace) + kWideOffset;
     CUtensorMap ma, mb;
-    if (!encode_i8_tiles(&ma, &mb, swap ? xq : wq, wide, swap ? R : N, swap ? N : R, K))
+    if (!encode_i8_tiles(&ma, &mb, swap ? xq : wq, wide, swap ? R : N, swap ? N : R, K, a.width))
         return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     return launched(launch_i8_tiles(a, ma, mb, wide, sms, clusters, st), "gemm launch");
 }

@@ -37,6 +37,7 @@ struct I8GemmArgs {
     int ydtype;
     uint32_t* status;
     int y_vec;                // rows of y begin on 32 bytes
+    int width;                // rows of B in a tile: 256, 128 or 64
 };
 // Few rows or little work: k_i8_rows, which needs no workspace.
 bool i8_rows_applies(int R, int N, int K);
@@ -44,13 +45,14 @@ cudaError_t launch_i8_rows(const I8GemmArgs&, cudaStream_t);
 // Else k_i8_widen and k_i8_tiles.  The operand with fewer rows (B) is widened to fp16 ahead, in
 // `wide`, the other one (A) as it is read.
 inline bool i8_swapped(int R, int N) { return N < R; }   // A: x, B: W; else A: W, B: x
-// a: codes of A in 64 x 128 boxes (64-byte swizzle), b: `wide` in 64 x 128 boxes (128-byte swizzle);
+int i8_width(int R, int N, int K);   // rows of B in a tile
+// a: codes of A in boxes of 128 x 128, b: `wide` in 64 x width / 2, both with the 128-byte swizzle;
 // clusters: CTA pairs resident at once.
 cudaError_t i8_tiles_set_attributes(int num_sms, int* clusters);
 cudaError_t launch_i8_tiles(const I8GemmArgs&, const CUtensorMap& a, const CUtensorMap& b, void* wide, int num_sms,
                             int clusters, cudaStream_t);
 // The maps of A [M, K] and B [C, K] (implemented in api.cu).
-bool encode_i8_tiles(CUtensorMap* a, CUtensorMap* b, const void* codes, const void* wide, int M, int C, int K);
+bool encode_i8_tiles(CUtensorMap* a, CUtensorMap* b, const void* codes, const void* wide, int M, int C, int K, int width);
 
 // An int32 sum of K products of codes stays in range (128 * 128 * K < 2^31).
 constexpr int kI8MaxK = (1 << 17) - 16;

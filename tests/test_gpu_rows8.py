@@ -356,6 +356,25 @@ def test_product(R, N, K, dt):
     assert torch.all((y.double() - v).abs() <= (F.HALF[dt] + 2.0 ** -24) * v.abs() + off * sc + TINY[dt])
 
 
+# tiles of 64, 128 and 256 rows of the smaller operand, either operand the smaller one; K that ends in
+# the first or second half of a stage, or before it; rows of y that begin anywhere
+TILES = [(700, 2048, 336), (2048, 700, 336), (2048, 701, 400), (1900, 2100, 400), (2100, 1900, 400), (2100, 1901, 144),
+         (300, 2048, 512), (1000, 500, 592), (2000, 2000, 16), (1500, 1510, 80), (9000, 264, 272), (264, 9001, 272)]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=str)
+@pytest.mark.parametrize("R,N,K", TILES)
+def test_product_of_tiles(R, N, K, dt):
+    assert mb.moe_i8_gemm_workspace_bytes(R, N, K) > 2 * K * min(R, N)
+    xq, wq = codes(R, K, seed=R), codes(N, K, seed=N + 1)
+    xs, ws = torch.exp(randn(R, seed=2)) * 0.01, torch.exp(randn(N, seed=3)) * 0.003
+    y = product(xq, xs, wq, ws, dt)
+    acc, sc, mag = reference(xq, xs, wq, ws)
+    v = acc * sc
+    assert float(mag.max()) < 2 ** 24   # exact sums
+    assert torch.all((y.double() - v).abs() <= (F.HALF[dt] + 2.0 ** -24) * v.abs() + TINY[dt])
+
+
 @pytest.mark.parametrize("R,N,K", [(4, 64, 1024), (40, 300, 1024), (200, 300, 1008), (1030, 520, 960)])
 def test_product_of_whole_numbers_is_exact(R, N, K):
     """Any codes, -128 among them, scales 1: whole numbers below 2^24 come out as they are."""
