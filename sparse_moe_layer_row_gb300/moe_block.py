@@ -235,8 +235,12 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
 def _need_rows(t: torch.Tensor, name: str, shape=None) -> int:
     """A matrix of a float type whose rows are contiguous; returns the row stride."""
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES and t.dim() == 2
-            and t.is_contiguous() and (shape is None or t.shape == shape)):
-        return t.shape[1]
+            and (shape is None or t.shape == shape)):
+        if t.is_contiguous():
+            return t.shape[1]
+        ld, step = t.stride()
+        if step == 1 and t.shape[0] > 1:
+            return ld
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -273,8 +277,12 @@ def _need_at(t: torch.Tensor, name: str, device: int, dtype, shape):
 def _need_rows_at(t: torch.Tensor, name: str, device: int, dtype, shape) -> int:
     """_need_rows and _same_device in one, of one type; returns the row stride."""
     if (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype == dtype
-            and t.shape == shape and t.is_contiguous()):
-        return shape[1]
+            and t.shape == shape):
+        if t.is_contiguous():
+            return shape[1]
+        ld, step = t.stride()
+        if step == 1 and shape[0] > 1:
+            return ld
     ld = _need_rows(t, name, shape)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
