@@ -23,8 +23,9 @@
 //                shared-memory traffic of the loop
 // so that A is read as bytes and never written, and an SM's shared memory carries 96 KB per 128 of
 // K (1024 clocks of the tensor core).  Tensor memory holds the accumulators (256 columns) and four A
-// slots of 64, one per stage.  Roles, 512 threads per CTA:
-//   warps 0, 3      lane 0: TMA producers of A (`afull`) and of B (`bfull`), ring of 4 stages
+// slots of 64, one per stage (narrow tiles leave room for more).  Roles, 512 threads per CTA:
+//   warps 0, 3      lane 0: TMA producers of A (`afull`) and of B (`bfull`), ring of 4 stages of 128
+//                   of K (6 or 7 with tiles of 128 or 64 rows of B)
 //   warp 1          tensor memory; in rank 0, issues the MMAs and commits (`empty` of both ranks:
 //                   the stage and its A slot; `tfull`)
 //   warp 2 lane 0   forwarder: the CTA's B of a stage has landed -> rank 0's `ready`
@@ -40,9 +41,10 @@
 // would need flags that a call clears first), 512 clocks per 64 of K the tensor core's, and the last
 // tile's epilogue.  Issued by one lane in a branch of its own the 64 of K took 560: the whole warp
 // runs the loop.  Stages of 64 of K cost 230 ns each whatever the tile's width (rows of 64 bytes are
-// slow to copy), those of 128 some 270.  Two converter warpgroups, the wait for the tensor memory
-// stores deferred by a stage, four conversions in flight and prefetches of A to L2 gained nothing
-// where stages were of 64.  2048 x 2048 x 2048: 20 us, one round of 64 units on 76 pairs.
+// slow to copy); a narrow tile's stages of 128 cost 250, with other pairs at work 340.  Two converter
+// warpgroups gained nothing with either; nor did the wait for the tensor memory stores deferred by a
+// stage, four conversions in flight and prefetches of A to L2.  Rings of 6 and 7 stages instead of
+// 4: 256 x 4096 x 2048 14.4 to 13.1 us.  2048 x 2048 x 2048: 20 us, one round of 64 units.
 #include <cstring>
 #include <type_traits>
 
@@ -184,18 +186,22 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
-constexpr int kStages = 4, kThreads = 512;
-constexpr int kStepK = 128, kRaw = 128 * 128, kBHalf = 128 * 128, kBTile = 2 * kBHalf;   // bytes per stage: codes of A, fp16 of B
-constexpr int kStageBytes = kRaw + kBTile;
-constexpr int kBOff = kStages * kRaw;                // tiles of B behind the codes (1 KB boundaries)
-constexpr int kScaleOff = kStages * kStageBytes;     // float [8][128]: xs of an epilogue warp's rows
+constexpr int kThreads = 512, kMaxStages = 7;
+constexpr int kStepK = 128, kRaw = 128 * 128;        // K and bytes of A per stage
+// Stages of a tile's ring, by its width: what shared memory (16 KB of A, 128 `width` bytes of B) and
+// tensor memory (64 columns of A beside `width` of accumulators) hold.
+__host__ __device__ constexpr int stages_of(int width) { return width > 128 ? 4 : width > 64 ? 6 : 7; }
+constexpr int kScaleOff = 192 * 1024;                // float [8][128]: sb of an epilogue warp's rows
 constexpr int kBarOff = kScaleOff + 8 * 128 * 4;
 constexpr int kSmem = kBarOff + 512 + 1024;
-constexpr int kACol = 256;                           // A slots behind the accumulators
 constexpr int kTmemCols = 512;
-static_assert(kACol + 64 * kStages <= kTmemCols, "TMEM columns");
+constexpr bool fits(int width) {
+    return stages_of(width) * (kRaw + 128 * width) <= kScaleOff && width + 64 * stages_of(width) <= kTmemCols &&
+           stages_of(width) <= kMaxStages;
+}
+static_assert(fits(256) && fits(128) && fits(64), "shared memory and TMEM columns");
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
-static_assert(8 * (4 * kStages + 3) + 12 <= 512, "barrier region");
+static_assert(8 * (4 * kMaxStages + 3) + 12 <= 512, "barrier region");
 // registers per thread after the split; the pool is what the CTA was launched with (checked on
 // the host)
 constexpr int kLaunchRegs = 128, kFewRegs = 56, kManyRegs = 200;
@@ -286,10 +292,10 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
     const uint32_t sbase = (raw + 1023u) & ~1023u;   // same offset in both CTAs
     uint8_t* base = smem_raw + (sbase - raw);
     uint64_t* afull = reinterpret_cast<uint64_t*>(base + kBarOff);   // [S] codes landed
-    uint64_t* bfull = afull + kStages;                                // [S] x landed
-    uint64_t* ready = bfull + kStages;                                // [S] both ranks' x and A (rank 0)
-    uint64_t* empty = ready + kStages;                                // [S] stage and A slot free (both)
-    uint64_t* tfull = empty + kStages;                                // accumulators ready (both)
+    uint64_t* bfull = afull + kMaxStages;                                // [S] x landed
+    uint64_t* ready = bfull + kMaxStages;                                // [S] both ranks' x and A (rank 0)
+    uint64_t* empty = ready + kMaxStages;                                // [S] stage and A slot free (both)
+    uint64_t* tfull = empty + kMaxStages;                                // accumulators ready (both)
     uint64_t* tempty = tfull + 1;                                     // accumulators free (rank 0)
     uint64_t* dbar = tempty + 1;                                      // MMA drain (rank 0)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dbar + 1);
@@ -298,8 +304,11 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
+    const int stages = stages_of(a.width);
+    const uint32_t b_tile = 128 * a.width, b_off = sbase + stages * kRaw;   // tiles of B behind the codes (1 KB boundaries)
+    const uint32_t a_col = kTmemCols - 64 * stages;                         // A's slots behind the accumulators
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(afull + s, 1);
             mbar_init(bfull + s, 1);
             mbar_init(ready + s, 2 * (1 + 4));   // of each rank: the forwarder, four converter warps
@@ -357,21 +366,21 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(full + stage, b ? 128 * a.width : kRaw);
+                    mbar_expect_tx(full + stage, b ? b_tile : kRaw);
                     if (b) {
-                        const uint32_t to = sbase + kBOff + stage * kBTile;
+                        const uint32_t to = b_off + stage * b_tile;
                         tma_load_2d(to, &tmB, kb * kStepK, r0 + n / 2 * rank, full + stage);
-                        tma_load_2d(to + kBHalf, &tmB, kb * kStepK + 64, r0 + n / 2 * rank, full + stage);
+                        tma_load_2d(to + b_tile / 2, &tmB, kb * kStepK + 64, r0 + n / 2 * rank, full + stage);
                     } else {
                         tma_load_2d(sbase + stage * kRaw, &tmA, kb * kStepK, m * 256 + 128 * rank, full + stage);
                     }
                     ++nfills;
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
             }
             // drain: the last fill of every stage has landed (consumed or not)
-            for (int s = 0; s < kStages; ++s) {
-                if (nfills < kStages && s >= nfills) break;
+            for (int s = 0; s < stages; ++s) {
+                if (nfills < stages && s >= nfills) break;
                 const uint32_t par = s < stage ? phase : (phase ^ 1u);
                 if (!mbar_wait_bounded(full + s, par, never, kDrainLimitNs)) give_up();
             }
@@ -402,17 +411,17 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t bd = smem_desc_sw128(sbase + kBOff + stage * kBTile);
-                    const uint32_t at = tmem + (uint32_t)(kACol + 64 * stage);
+                    const uint64_t bd = smem_desc_sw128(b_off + stage * b_tile);
+                    const uint32_t at = tmem + a_col + (uint32_t)(64 * stage);
                     if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
-                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + (kk >> 2) * (kBHalf >> 4) + 2 * (kk & 3), idesc, (kb | kk) != 0);
+                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + (kk >> 2) * (b_tile >> 5) + 2 * (kk & 3), idesc, (kb | kk) != 0);
                         tc_commit_pair(empty + stage);
                         if (kb == nkb - 1) tc_commit_pair(tfull);
                     }
                     __syncwarp();
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
             }
             // drain: arrives once every MMA issued above has completed
@@ -433,7 +442,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                         break;
                     }
                     mbar_arrive_cluster(ready0 + stage * 8);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
         }
     } else if (warp < 8) {
@@ -443,7 +452,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
         // 128-byte swizzle) into lane r of the stage's A slot.
         const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
         const int r = 32 * (warp & 3) + lane, sw = r & 7;
-        const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)kACol;
+        const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + a_col;
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -475,7 +484,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(ready0 + stage * 8);
-                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
@@ -594,13 +603,13 @@ cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CU
 // to 32 rows per CTA; the tiles 7800 (6500 where a lane holds a row of y) + kStep per 64 of K and round
 // of units.  Narrow tiles leave the tensor core waiting for the converters, but give few rows more
 // pairs.  Measured, us, rows kernel / tiles of 256, 128, 64:
-//    256 x 2048 x 2048   13.5 / 16.6 12.5 11.9       512 x 2048 x 2048   25.2 / 17.3 14.3 14.1
-//    128 x 4096 x 2048   14.6 / 14.1 13.8 13.1      1024 x 4096 x 4096      - / 28.3 32.8 49.1
-//   1000 x 1000 x  992   24.7 / 12.6 10.4 11.3 (the rule's 64 is not the best)
-//   1000 x  512 x  512    9.5 /  9.1  7.1  6.9        64 x 4096 x 7168   23.8 / 30.0 29.1 29.0
+//    256 x 2048 x 2048   13.5 / 16.7 12.3 11.8       512 x 2048 x 2048   25.2 / 17.4 13.1 13.3
+//    128 x 4096 x 2048   14.6 / 14.1 12.5 12.1      1024 x 4096 x 4096      - / 28.1 29.1 45.9
+//   1000 x 1000 x  992   24.7 / 12.6 10.2 11.1 (the rule's 64 is not the best)
+//   1000 x  512 x  512    9.5 /  9.1  7.1  6.9       128 x 8192 x 4096   43.3 / 22.8 18.9 17.9
 namespace {
 int64_t tiles_ns(int R, int N, int K, int* width) {
-    constexpr int kStep[3] = {265, 200, 195};   // widths 256, 128, 64
+    constexpr int kStep[3] = {265, 200, 170};   // widths 256, 128, 64
     const int64_t M = R > N ? R : N, C = R > N ? N : R, steps = (K + 63) / 64;
     int64_t best = 0;
     for (int i = 0; i < 3; ++i) {
