@@ -699,8 +699,8 @@ def moe_i8_quantize(x, codes, scales, stream=None):
     R, K = shape
     _need_at(codes, "codes", dev, torch.int8, shape)
     _need_at(scales, "scales", dev, torch.float32, (R,))
-    _on(dev, load().moe_i8_quantize, _ptr(x), _DTYPES[x.dtype], ld, R, K, _ptr(codes),
-        _ptr(scales), _stream(stream, dev))
+    _on(dev, load().moe_i8_quantize, x.data_ptr(), _DTYPES[x.dtype], ld, R, K, codes.data_ptr(),
+        scales.data_ptr(), _stream(stream, dev))
 
 
 def moe_i8_gemm_workspace_bytes(R: int, N: int, K: int) -> int:
@@ -724,8 +724,9 @@ def moe_i8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
     _need_at(wq, "wq", dev, torch.int8, (N, K))
     _need_at(ws, "ws", dev, torch.float32, (N,))
     _need_at(workspace, "workspace", dev, torch.uint8, getattr(workspace, "shape", None))
-    _on(dev, load().moe_i8_gemm, _ptr(xq), _ptr(xs), R, _ptr(wq), _ptr(ws), N, K, _ptr(y),
-        _DTYPES[y.dtype], ld, _ptr(workspace), workspace.numel(), _stream(stream, dev))
+    _on(dev, load().moe_i8_gemm, xq.data_ptr(), xs.data_ptr(), R, wq.data_ptr(), ws.data_ptr(), N, K,
+        y.data_ptr(), _DTYPES[y.dtype], ld, workspace.data_ptr(), workspace.numel(),
+        _stream(stream, dev))
 
 
 def _or_fp32(t, dtype):
@@ -745,30 +746,34 @@ def moe_add_rmsnorm(x, weight, eps, residual=None, total=None, y=None, codes=Non
     ldx = _need_rows(x, "x")
     dev, dt, shape = x.get_device(), x.dtype, x.shape
     R, H = shape
-    ldr = ldt = ldy = 0
+    ldr = ldt = ldy = kind = 0
+    pr = pt = pw = py = pc = ps = None
     rt = wt = dt
     if residual is not None:
         rt = _or_fp32(residual, dt)
         ldr = _need_rows_at(residual, "residual", dev, rt, shape)
+        pr = residual.data_ptr()
     if total is not None:
         if residual is None:
             raise ValueError("total needs a residual")
         ldt = _need_rows_at(total, "total", dev, rt, shape)
+        pt = total.data_ptr()
     if weight is not None:
         wt = _or_fp32(weight, dt)
         _need_at(weight, "weight", dev, wt, (H,))
+        pw = weight.data_ptr()
     if y is not None:
         ldy = _need_rows_at(y, "y", dev, dt, shape)
-    kind = 0
+        py = y.data_ptr()
     if codes is not None:
         kind = 2 if codes.dtype == torch.int8 else 1
         _need_at(codes, "codes", dev, torch.int8 if kind == 2 else torch.float8_e4m3fn, shape)
         _need_at(scales, "scales", dev, torch.float32, (R,) if kind == 2 else (-(-H // 128), R))
+        pc, ps = codes.data_ptr(), scales.data_ptr()
     elif scales is not None:
         raise ValueError("scales go with codes")
-    _on(dev, load().moe_add_rmsnorm, _ptr(x), _DTYPES[dt], ldx, R, H, _ptr(residual), _DTYPES[rt],
-        ldr, _ptr(total), ldt, _ptr(weight), _DTYPES[wt], eps, _ptr(y), ldy, kind, _ptr(codes),
-        _ptr(scales), _stream(stream, dev))
+    _on(dev, load().moe_add_rmsnorm, x.data_ptr(), _DTYPES[dt], ldx, R, H, pr, _DTYPES[rt], ldr, pt,
+        ldt, pw, _DTYPES[wt], eps, py, ldy, kind, pc, ps, _stream(stream, dev))
 
 
 def moe_read_device_status(workspace: torch.Tensor, stream=None) -> dict:
