@@ -505,8 +505,11 @@ size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K);
 /* y = x W^T on int8 codes, x with a scale for each row (token), W for each output channel.
  *   y[r, n] = (xs[r] * ws[n]) * sum_k xq[r, k] wq[n, k]
  * The sum is that of integers, held in 32 bits: exact while its partial sums stay
- * below 2^24, rounded as fp32 sums are beyond; the product of the two scales is
- * formed first, in fp32; y is rounded once.
+ * below 2^24.  Beyond, calls with the 1 KB workspace (see above) still give the integer,
+ * rounded to fp32 once; the others are off by at most 2^-13.8 of the sum of the products'
+ * magnitudes (some 1e-5 with codes of one sign), so that a row there may differ in its last
+ * bits from the same row in a call of few rows.  The product of the two scales is formed
+ * first, in fp32; y is rounded once.
  *   xq  [R, K] codes, xs [R] scales (as moe_i8_quantize writes them)
  *   wq  [N, K] codes, ws [N] scales
  *   y   [R, N] of `dtype` out, rows row_stride elements apart (>= N)

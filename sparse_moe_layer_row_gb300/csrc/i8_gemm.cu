@@ -3,7 +3,15 @@
 // sm_103a has no fast path for int8 products: mma.sync on int8 takes an SM some 20 clocks for 16 x
 // 8 x 32, which up to 8 rows hide behind the weights' loads.  With more, codes become fp16 in
 // registers (exact, as their products and sums below 2^24 are in fp32), and the sum of whole
-// numbers is the fp16 tensor core's.
+// numbers is the fp16 tensor core's.  Past 2^24 the tensor core drops what lies below its
+// accumulator's last bit, at every addition of 16 products and always towards zero:
+//   k_i8_rows   a warp's share of K is summed in pieces of 1024, none of which passes 2^24, and the
+//               pieces and shares in int32 (shares whose fp32 sum cannot pass 2^24: in fp32): the whole
+//               number for any K.  Costs 0.1 us of 4.5 (32 x 4096 x 2048).
+//   k_i8_tiles  parts of 8192 of K, added in fp32: off by (512 + parts) 2^-23 of the addends' magnitudes
+//               at most.  Codes of 100 to 127 at K = 7168: 1.2e-5; in one part K = 131056 had 7.6e-4.
+//               Parts of 1024, exact up to K = 2048, were 3 to 8% slower for every K above 1024
+//               (2048 x 4096 x 7168: 83.7 against 77.1 us; the accumulators' way out is not overlapped).
 //
 // k_i8_rows: a CTA takes 16 outputs and 32 rows, and its eight warps share K: warp w
 // takes the blocks of 128 w, w + 8, ...  The weights are the M of mma.sync m16n8k16 (up to 8
@@ -57,6 +65,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kCols = 16, kRowsPerCta = 32;
+constexpr int kExactK = 1024;   // a sum of as many products of codes is at most 2^24: exact in fp32
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                        uint32_t b0, uint32_t b1) {
@@ -95,12 +104,13 @@ __device__ __forceinline__ void store_one(void* y, int64_t i, int dtype, float v
 }  // namespace
 
 // NT tiles of 8 rows per CTA
-template <int NT>
+template <int NT, bool LONG>
 __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
     using Acc = std::conditional_t<NT == 1, int, float>;
+    using Part = std::conditional_t<LONG, int, Acc>;
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
-    __shared__ Acc part[kWarps][NT * 8][kCols + 1];
+    __shared__ Part part[kWarps][NT * 8][kCols + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gi = lane >> 2, c = lane & 3;
     const int r0 = blockIdx.y * kRowsPerCta;
@@ -117,6 +127,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[t][j] = 0;
+    int whole[LONG ? NT : 1][4] = {}, held = 0;   // LONG: what acc held before; of the warp's K in acc
+    auto fold = [&]() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                whole[t][j] += (int)acc[t][j];
+                acc[t][j] = 0;
+            }
+        held = 0;
+    };
     auto load = [&](const int8_t* p, int kb, int half) {   // zeros past the row's end (K % 16 == 0)
         const int at = kb * kFp8Block + 16 * half;
         return at + 32 * c < a.K ? __ldg(reinterpret_cast<const uint4*>(p + at)) : make_uint4(0, 0, 0, 0);
@@ -160,23 +181,42 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
                     }
                 }
             }
+        if constexpr (LONG) {
+            if ((held += 2 * kFp8Block) == kExactK) fold();
+        }
     }
+    if constexpr (LONG) fold();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {   // D: outputs gi and gi + 8 of rows 2c and 2c + 1
-        part[warp][8 * t + 2 * c][gi] = acc[t][0];
-        part[warp][8 * t + 2 * c + 1][gi] = acc[t][1];
-        part[warp][8 * t + 2 * c][gi + 8] = acc[t][2];
-        part[warp][8 * t + 2 * c + 1][gi + 8] = acc[t][3];
+        auto value = [&](int j) -> Part {
+            if constexpr (LONG) return whole[t][j];
+            else return acc[t][j];
+        };
+        part[warp][8 * t + 2 * c][gi] = value(0);
+        part[warp][8 * t + 2 * c + 1][gi] = value(1);
+        part[warp][8 * t + 2 * c][gi + 8] = value(2);
+        part[warp][8 * t + 2 * c + 1][gi + 8] = value(3);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < NT * 8 * kCols; i += 32 * kWarps) {
         const int r = i / kCols, n = i % kCols;
         if (r0 + r >= a.R || n0 + n >= a.N) continue;
-        Acc v = part[0][r][n];
+        Part v = part[0][r][n];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) v += part[w][r][n];
+        float sum = (float)v;
+        if constexpr (std::is_same_v<Part, float>) {
+            float most = 0.0f;   // no sum on the way exceeds it
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) most += fabsf(part[w][r][n]);
+            if (most > (float)(1 << 24)) {
+                int whole = 0;
+                for (int w = 0; w < kWarps; ++w) whole += (int)part[w][r][n];
+                sum = (float)whole;
+            }
+        }
         store_one(a.y, (int64_t)(r0 + r) * a.ldy + n0 + n, a.ydtype,
-                  (float)v * (__ldg(a.xs + r0 + r) * __ldg(a.ws + n0 + n)));
+                  sum * (__ldg(a.xs + r0 + r) * __ldg(a.ws + n0 + n)));
     }
 }
 
@@ -188,6 +228,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal 
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
 constexpr int kThreads = 512, kMaxStages = 7;
 constexpr int kStepK = 128, kRaw = 128 * 128;        // K and bytes of A per stage
+constexpr int kPartK = 8192, kPart = kPartK / kStepK;   // K (and stages) between two reads of the accumulators
 // Stages of a tile's ring, by its width: what shared memory (16 KB of A, 128 `width` bytes of B) and
 // tensor memory (64 columns of A beside `width` of accumulators) hold.
 __host__ __device__ constexpr int stages_of(int width) { return width > 128 ? 4 : width > 64 ? 6 : 7; }
@@ -282,7 +323,7 @@ __global__ void __launch_bounds__(256) k_i8_widen(const int8_t* q, __half* x, in
     }
 }
 
-template <bool SWAP>
+template <bool SWAP, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, I8GemmArgs a) {
     const int M = SWAP ? a.R : a.N, C = SWAP ? a.N : a.R;   // rows of A and of B
@@ -333,7 +374,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
     const int mt = (M + 255) / 256, nunits = mt * ((C + a.width - 1) / a.width);
     const int nact = active_workers(nunits, (int)cluster_count());   // balanced rounds
     const int ufirst = (int)cluster_id() < nact ? (int)cluster_id() : nunits;
-    const int nkb = (a.K + kStepK - 1) / kStepK;
+    const int nkb = (a.K + kStepK - 1) / kStepK, parts = (nkb + kPart - 1) / kPart;
     auto rows_of = [&](int u, int& m, int& r0) {   // the MMA's N: rows of B of the unit, in 32s
         const int c = u / mt;
         m = u - c * mt;
@@ -403,9 +444,15 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                 int m, r0;
                 const int n = rows_of(u, m, r0);
                 const uint32_t idesc = 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(256 >> 4) << 24;   // fp16 A and B
-                if (!wait(tempty, tphase ^ 1u)) break;
-                tphase ^= 1u;
                 for (int kb = 0; kb < nkb; ++kb) {
+                    const int at_part = LONG ? kb % kPart : kb;
+                    if (at_part == 0) {
+                        if (!wait(tempty, tphase ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tphase ^= 1u;
+                    }
                     if (!wait(ready + stage, phase)) {
                         ok = false;
                         break;
@@ -416,9 +463,9 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                     if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)   // 32 bytes along K are 2 in the descriptor's address field
-                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + (kk >> 2) * (b_tile >> 5) + 2 * (kk & 3), idesc, (kb | kk) != 0);
+                            mma_f16_pair_ta(tmem, at + 8 * kk, bd + (kk >> 2) * (b_tile >> 5) + 2 * (kk & 3), idesc, (at_part | kk) != 0);
                         tc_commit_pair(empty + stage);
-                        if (kb == nkb - 1) tc_commit_pair(tfull);
+                        if ((LONG && at_part == kPart - 1) || kb == nkb - 1) tc_commit_pair(tfull);
                     }
                     __syncwarp();
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -494,6 +541,21 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
         float* xs = reinterpret_cast<float*>(base + kScaleOff) + 128 * (warp - 8);
         uint32_t tphase = 0;
+        auto accumulators_ready = [&]() {
+            const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitLimitNs);
+            if (__any_sync(0xffffffffu, !got)) {
+                give_up();
+                return false;
+            }
+            tphase ^= 1u;
+            tc_fence_after();
+            return true;
+        };
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0);
+        };
         for (int u = half && a.width <= 128 ? nunits : ufirst; u < nunits; u += nact) {
             int m, r0;
             rows_of(u, m, r0);
@@ -504,24 +566,41 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
 #pragma unroll
             for (int i = lane; i < 128; i += 32) xs[i] = i < n ? __ldg(sb + rb + i) : 0.0f;
             __syncwarp();
-            const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitLimitNs);
-            if (__any_sync(0xffffffffu, !got)) { give_up(); break; }
-            tphase ^= 1u;
-            tc_fence_after();
             float v[128];
+            if constexpr (LONG) {   // all parts but the last
+#pragma unroll
+                for (int c = 0; c < 128; ++c) v[c] = 0.0f;
+                bool ok = true;
+                for (int part = 1; ok && part < parts; ++part) {
+                    ok = accumulators_ready();
+                    if (ok) {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 32) {
+                            float lo[16], hi[16];
+                            tmem_ld16x2(tq + c, tq + c + 16, lo, hi);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                v[c + i] += lo[i];
+                                v[c + 16 + i] += hi[i];
+                            }
+                        }
+                        release();
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!accumulators_ready()) break;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 float lo[16], hi[16];
                 tmem_ld16x2(tq + c, tq + c + 16, lo, hi);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    v[c + i] = lo[i];
-                    v[c + 16 + i] = hi[i];
+                    v[c + i] = LONG ? v[c + i] + lo[i] : lo[i];
+                    v[c + 16 + i] = LONG ? v[c + 16 + i] + hi[i] : hi[i];
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0);
+            release();
             if (ra < M) {
                 auto store = [&](auto* y) {
                     if (SWAP) store_along(y + (int64_t)ra * a.ldy + rb, a.y_vec, v, xs, ls, n);
@@ -580,8 +659,10 @@ cudaError_t i8_tiles_set_attributes(int num_sms, int* clusters) {
         *clusters = n < *clusters ? n : *clusters;
         return cudaSuccess;
     };
-    const cudaError_t e = set(k_i8_tiles<false>);
-    return e == cudaSuccess ? set(k_i8_tiles<true>) : e;
+    cudaError_t e = set(k_i8_tiles<false, false>);
+    if (e == cudaSuccess) e = set(k_i8_tiles<true, false>);
+    if (e == cudaSuccess) e = set(k_i8_tiles<false, true>);
+    return e == cudaSuccess ? set(k_i8_tiles<true, true>) : e;
 }
 
 cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, void* wide, int num_sms,
@@ -596,7 +677,10 @@ cudaError_t launch_i8_tiles(const I8GemmArgs& a, const CUtensorMap& ma, const CU
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = tiles_config(attr, clusters, st);
-    return cudaLaunchKernelEx(&cfg, swap ? k_i8_tiles<true> : k_i8_tiles<false>, ma, mb, a);
+    const bool longer = a.K > kPartK;
+    auto k = swap ? (longer ? k_i8_tiles<true, true> : k_i8_tiles<true, false>)
+                  : (longer ? k_i8_tiles<false, true> : k_i8_tiles<false, false>);
+    return cudaLaunchKernelEx(&cfg, k, ma, mb, a);
 }
 
 // By what the kernels were measured to take (ns): the rows kernel 1800 + CTAs (5.9 + 0.0031 K) with 17
@@ -640,7 +724,9 @@ bool i8_rows_applies(int R, int N, int K) {
 
 cudaError_t launch_i8_rows(const I8GemmArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)((a.N + kCols - 1) / kCols), (unsigned)((a.R + kRowsPerCta - 1) / kRowsPerCta));
-    auto k = a.R <= 8 ? k_i8_rows<1> : a.R <= 16 ? k_i8_rows<2> : k_i8_rows<4>;
+    const bool longer = a.K > kWarps * kExactK;
+    auto k = a.R <= 8 ? k_i8_rows<1, false> : a.R <= 16 ? (longer ? k_i8_rows<2, true> : k_i8_rows<2, false>)
+                                                        : (longer ? k_i8_rows<4, true> : k_i8_rows<4, false>);
     return launch_kernel(k, grid, dim3(32 * kWarps), 0, st, a);
 }
 
