@@ -530,8 +530,9 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
  *           operands of moe_fp8_gemm;
  *           MOE_CODES_I8: int8, as moe_i8_quantize's of p, the scale a * rstd / 127
  *           for each row: the operands of moe_i8_gemm.
- * Sums are fp32; a row whose sum of squares exceeds fp32 is scaled first.  A row with
- * a NaN or an infinity has NaN values, or scales, at least there.
+ * Sums are fp32; where a row's exceeds fp32, that of the squares of 2^-80 r is taken, and
+ * where a block's (int8: such a row's) largest |p| does, its codes are those of 2^-80 r times
+ * the weight.  A row with a NaN or an infinity has NaN values, or scales, at least there.
  *   x         [R, H] of `dtype`, rows x_stride elements apart (>= H); any H >= 1
  *   residual  [R, H] of `residual_dtype` (that of x, or fp32), or NULL
  *   total     [R, H] of `residual_dtype` out: r, or NULL; needs a residual; may be the

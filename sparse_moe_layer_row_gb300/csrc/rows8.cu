@@ -22,8 +22,8 @@
 // 20.6; int8 quantising 9.9 (5.1 TB/s, floor 7.6); with an fp32 residual 31.3 (6.4 TB/s, floor 30.2).
 // Bound by the issue of some 13 instructions a value beside HBM (CTAs that come and go: 29.7 and
 // 12.3).  One row takes 1.7 us; 777 x 1000, fp16 with an fp32 residual and int8 codes, 3.4 (floor 1.3).
-// Sums are fp32: 8 NV squares per thread, then a tree.  A row whose sum of squares
-// overflows is scaled by 2^-80 and summed again.
+// Sums are fp32: 8 NV squares per thread, then a tree.  A row whose sum of squares overflows is
+// read again and the squares of 2^-80 r summed (huge_row); its codes are those of p all the same.
 #include <type_traits>
 
 #include "rows8.cuh"
@@ -33,6 +33,7 @@ namespace moe {
 namespace {
 
 constexpr float kTiny = 1.0f / (1 << 20) / (1 << 20) / (1 << 20) / (1 << 20);   // 2^-80
+constexpr float kRoot = 1.0f / (1 << 20) / (1 << 20);                           // 2^-40
 
 // Two values in 16 bits each.
 template <typename T>
@@ -211,6 +212,145 @@ __device__ __forceinline__ void combine_row(Exchange& x, int& buf, float& ss, ui
     }
 }
 
+// x and the residual of eight values from c on; `stored`: their sum, which has been written
+struct In { Raw8 x, res; };
+template <int WHAT, typename T, bool VEC>
+__device__ __forceinline__ In load_in(const RmsNormArgs& a, int64_t row, int c, bool stored) {
+    constexpr bool kNorm = WHAT != kQuantI8;
+    In in{};
+    const int n = a.H - c;
+    if (n <= 0 || row >= a.R) return in;
+    if (kNorm && stored && a.residual && a.total) {
+        if (a.res_f32) in.res = load8<float, VEC>(static_cast<const float*>(a.total) + row * a.ldt + c, n);
+        else in.x = load8<T, VEC>(static_cast<const T*>(a.total) + row * a.ldt + c, n);
+        return in;
+    }
+    in.x = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + c, n);
+    if (kNorm && a.residual) {
+        if (a.res_f32) in.res = load8<float, VEC>(static_cast<const float*>(a.residual) + row * a.ldr + c, n);
+        else in.res = load8<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr + c, n);
+    }
+    return in;
+}
+// r, and its store
+template <int WHAT, typename T, bool VEC>
+__device__ __forceinline__ void sum_in(const RmsNormArgs& a, int64_t row, const In& in, int c, bool stored, float (&r)[8]) {
+    values<T>(in.x, r);
+    if (WHAT == kQuantI8 || !a.residual) return;
+    const int n = a.H - c;
+    if (stored && a.total) {
+        if (a.res_f32) values<float>(in.res, r);
+        return;
+    }
+    float b[8];
+    if (a.res_f32) {
+        values<float>(in.res, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] += b[i];
+        if (!stored && a.total && n > 0)
+            store8<float, VEC>(static_cast<float*>(a.total) + row * a.ldt + c, n, raw_of<float>(r));
+    } else {
+        values<T>(in.res, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] += b[i];
+        const Raw8 sum = raw_of<T>(r);
+        values<T>(sum, r);
+        if (!stored && a.total && n > 0) store8<T, VEC>(static_cast<T*>(a.total) + row * a.ldt + c, n, sum);
+    }
+}
+template <int WHAT, typename T, bool VEC>
+__device__ __forceinline__ void times_w(const RmsNormArgs& a, int c, float (&p)[8]) {
+    const int n = a.H - c;
+    if (WHAT == kQuantI8 || !a.w || n <= 0) return;
+    float w[8];
+    if (a.w_f32) values<float>(load8<float, VEC>(static_cast<const float*>(a.w) + c, n), w);
+    else values<T>(load8<T, VEC>(static_cast<const T*>(a.w) + c, n), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] *= w[i];
+}
+template <bool VEC>
+__device__ __forceinline__ void store_codes(const RmsNormArgs& a, int64_t row, int c, uint2 q) {
+    uint8_t* dst = a.codes + row * a.H + c;
+    if (VEC) {
+        *reinterpret_cast<uint2*>(dst) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < a.H - c) dst[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    }
+}
+
+// A row whose sum of squares passes fp32, or with an infinity or a NaN: read again, with the squares
+// of 2^-80 r.  The codes are those of p as everywhere; where a block's largest |p| (int8: the row's, m)
+// passes fp32 itself they are those of 2^-80 r times w.  All threads of the row call it (buf: as
+// combine_row's, which is called once).
+template <int WHAT, typename T, bool VEC>
+__device__ __noinline__ void huge_row(const RmsNormArgs& a, int64_t row, int warps, int t, uint32_t m, Exchange& x, int buf) {
+    constexpr bool kRowMax = WHAT == kNormI8;
+    const int step = 256 * warps;
+    float ss = 0.0f, mf = 0.0f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < a.H; c0 += step) {
+        const int c = c0 + 8 * t;
+        float r[8];
+        sum_in<WHAT, T, VEC>(a, row, load_in<WHAT, T, VEC>(a, row, c, true), c, true, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[i] *= kTiny;
+            ss = fmaf(r[i], r[i], ss);
+        }
+        if (kRowMax) {
+            times_w<WHAT, T, VEC>(a, c, r);
+            mf = largest(r, mf);
+        }
+    }
+    uint32_t small = __float_as_uint(mf);
+    combine_row<true, kRowMax>(x, buf, ss, small, warps);
+    const float rstd = rsqrtf(fmaf(ss, a.inv_h, a.eps * kTiny * kTiny));   // that of 2^-80 r
+    // 2^-80 v rstd, in two steps that neither overflow nor lose a result's bits
+    auto normed = [&](float v) { return (v * kRoot) * (rstd * kRoot); };
+    constexpr uint32_t kInf = 0x7F800000u;
+    const bool row_over = kRowMax && m == kInf;
+    if (kRowMax) {
+        m = fp8_amax_bits(row_over ? small : m);
+        const float v = __uint_as_float(m);
+        if (t == 0) a.scales[row] = over(row_over ? v * rstd : normed(v), 127.0f, 1.0f / 127.0f);
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < a.H; c0 += step) {
+        const int c = c0 + 8 * t, n = a.H - c;
+        float p[8], s[8];
+        sum_in<WHAT, T, VEC>(a, row, load_in<WHAT, T, VEC>(a, row, c, true), c, true, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = p[i] * kTiny;
+        times_w<WHAT, T, VEC>(a, c, p);
+        times_w<WHAT, T, VEC>(a, c, s);
+        uint2 q = make_uint2(0, 0);
+        if (WHAT == kNormE4m3) {   // every lane takes part in the block's maxima
+            uint32_t bm = __float_as_uint(largest(p, 0.0f)), bs = __float_as_uint(largest(s, 0.0f));
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) {
+                bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+                bs = max(bs, __shfl_xor_sync(0xffffffffu, bs, o));
+            }
+            const bool block_over = bm == kInf;
+            bm = fp8_amax_bits(block_over ? bs : bm);
+            const float v = __uint_as_float(bm);
+            q = block_over ? e4m3_codes(s, bm) : e4m3_codes(p, bm);
+            if ((t & 15) == 0 && n > 0)
+                a.scales[(int64_t)(c / kFp8Block) * a.R + row] = over(block_over ? v * rstd : normed(v), 448.0f, 1.0f / 448.0f);
+        }
+        if (kRowMax) q = row_over ? i8_codes(s, m) : i8_codes(p, m);
+        if (n <= 0) continue;
+        if (WHAT != kNormOnly) store_codes<VEC>(a, row, c, q);
+        if (WHAT == kNormOnly || a.y) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = fabsf(p[i]) < INFINITY ? normed(p[i]) : s[i] * rstd;
+            store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy + c, n, raw_of<T>(p));
+        }
+    }
+}
+
 }  // namespace
 
 namespace {
@@ -284,110 +424,109 @@ __device__ __forceinline__ void rows_many(const RmsNormArgs& a, int warps, const
         for (int i = 0; i < 4; ++i) m = max_magnitude(p[i].x, p[i].y, m);
         return m;
     };
-    if (row < a.R) load_row(row);
-    for (; row < a.R; row += stride) {   // the same rows in every thread of a barrier
-        float2 r[NV][4], s2 = make_float2(0.0f, 0.0f);
-        float ss = 0.0f, mf = 0.0f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float f[8];
-            values<T>(nx[v], f);
-            pairs(f, r[v]);
-            if (RES) {
-                values<RT>(nr[v], f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[v][i] = add2(r[v][i], make_float2(f[2 * i], f[2 * i + 1]));
-                singles(r[v], f);
-                const Raw8 sum = raw_of<RT>(f);
-                if (sizeof(RT) == 2) {
-                    values<RT>(sum, f);
-                    pairs(f, r[v]);
-                }
-                if (a.total && inside(v)) store_raw(static_cast<RT*>(a.total) + (int64_t)row * a.ldt + c0 + v * step, sum);
-            }
-        }
-        if (row + stride < a.R) load_row(row + stride);   // before the exchange
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (kNorm)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s2 = fma22(r[v][i], r[v][i], s2);
-            if (kRowMax) {
-                float2 p[4] = {r[v][0], r[v][1], r[v][2], r[v][3]};
-                if (inside(v)) times_w(v, p);
-                mf = largest4(p, mf);
-            }
-        }
-        ss = s2.x + s2.y;
-        uint32_t m = __float_as_uint(mf);
-        combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
-        const bool huge = kNorm && !(ss < INFINITY);   // as in k_rows8
-        if (huge) {
-            ss = mf = 0.0f;
+    // to the end, or to a row for huge_row, whose m it returns
+    auto run = [&]() {
+        for (; row < a.R; row += stride) {   // the same rows in every thread of a barrier
+            float2 r[NV][4], s2 = make_float2(0.0f, 0.0f);
+            float ss = 0.0f, mf = 0.0f;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
+                float f[8];
+                values<T>(nx[v], f);
+                pairs(f, r[v]);
+                if (RES) {
+                    values<RT>(nr[v], f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    r[v][i] = make_float2(r[v][i].x * kTiny, r[v][i].y * kTiny);
-                    ss = fmaf(r[v][i].x, r[v][i].x, fmaf(r[v][i].y, r[v][i].y, ss));
+                    for (int i = 0; i < 4; ++i) r[v][i] = add2(r[v][i], make_float2(f[2 * i], f[2 * i + 1]));
+                    singles(r[v], f);
+                    const Raw8 sum = raw_of<RT>(f);
+                    if (sizeof(RT) == 2) {
+                        values<RT>(sum, f);
+                        pairs(f, r[v]);
+                    }
+                    if (a.total && inside(v)) store_raw(static_cast<RT*>(a.total) + (int64_t)row * a.ldt + c0 + v * step, sum);
                 }
+            }
+            if (row + stride < a.R) load_row(row + stride);   // before the exchange
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (kNorm)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s2 = fma22(r[v][i], r[v][i], s2);
                 if (kRowMax) {
                     float2 p[4] = {r[v][0], r[v][1], r[v][2], r[v][3]};
                     if (inside(v)) times_w(v, p);
                     mf = largest4(p, mf);
                 }
             }
-            m = __float_as_uint(mf);
+            ss = s2.x + s2.y;
+            uint32_t m = __float_as_uint(mf);
             combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
-        }
-        const float rstd = kNorm ? rsqrtf(fmaf(ss, a.inv_h, huge ? 0.0f : a.eps)) : 1.0f;
-        if (kRowMax) {
-            m = fp8_amax_bits(m);
-            if (t == 0) a.scales[row] = over(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f, 1.0f / 127.0f);
-        }
-        uint32_t bm[NV];   // e4m3: the blocks' largest magnitudes, their exchanges side by side
+            if (kNorm && !(ss < INFINITY)) return m;   // the same in each thread
+            const float rstd = kNorm ? rsqrtf(fmaf(ss, a.inv_h, a.eps)) : 1.0f;
+            if (kRowMax) {
+                m = fp8_amax_bits(m);
+                if (t == 0) a.scales[row] = over(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f, 1.0f / 127.0f);
+            }
+            uint32_t bm[NV];   // e4m3: the blocks' largest magnitudes, their exchanges side by side
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (inside(v)) times_w(v, r[v]);
-            if (WHAT == kNormE4m3) bm[v] = __float_as_uint(largest4(r[v], 0.0f));
-        }
-        if (WHAT == kNormE4m3)
+            for (int v = 0; v < NV; ++v) {
+                if (inside(v)) times_w(v, r[v]);
+                if (WHAT == kNormE4m3) bm[v] = __float_as_uint(largest4(r[v], 0.0f));
+            }
+            if (WHAT == kNormE4m3)
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1)
+                for (int o = 8; o >= 1; o >>= 1)
 #pragma unroll
-                for (int v = 0; v < NV; ++v) bm[v] = max(bm[v], __shfl_xor_sync(0xffffffffu, bm[v], o));
+                    for (int v = 0; v < NV; ++v) bm[v] = max(bm[v], __shfl_xor_sync(0xffffffffu, bm[v], o));
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float p[8];
-            singles(r[v], p);
-            if (WHAT == kNormE4m3) {
-                const uint32_t b = fp8_amax_bits(bm[v]);
-                const uint2 q = e4m3_codes(p, b);
-                if (inside(v)) {
-                    *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.H + c0 + v * step) = q;
-                    if ((lane & 15) == 0)
-                        a.scales[(int64_t)((c0 + v * step) / kFp8Block) * a.R + row] =
-                            over(__uint_as_float(b) * rstd, 448.0f, 1.0f / 448.0f);
+            for (int v = 0; v < NV; ++v) {
+                float p[8];
+                singles(r[v], p);
+                if (WHAT == kNormE4m3) {
+                    const uint32_t b = fp8_amax_bits(bm[v]);
+                    const uint2 q = e4m3_codes(p, b);
+                    if (inside(v)) {
+                        *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.H + c0 + v * step) = q;
+                        if ((lane & 15) == 0)
+                            a.scales[(int64_t)((c0 + v * step) / kFp8Block) * a.R + row] =
+                                over(__uint_as_float(b) * rstd, 448.0f, 1.0f / 448.0f);
+                    }
+                }
+                if (kRowMax) {
+                    const uint2 q = i8_codes(p, m);
+                    if (inside(v)) *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.H + c0 + v * step) = q;
+                }
+                if (kNorm && (WHAT == kNormOnly || a.y) && inside(v)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[v][i] = mul2(r[v][i], rstd);
+                    singles(r[v], p);
+                    store_raw(static_cast<T*>(a.y) + (int64_t)row * a.ldy + c0 + v * step, raw_of<T>(p));
                 }
             }
-            if (kRowMax) {
-                const uint2 q = i8_codes(p, m);
-                if (inside(v)) *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.H + c0 + v * step) = q;
-            }
-            if (kNorm && (WHAT == kNormOnly || a.y) && inside(v)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[v][i] = mul2(r[v][i], rstd);
-                singles(r[v], p);
-                store_raw(static_cast<T*>(a.y) + (int64_t)row * a.ldy + c0 + v * step, raw_of<T>(p));
-            }
         }
+        return 0u;
+    };
+    if (!kNorm) {
+        if (row < a.R) load_row(row);
+        run();
+        return;
+    }
+    while (row < a.R) {
+        load_row(row);
+        const uint32_t m = run();
+        if (row >= a.R) break;
+        // out of the loop, whose registers need not outlast the call
+        huge_row<WHAT, T, true>(a, row, warps, t, m, s_x, buf);
+        if (warps != 1) buf ^= 1;
+        row += stride;
     }
 }
 
 }  // namespace
 
 template <int WHAT, typename T, int NV, int MINB>
-__global__ void __launch_bounds__(256, MINB) k_rows8_many(RmsNormArgs a, int warps) {
+__global__ void __launch_bounds__(256, MINB) k_rows8_many(const __grid_constant__ RmsNormArgs a, int warps) {
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
     extern __shared__ __align__(16) float s_w[];
@@ -417,11 +556,11 @@ __global__ void __launch_bounds__(256, MINB) k_rows8_many(RmsNormArgs a, int war
     }
 }
 
-// Rows blockIdx.x, + gridDim.x, ...: a row per `warps` warps; a CTA has several at once only where
-// that is one.  NV vectors of eight values per thread; ONE: they hold the row, else it is gone
-// through twice.  MAXT, MINB: threads of a CTA at most, CTAs per SM at least.
+// A row per `warps` warps; a CTA has several only where that is one.  NV vectors of eight values per
+// thread; ONE: they hold the row, else it is gone through twice.  MAXT, MINB: threads of a CTA at
+// most, CTAs per SM at least.
 template <int WHAT, typename T, bool VEC, int NV, bool ONE, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) k_rows8(RmsNormArgs a, int warps) {
+__global__ void __launch_bounds__(MAXT, MINB) k_rows8(const __grid_constant__ RmsNormArgs a, int warps) {
     pdl_wait();  // see common.cuh: nothing global is touched before
     pdl_trigger();
     constexpr bool kNorm = WHAT != kQuantI8, kRowMax = WHAT == kNormI8 || WHAT == kQuantI8;
@@ -431,61 +570,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rows8(RmsNormArgs a, int warps) 
     const int t = warps == 1 ? lane : threadIdx.x;
     const int step = 256 * warps;   // values per vector of the row's threads
     const int per_cta = warps == 1 ? blockDim.x >> 5 : 1;
-    const int64_t stride = (int64_t)gridDim.x * per_cta;
-    int64_t row = (int64_t)blockIdx.x * per_cta + (warps == 1 ? threadIdx.x >> 5 : 0);
+    const int64_t row = (int64_t)blockIdx.x * per_cta + (warps == 1 ? threadIdx.x >> 5 : 0);
+    if (row >= a.R) return;   // whole warps, and no barrier follows where a CTA has several rows
 
-    // x and the residual of eight values from c on; `stored`: their sum, which has been written
-    struct In { Raw8 x, res; };
-    auto load_in = [&](int64_t row, int c, bool stored) {
-        In in{};
-        const int n = a.H - c;
-        if (n <= 0 || row >= a.R) return in;
-        if (kNorm && stored && a.residual && a.total) {
-            if (a.res_f32) in.res = load8<float, VEC>(static_cast<const float*>(a.total) + row * a.ldt + c, n);
-            else in.x = load8<T, VEC>(static_cast<const T*>(a.total) + row * a.ldt + c, n);
-            return in;
-        }
-        in.x = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + c, n);
-        if (kNorm && a.residual) {
-            if (a.res_f32) in.res = load8<float, VEC>(static_cast<const float*>(a.residual) + row * a.ldr + c, n);
-            else in.res = load8<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr + c, n);
-        }
-        return in;
-    };
-    // r, and its store
-    auto sum_in = [&](int64_t row, const In& in, int c, bool stored, float (&r)[8]) {
-        values<T>(in.x, r);
-        if (!kNorm || !a.residual) return;
-        const int n = a.H - c;
-        if (stored && a.total) {
-            if (a.res_f32) values<float>(in.res, r);
-            return;
-        }
-        float b[8];
-        if (a.res_f32) {
-            values<float>(in.res, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] += b[i];
-            if (!stored && a.total && n > 0)
-                store8<float, VEC>(static_cast<float*>(a.total) + row * a.ldt + c, n, raw_of<float>(r));
-        } else {
-            values<T>(in.res, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] += b[i];
-            const Raw8 sum = raw_of<T>(r);
-            values<T>(sum, r);
-            if (!stored && a.total && n > 0) store8<T, VEC>(static_cast<T*>(a.total) + row * a.ldt + c, n, sum);
-        }
-    };
-    auto times_w = [&](int c, float (&p)[8]) {
-        const int n = a.H - c;
-        if (!kNorm || !a.w || n <= 0) return;
-        float w[8];
-        if (a.w_f32) values<float>(load8<float, VEC>(static_cast<const float*>(a.w) + c, n), w);
-        else values<T>(load8<T, VEC>(static_cast<const T*>(a.w) + c, n), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] *= w[i];
-    };
     auto add_in = [&](int c, const float (&r)[8], float& ss, float& m) {
         if (kNorm)
 #pragma unroll
@@ -494,91 +581,63 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rows8(RmsNormArgs a, int warps) 
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] = r[i];
-            times_w(c, p);
+            times_w<WHAT, T, VEC>(a, c, p);
             m = largest(p, m);
         }
     };
-    auto shrink = [&](float (&r)[8]) {   // rows beyond fp32's range
+    float r[NV][8], ss = 0.0f, mf = 0.0f;
+    for (int c0 = 0; c0 < a.H; c0 += NV * step) {
+        In in[NV];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] *= kTiny;
-    };
-
-    for (; row < a.R; row += stride) {   // the same rows in every thread of a barrier
-        float r[NV][8], ss = 0.0f, mf = 0.0f;
-        for (int c0 = 0; c0 < a.H; c0 += NV * step) {
-            In in[NV];
+        for (int v = 0; v < NV; ++v) in[v] = load_in<WHAT, T, VEC>(a, row, c0 + v * step + 8 * t, false);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) in[v] = load_in(row, c0 + v * step + 8 * t, false);
+        for (int v = 0; v < NV; ++v) sum_in<WHAT, T, VEC>(a, row, in[v], c0 + v * step + 8 * t, false, r[v]);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) sum_in(row, in[v], c0 + v * step + 8 * t, false, r[v]);
-#pragma unroll
-            for (int v = 0; v < NV; ++v) add_in(c0 + v * step + 8 * t, r[v], ss, mf);
-            if (ONE) break;
+        for (int v = 0; v < NV; ++v) add_in(c0 + v * step + 8 * t, r[v], ss, mf);
+        if (ONE) break;
+    }
+    uint32_t m = __float_as_uint(mf);
+    combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
+    if constexpr (kNorm) {
+        if (!(ss < INFINITY)) {   // the same in each thread
+            huge_row<WHAT, T, VEC>(a, row, warps, t, m, s_x, buf);
+            return;
         }
-        uint32_t m = __float_as_uint(mf);
-        combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
-        // beyond fp32's range, or not finite at all; the same in each thread
-        const bool huge = kNorm && !(ss < INFINITY);
-        if (huge) {
-            ss = mf = 0.0f;
-            for (int c0 = 0; c0 < a.H; c0 += NV * step)
+    }
+    const float rstd = kNorm ? rsqrtf(fmaf(ss, a.inv_h, a.eps)) : 1.0f;
+    if (kRowMax) {
+        m = fp8_amax_bits(m);
+        if (t == 0) a.scales[row] = over(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f, 1.0f / 127.0f);
+    }
+    for (int c0 = 0; c0 < a.H; c0 += NV * step) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int c = c0 + v * step + 8 * t;
-                    if (!ONE) sum_in(row, load_in(row, c, true), c, true, r[v]);
-                    shrink(r[v]);
-                    add_in(c, r[v], ss, mf);
-                }
-            m = __float_as_uint(mf);
-            combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
-        }
-        const float rstd = kNorm ? rsqrtf(fmaf(ss, a.inv_h, huge ? 0.0f : a.eps)) : 1.0f;
-        if (kRowMax) {
-            m = fp8_amax_bits(m);
-            if (t == 0) a.scales[row] = over(kNorm ? __uint_as_float(m) * rstd : __uint_as_float(m), 127.0f, 1.0f / 127.0f);
-        }
-        for (int c0 = 0; c0 < a.H; c0 += NV * step) {
+        for (int v = 0; v < NV; ++v) {
+            const int c = c0 + v * step + 8 * t, n = a.H - c;
+            if (!ONE) sum_in<WHAT, T, VEC>(a, row, load_in<WHAT, T, VEC>(a, row, c, true), c, true, r[v]);
+            float p[8];
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = c0 + v * step + 8 * t, n = a.H - c;
-                if (!ONE) {
-                    sum_in(row, load_in(row, c, true), c, true, r[v]);
-                    if (huge) shrink(r[v]);
-                }
-                float p[8];
+            for (int i = 0; i < 8; ++i) p[i] = r[v][i];
+            times_w<WHAT, T, VEC>(a, c, p);
+            uint2 q = make_uint2(0, 0);
+            if (WHAT == kNormE4m3) {   // every lane takes part in the block's maximum
+                uint32_t bm = __float_as_uint(largest(p, 0.0f));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = r[v][i];
-                times_w(c, p);
-                uint2 q = make_uint2(0, 0);
-                if (WHAT == kNormE4m3) {   // every lane takes part in the block's maximum
-                    uint32_t bm = __float_as_uint(largest(p, 0.0f));
-#pragma unroll
-                    for (int o = 8; o >= 1; o >>= 1) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-                    bm = fp8_amax_bits(bm);
-                    q = e4m3_codes(p, bm);
-                    if ((lane & 15) == 0 && n > 0)
-                        a.scales[(int64_t)(c / kFp8Block) * a.R + row] = over(__uint_as_float(bm) * rstd, 448.0f, 1.0f / 448.0f);
-                }
-                if (kRowMax) q = i8_codes(p, m);
-                if (n <= 0) continue;
-                if (WHAT != kNormOnly) {
-                    uint8_t* dst = a.codes + row * a.H + c;
-                    if (VEC) {
-                        *reinterpret_cast<uint2*>(dst) = q;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < n) dst[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
-                    }
-                }
-                if (kNorm && (WHAT == kNormOnly || a.y)) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] *= rstd;
-                    store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy + c, n, raw_of<T>(p));
-                }
+                for (int o = 8; o >= 1; o >>= 1) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+                bm = fp8_amax_bits(bm);
+                q = e4m3_codes(p, bm);
+                if ((lane & 15) == 0 && n > 0)
+                    a.scales[(int64_t)(c / kFp8Block) * a.R + row] = over(__uint_as_float(bm) * rstd, 448.0f, 1.0f / 448.0f);
             }
-            if (ONE) break;
+            if (kRowMax) q = i8_codes(p, m);
+            if (n <= 0) continue;
+            if (WHAT != kNormOnly) store_codes<VEC>(a, row, c, q);
+            if (kNorm && (WHAT == kNormOnly || a.y)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] *= rstd;
+                store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy + c, n, raw_of<T>(p));
+            }
         }
+        if (ONE) break;
     }
 }
 

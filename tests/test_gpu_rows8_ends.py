@@ -6,9 +6,12 @@ import pytest
 import torch
 
 from sparse_moe_layer_row_gb300 import moe_block as mb
+from tests import fp8_ref as F
+from tests.test_gpu_rows8 import NORM_ERR, check, outputs
 
 pytestmark = pytest.mark.gpu
-BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+E4M3 = torch.float8_e4m3fn
+BF, FP = torch.bfloat16, torch.float32
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -79,3 +82,81 @@ def test_product_row_does_not_depend_on_its_batch():
             y = product(xq[:rows[-1]], xs[:rows[-1]], wq, ws, dt)
             for R in rows:
                 assert torch.equal(product(xq[:R], xs[:R], wq, ws, dt), y[:R])
+
+
+# ----------------------------------------------------------------- rows beyond fp32
+
+def huge_rows(R, H, dt, seed=1):
+    """Ordinary rows, whose sum of squares a block of 1e25 takes past fp32, with a block of tiny values."""
+    x = randn(R, H, seed=seed)
+    x[:, :min(128, H // 3)] = 1e25 * (1 + randn(R, min(128, H // 3), seed=seed + 1).abs())
+    x[:, 2 * H // 3:] *= 1e-8
+    return x.to(dt)
+
+
+def check_far(r, w, eps, dt, y, codes, scales):
+    """test_gpu_rows8's check, with scales that may lie below fp32's normal range: the product with rstd
+    and the quotient are rounded to steps of 2^-149 there."""
+    if codes is not None:
+        p = r.double() * (1.0 if w is None else w.double())
+        rstd = torch.rsqrt(r.double().square().mean(1, keepdim=True) + eps)
+        if codes.dtype == torch.int8:
+            s = (p.abs().amax(1, keepdim=True).clamp_min(2.0 ** -100) * rstd / 127.0)[:, 0]
+        else:
+            s = (F.pad_blocks(p).abs().amax(-1).clamp_min(2.0 ** -100) * rstd / 448.0).t()
+        assert torch.all((scales.double() - s).abs() <= 2 * NORM_ERR * s + 2 * 2.0 ** -149)
+        scales = s
+    check(r, w, eps, dt, y, codes, scales)
+
+
+# a row per CTA, rows of CTAs that stay, unaligned rows, rows that are read twice
+HUGE = [(3, 2048), (700, 200), (700, 2048), (700, 7168), (5, 1001), (2, 40000), (2, 33001)]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=str)
+@pytest.mark.parametrize("R,H", HUGE)
+def test_norm_codes_of_rows_beyond_fp32(R, H, dt):
+    """Codes do not depend on the sum of squares: they are those of the plain quantising calls."""
+    x = huge_rows(R, H, dt)
+    want, ws = torch.empty(R, H, dtype=E4M3, device="cuda"), torch.empty(-(-H // 128), R, device="cuda")
+    mb.moe_fp8_quantize(x, want, ws)
+    want8, ws8 = torch.empty(R, H, dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    mb.moe_i8_quantize(x, want8, ws8)
+    for res in (None, torch.zeros(R, H, dtype=dt, device="cuda"), torch.zeros(R, H, device="cuda")):
+        for total in ((None,) if res is None else (None, torch.empty_like(res))):
+            y, q, s = outputs(R, H, dt, "y+e4m3")
+            mb.moe_add_rmsnorm(x, None, 1e-6, residual=res, total=total, y=y, codes=q, scales=s)
+            assert torch.equal(q.view(torch.uint8), want.view(torch.uint8))
+            check_far(x, None, 1e-6, dt, y, q, s)
+            y, q, s = outputs(R, H, dt, "y+i8")
+            mb.moe_add_rmsnorm(x, None, 1e-6, residual=res, total=total, y=y, codes=q, scales=s)
+            assert torch.equal(q, want8)
+            check_far(x, None, 1e-6, dt, y, q, s)
+    if dt == FP:   # the sum is formed again from what is not overwritten yet
+        y, q, s = outputs(R, H, dt, "y+i8")
+        at = x.clone()
+        mb.moe_add_rmsnorm(at, None, 1e-6, residual=torch.zeros_like(x), y=at, codes=q, scales=s)
+        check_far(x, None, 1e-6, dt, at, q, s)
+
+
+@pytest.mark.parametrize("R,H", HUGE)
+def test_norm_products_beyond_fp32(R, H):
+    """r w passes fp32: such blocks (int8: rows) are scaled; the others' codes are those of r w."""
+    x = huge_rows(R, H, FP)
+    x[:, 1] = 3e38
+    w = 1 + 0.2 * randn(H, seed=5)
+    w[:4] = 4.0
+    for out in ("y+e4m3", "y+i8", "y"):
+        y, q, s = outputs(R, H, FP, out)
+        mb.moe_add_rmsnorm(x, w, 1e-6, y=y, codes=q, scales=s)
+        check_far(x, w, 1e-6, FP, y, q, s)
+        assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("R,H", [(400, 8192), (2, 8192), (2, 1 << 16), (2, (1 << 16) + 1)])
+def test_norm_eps_of_rows_beyond_fp32(R, H):
+    """The largest eps counts beside a sum of squares just beyond fp32."""
+    x = randn(R, H, seed=3).sign() * (2.0 ** 128.2 / H) ** 0.5
+    y, q, s = outputs(R, H, FP, "y+i8")
+    mb.moe_add_rmsnorm(x, None, 2.0 ** 100, y=y, codes=q, scales=s)
+    check_far(x, None, 2.0 ** 100, FP, y, q, s)
