@@ -22,8 +22,10 @@
 // 20.6; int8 quantising 9.9 (5.1 TB/s, floor 7.6); with an fp32 residual 31.3 (6.4 TB/s, floor 30.2).
 // Bound by the issue of some 13 instructions a value beside HBM (CTAs that come and go: 29.7 and
 // 12.3).  One row takes 1.7 us; 777 x 1000, fp16 with an fp32 residual and int8 codes, 3.4 (floor 1.3).
-// Sums are fp32: 8 NV squares per thread, then a tree.  A row whose sum of squares overflows is
-// read again and the squares of 2^-80 r summed (huge_row); its codes are those of p all the same.
+// Sums are fp32: 8 NV squares per thread, then a tree; rows read twice add up such pieces and keep
+// what each addition drops (without, constant rows of 2^22 values were off by 1.2e-5, of 2^28 by
+// 4e-4).  A row whose sum of squares overflows is read again and the squares of 2^-80 r are summed
+// (huge_row); its codes are those of p all the same.
 #include <type_traits>
 
 #include "rows8.cuh"
@@ -181,6 +183,17 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&p)[8], uint32_t m) {
                       fp8_pair(w[2].x, w[2].y) | fp8_pair(w[3].x, w[3].y) << 16);
 }
 
+// A sum of many parts: sum + low, where low collects what each addition drops (Knuth's two-sum).
+struct LongSum {
+    float sum = 0.0f, low = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float s = __fadd_rn(sum, v), b = __fsub_rn(s, sum);
+        low += __fadd_rn(__fsub_rn(sum, __fsub_rn(s, b)), __fsub_rn(v, b));
+        sum = s;
+    }
+    __device__ __forceinline__ float value() const { return sum < INFINITY ? sum + low : sum; }
+};
+
 // The row's sum of squares and largest magnitude over the threads that hold it (`warps`
 // warps: the whole CTA, or one warp of several rows'), the same in each of them.  Two buffers,
 // taken in turn: one is written again behind the barrier of the other.
@@ -288,22 +301,25 @@ template <int WHAT, typename T, bool VEC>
 __device__ __noinline__ void huge_row(const RmsNormArgs& a, int64_t row, int warps, int t, uint32_t m, Exchange& x, int buf) {
     constexpr bool kRowMax = WHAT == kNormI8;
     const int step = 256 * warps;
-    float ss = 0.0f, mf = 0.0f;
+    LongSum all;
+    float mf = 0.0f;
 #pragma unroll 1
     for (int c0 = 0; c0 < a.H; c0 += step) {
         const int c = c0 + 8 * t;
-        float r[8];
+        float r[8], ss = 0.0f;
         sum_in<WHAT, T, VEC>(a, row, load_in<WHAT, T, VEC>(a, row, c, true), c, true, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             r[i] *= kTiny;
             ss = fmaf(r[i], r[i], ss);
         }
+        all.add(ss);
         if (kRowMax) {
             times_w<WHAT, T, VEC>(a, c, r);
             mf = largest(r, mf);
         }
     }
+    float ss = all.value();
     uint32_t small = __float_as_uint(mf);
     combine_row<true, kRowMax>(x, buf, ss, small, warps);
     const float rstd = rsqrtf(fmaf(ss, a.inv_h, a.eps * kTiny * kTiny));   // that of 2^-80 r
@@ -586,6 +602,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rows8(const __grid_constant__ Rm
         }
     };
     float r[NV][8], ss = 0.0f, mf = 0.0f;
+    LongSum all;
     for (int c0 = 0; c0 < a.H; c0 += NV * step) {
         In in[NV];
 #pragma unroll
@@ -595,7 +612,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rows8(const __grid_constant__ Rm
 #pragma unroll
         for (int v = 0; v < NV; ++v) add_in(c0 + v * step + 8 * t, r[v], ss, mf);
         if (ONE) break;
+        if (kNorm) {
+            all.add(ss);
+            ss = 0.0f;
+        }
     }
+    if (!ONE && kNorm) ss = all.value();
     uint32_t m = __float_as_uint(mf);
     combine_row<kNorm, kRowMax>(s_x, buf, ss, m, warps);
     if constexpr (kNorm) {

@@ -160,3 +160,17 @@ def test_norm_eps_of_rows_beyond_fp32(R, H):
     y, q, s = outputs(R, H, FP, "y+i8")
     mb.moe_add_rmsnorm(x, None, 2.0 ** 100, y=y, codes=q, scales=s)
     check_far(x, None, 2.0 ** 100, FP, y, q, s)
+
+
+# ------------------------------------------------------------------------- long rows
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 70])
+@pytest.mark.parametrize("H", [1 << 20, (1 << 22) + 8, (1 << 22) + 3, 1 << 26])
+def test_norm_of_long_rows(H, scale):
+    """Rows of equal values, whose serial sum would lose bits, hold the bound of short ones."""
+    for dt in (FP, BF):
+        x = torch.full((1, H), 1.1 * scale, dtype=dt, device="cuda")
+        x[0, ::3] *= -1
+        y, _, _ = outputs(1, H, dt, "y")
+        mb.moe_add_rmsnorm(x, None, 1e-6, y=y)
+        check(x, None, 1e-6, dt, y, None, None)
