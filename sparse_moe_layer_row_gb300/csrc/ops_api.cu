@@ -292,9 +292,9 @@ moe_status moe_add_rmsnorm(const void* x, moe_dtype dtype, int64_t x_stride, int
         return fail(MOE_ERR_INVALID_ARG, "total_stride=%lld is below H=%d", (long long)total_stride, H);
     if (y && y_stride < H) return fail(MOE_ERR_INVALID_ARG, "y_stride=%lld is below H=%d", (long long)y_stride, H);
     if (total && !residual) return fail(MOE_ERR_INVALID_ARG, "total without a residual");
+    if (R == 0) return set_error(MOE_OK, "");   // a buffer of no rows may be NULL
     if ((code_type == MOE_CODES_NONE) != !codes || !codes != !scales)
         return fail(MOE_ERR_INVALID_ARG, "codes and scales go with a code_type, and it with them");
-    if (R == 0) return set_error(MOE_OK, "");
     if (!y && !codes) return fail(MOE_ERR_INVALID_ARG, "neither y nor codes");
     const size_t es = dtype_size(dtype), rs = dtype_size(residual_dtype);
     if (!x || !aligned(x, es)) return fail(MOE_ERR_INVALID_ARG, "x NULL or misaligned");

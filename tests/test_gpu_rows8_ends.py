@@ -174,3 +174,19 @@ def test_norm_of_long_rows(H, scale):
         y, _, _ = outputs(1, H, dt, "y")
         mb.moe_add_rmsnorm(x, None, 1e-6, y=y)
         check(x, None, 1e-6, dt, y, None, None)
+
+
+# --------------------------------------------------------------------------- no rows
+
+def test_calls_of_no_rows():
+    """An empty batch: tensors of no rows, whose pointers are null, are taken by every call."""
+    x = torch.empty(0, 256, dtype=BF, device="cuda")
+    res = torch.empty(0, 256, device="cuda")
+    for out in ("y", "e4m3", "i8", "y+e4m3", "y+i8"):
+        for r in (None, x.clone(), res):
+            y, q, s = outputs(0, 256, BF, out)
+            mb.moe_add_rmsnorm(x, None, 1e-6, residual=r, total=r, y=y, codes=q, scales=s)
+    _, q, s = outputs(0, 256, BF, "i8")
+    mb.moe_i8_quantize(x, q, s)
+    wq, ws = codes(40, 256, -128, 1), torch.ones(40, device="cuda")
+    mb.moe_i8_gemm(q, s, wq, ws, torch.empty(0, 40, device="cuda"), torch.zeros(1024, dtype=torch.uint8, device="cuda"))
