@@ -519,6 +519,13 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
                        int64_t row_stride, void* workspace, size_t workspace_bytes,
                        moe_stream_t stream);
 
+/* Limit of the waits in moe_i8_gemm's pipeline, for tests of the failure path, as
+ * moe_plan_set_wait_limit is for a plan's: after it (built in: 2 s) the kernel counts
+ * MOE_STATUS_WAIT_TIMEOUT, waits for its own copies and MMAs in flight, releases its tensor
+ * memory and ends; that call's y is not valid.  0 restores the built-in limit.  For the
+ * process's calls enqueued after it. */
+moe_status moe_i8_gemm_set_wait_limit(uint64_t limit_ns);
+
 /* ---- Residual addition and root-mean-square norm of rows (no counterpart on the pages:
  * what a model computes between its MoE layers), with the values or their 8-bit codes out.
  *   r = x + residual, rounded to the residual's type (without a residual: r = x)

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
 
 namespace {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far beyond any legal wait (0 in the arguments)
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s when draining after an abort
 constexpr int kThreads = 512, kMaxStages = 7;
 constexpr int kStepK = 128, kRaw = 128 * 128;        // K and bytes of A per stage
@@ -345,6 +345,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
+    const uint64_t limit = a.wait_ns ? a.wait_ns : kWaitLimitNs;
     const int stages = stages_of(a.width);
     const uint32_t b_tile = 128 * a.width, b_off = sbase + stages * kRaw;   // tiles of B behind the codes (1 KB boundaries)
     const uint32_t a_col = kTmemCols - 64 * stages;                         // A's slots behind the accumulators
@@ -381,7 +382,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
         r0 = c * a.width;
         return (min(a.width, C - r0) + 31) / 32 * 32;
     };
-    auto give_up = [&]() {
+    auto give_up = [&]() {   // one lane of a warp
         if (!*abort_flag) { *abort_flag = 1; status_add(a.status, MOE_STATUS_WAIT_TIMEOUT, 1); }
     };
 
@@ -402,7 +403,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
                 int m, r0;
                 const int n = rows_of(u, m, r0);
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, kWaitLimitNs)) {
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, abort_flag, limit)) {
                         give_up();
                         ok = false;
                         break;
@@ -435,7 +436,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 if (__all_sync(0xffffffffu, mbar_test_wait_cluster(smem_u32(bar), parity))) return true;
-                const bool got = mbar_wait_cluster_bounded(bar, parity, abort_flag, kWaitLimitNs);
+                const bool got = mbar_wait_cluster_bounded(bar, parity, abort_flag, limit);
                 if (!__any_sync(0xffffffffu, !got)) return true;
                 if (lane == 0) give_up();
                 return false;
@@ -483,7 +484,7 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
             bool ok = true;
             for (int u = ufirst; ok && u < nunits; u += nact)
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_bounded(bfull + stage, phase, abort_flag, kWaitLimitNs)) {
+                    if (!mbar_wait_bounded(bfull + stage, phase, abort_flag, limit)) {
                         give_up();
                         ok = false;
                         break;
@@ -506,9 +507,9 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
         for (int u = ufirst; ok && u < nunits; u += nact)
             for (int kb = 0; kb < nkb; ++kb) {
                 // codes landed; they were only asked for once the MMA had read the slot
-                const bool got = mbar_wait_bounded(afull + stage, phase, abort_flag, kWaitLimitNs);
+                const bool got = mbar_wait_bounded(afull + stage, phase, abort_flag, limit);
                 if (__any_sync(0xffffffffu, !got)) {
-                    give_up();
+                    if (lane == 0) give_up();
                     ok = false;
                     break;
                 }
@@ -542,9 +543,9 @@ k_i8_tiles(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUte
         float* xs = reinterpret_cast<float*>(base + kScaleOff) + 128 * (warp - 8);
         uint32_t tphase = 0;
         auto accumulators_ready = [&]() {
-            const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, kWaitLimitNs);
+            const bool got = mbar_wait_bounded(tfull, tphase, abort_flag, limit);
             if (__any_sync(0xffffffffu, !got)) {
-                give_up();
+                if (lane == 0) give_up();
                 return false;
             }
             tphase ^= 1u;

@@ -73,6 +73,8 @@ moe_status pairs_ready(int sms, int* clusters) {
     return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
 }
 
+std::atomic<uint64_t> g_i8_wait_ns{0};   // moe_i8_gemm_set_wait_limit
+
 moe_status launched(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return set_error(MOE_OK, "");
@@ -234,6 +236,11 @@ size_t moe_i8_gemm_workspace_bytes(int32_t R, int32_t N, int32_t K) {
     return i8_rows_applies(R, N, K) ? kGemmWorkspace : kWideOffset + 2 * (size_t)(R < N ? R : N) * (size_t)K;
 }
 
+moe_status moe_i8_gemm_set_wait_limit(uint64_t limit_ns) {
+    g_i8_wait_ns.store(limit_ns, std::memory_order_relaxed);
+    return set_error(MOE_OK, "");
+}
+
 moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_t* wq,
                        const float* ws, int32_t N, int32_t K, void* y, moe_dtype dtype,
                        int64_t row_stride, void* workspace, size_t workspace_bytes,
@@ -254,7 +261,8 @@ moe_status moe_i8_gemm(const int8_t* xq, const float* xs, int32_t R, const int8_
     if (workspace_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     I8GemmArgs a{xq, xs, wq, ws, R, N, K, y, row_stride, dtype, static_cast<uint32_t*>(workspace),
-                 aligned(y, 32) && row_stride * (int64_t)dtype_size(dtype) % 32 == 0, i8_width(R, N, K)};
+                 aligned(y, 32) && row_stride * (int64_t)dtype_size(dtype) % 32 == 0, i8_width(R, N, K),
+                 g_i8_wait_ns.load(std::memory_order_relaxed)};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (i8_rows_applies(R, N, K)) return launched(launch_i8_rows(a, st), "gemm launch");
     int sms = 0, clusters = 0;

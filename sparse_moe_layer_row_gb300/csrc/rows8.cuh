@@ -38,6 +38,7 @@ struct I8GemmArgs {
     uint32_t* status;
     int y_vec;                // rows of y begin on 32 bytes
     int width;                // rows of B in a tile: 256, 128 or 64
+    uint64_t wait_ns;         // limit of a wait of the tiles (0: the built-in limit)
 };
 // Few rows or little work: k_i8_rows, which needs no workspace.
 bool i8_rows_applies(int R, int N, int K);

@@ -182,6 +182,8 @@ def load(build_if_missing: bool = False):
     L.moe_i8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
     L.moe_i8_gemm.restype = ctypes.c_int
     L.moe_i8_gemm.argtypes = [P, P, i32, P, P, i32, i32, P, ctypes.c_int, i64, P, sz, P]
+    L.moe_i8_gemm_set_wait_limit.restype = ctypes.c_int
+    L.moe_i8_gemm_set_wait_limit.argtypes = [ctypes.c_uint64]
     L.moe_add_rmsnorm.restype = ctypes.c_int
     L.moe_add_rmsnorm.argtypes = [P, ctypes.c_int, i64, i32, i32, P, ctypes.c_int, i64, P, i64, P,
                                   ctypes.c_int, ctypes.c_float, P, i64, i32, P, P, P]
@@ -727,6 +729,12 @@ def moe_i8_gemm(xq, xs, wq, ws, y, workspace, stream=None):
     _on(dev, load().moe_i8_gemm, xq.data_ptr(), xs.data_ptr(), R, wq.data_ptr(), ws.data_ptr(), N, K,
         y.data_ptr(), _DTYPES[y.dtype], ld, workspace.data_ptr(), workspace.numel(),
         _stream(stream, dev))
+
+
+def moe_i8_gemm_set_wait_limit(limit_ns: int):
+    """The limit of the waits in moe_i8_gemm's pipeline, process-wide (0: built in).  For tests of
+    the failure path."""
+    _check(load().moe_i8_gemm_set_wait_limit(int(limit_ns)))
 
 
 def _or_fp32(t, dtype):

@@ -190,3 +190,34 @@ def test_calls_of_no_rows():
     mb.moe_i8_quantize(x, q, s)
     wq, ws = codes(40, 256, -128, 1), torch.ones(40, device="cuda")
     mb.moe_i8_gemm(q, s, wq, ws, torch.empty(0, 40, device="cuda"), torch.zeros(1024, dtype=torch.uint8, device="cuda"))
+
+
+# -------------------------------------------------------------------------- wait limit
+
+@pytest.mark.parametrize("R,N,K", [(700, 2048, 336), (2048, 700, 2064), (2100, 1900, 16400), (300, 2048, 8208)])
+def test_product_wait_limit(R, N, K):
+    """With a limit of 1 ns the tiles' waits run out: the call returns and counts them, one for a warp
+    that waits at most, and the next call, on the same workspace, is right bit for bit."""
+    xq, wq = codes(R, K, -128, 1), codes(N, K, -128, 2)
+    one = torch.ones(max(R, N), device="cuda")
+    mem = torch.zeros(mb.moe_i8_gemm_workspace_bytes(R, N, K), dtype=torch.uint8, device="cuda")
+    assert mem.numel() > 2 * K * min(R, N)
+    y, want = torch.empty(R, N, device="cuda"), torch.empty(R, N, device="cuda")
+    mb.moe_i8_gemm(xq, one[:R], wq, one[:N], want, mem)
+    torch.cuda.synchronize()
+    assert not any(mb.moe_read_device_status(mem).values())
+    for _ in range(3):
+        mb.moe_i8_gemm_set_wait_limit(1)
+        try:
+            mb.moe_i8_gemm(xq, one[:R], wq, one[:N], y, mem)
+            torch.cuda.synchronize()
+        finally:
+            mb.moe_i8_gemm_set_wait_limit(0)
+        st = mb.moe_read_device_status(mem)
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        assert 0 < st["wait_timeout"] <= 16 * sms, st
+        mb.moe_clear_device_status(mem)
+        y.fill_(float("nan"))
+        mb.moe_i8_gemm(xq, one[:R], wq, one[:N], y, mem)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and not any(mb.moe_read_device_status(mem).values())
