@@ -56,7 +56,11 @@ constexpr int kGroup = 4;                       // warps that share a gate/up un
 constexpr int kGroups = kWarps / kGroup;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxPairs = kTokenRows * 32;      // k <= 32
-constexpr int64_t kPrefetchBytes = 40 << 20;    // of gate/up, and of the down weights: a third of L2 each
+// What goes to L2 ahead, all CTAs' together: of the chosen experts' down weights; of the shared
+// expert's gate/up, and of its down weights.  More than L2 holds is read twice: one row of H 8192,
+// Is 16384 took 190 us with all of the shared expert's, 151 with 10, 20 or 40 MB of either (H 7168, Is
+// 8192 103 and 89; H 2048, Is 512, which is below all of these, 19.2).
+constexpr int64_t kPrefetchBytes = 40 << 20, kSharedPrefetchBytes = 20 << 20;
 
 // A tile: 16 weight rows by 128 bytes of K; a lane holds 32 bytes of two rows.
 template <bool FP8>
@@ -454,11 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_token(TokenArgs a) {
     // the shared expert's weights to L2
     if (tid == kThreads - 1) {
         const uint32_t gb = 8u * a.H * kES, db = 16u * a.Is * kES;
-        for (int t = cta; t < stiles; t += G) {
+        int left = (int)(kSharedPrefetchBytes / G / (2 * gb));
+        for (int t = cta; t < stiles && left > 0; t += G, --left) {
             prefetch_l2(sg + (int64_t)t * gb, gb);
             prefetch_l2(su + (int64_t)t * gb, gb);
         }
-        for (int t = cta; t < dtiles; t += G) prefetch_l2(sd + (int64_t)t * db, db);
+        left = (int)(kSharedPrefetchBytes / G / db);
+        for (int t = cta; t < dtiles && left > 0; t += G, --left) prefetch_l2(sd + (int64_t)t * db, db);
     }
 
     // ---- step 2: the experts of each row and the list of all of them
