@@ -774,7 +774,7 @@ def moe_add_rmsnorm(x, weight, eps, residual=None, total=None, y=None, codes=Non
         ldy = _need_rows_at(y, "y", dev, dt, shape)
         py = y.data_ptr()
     if codes is not None:
-        kind = 2 if codes.dtype == torch.int8 else 1
+        kind = 2 if isinstance(codes, torch.Tensor) and codes.dtype == torch.int8 else 1
         _need_at(codes, "codes", dev, torch.int8 if kind == 2 else torch.float8_e4m3fn, shape)
         _need_at(scales, "scales", dev, torch.float32, (R,) if kind == 2 else (-(-H // 128), R))
         pc, ps = codes.data_ptr(), scales.data_ptr()

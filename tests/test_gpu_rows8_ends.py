@@ -221,3 +221,21 @@ def test_product_wait_limit(R, N, K):
         mb.moe_i8_gemm(xq, one[:R], wq, one[:N], y, mem)
         torch.cuda.synchronize()
         assert torch.equal(y, want) and not any(mb.moe_read_device_status(mem).values())
+
+
+# --------------------------------------------------------------------------- refusals
+
+def test_arguments_that_are_no_tensors_are_named():
+    x = randn(4, 256).to(BF)
+    s, q, w = torch.empty(4, device="cuda"), torch.empty(4, 256, dtype=torch.int8, device="cuda"), torch.empty(0)
+    for kw, word in ((dict(codes=[1], scales=s), "codes"), (dict(codes=q, scales=[1.0]), "scales"), (dict(y="y"), "y"),
+                     (dict(y=x.clone(), residual=1.0), "residual"), (dict(y=x.clone(), residual=x, total=3), "total")):
+        with pytest.raises(TypeError, match=word):
+            mb.moe_add_rmsnorm(x, None, 1e-6, **kw)
+    with pytest.raises(TypeError, match="weight"):
+        mb.moe_add_rmsnorm(x, 1.0, 1e-6, y=x.clone())
+    for args, word in (((None, s, q, s, x, w), "xq"), ((q, None, q, s, x, w), "xs"), ((q, s, 1, s, x, w), "wq")):
+        with pytest.raises(TypeError, match=word):
+            mb.moe_i8_gemm(*args)
+    with pytest.raises(TypeError, match="codes"):
+        mb.moe_i8_quantize(x, None, s)
