@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(256, MINB) k_rows8_many(const __grid_constant_
     } else if (!a.res_f32 || sizeof(T) == 4) {
         if (full) rows_many<WHAT, T, 1, true, NV>(a, warps, s_w, s_x);
         else rows_many<WHAT, T, 1, false, NV>(a, warps, s_w, s_x);
-    } else {
+    } else if constexpr (NV < 4) {   // (launch_t has no such call for four)
         if (full) rows_many<WHAT, T, 2, true, NV>(a, warps, s_w, s_x);
         else rows_many<WHAT, T, 2, false, NV>(a, warps, s_w, s_x);
     }
