@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_i8_rows(I8GemmArgs a) {
         for (int w = 1; w < kWarps; ++w) v += part[w][r][n];
         float sum = (float)v;
         if constexpr (std::is_same_v<Part, float>) {
-            float most = 0.0f;   // no sum on the way exceeds it
+            float most = 0.0f;   // no sum on the way exceeds it (2^24 may have been rounded to)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) most += fabsf(part[w][r][n]);
-            if (most > (float)(1 << 24)) {
+            if (most >= (float)(1 << 24)) {
                 int whole = 0;
                 for (int w = 0; w < kWarps; ++w) whole += (int)part[w][r][n];
                 sum = (float)whole;

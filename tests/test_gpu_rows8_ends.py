@@ -72,6 +72,21 @@ def test_product_sums_past_24_bits(R, N, K, lo):
         assert torch.all((y.double() - acc).abs() <= n * 2.0 ** -23 * mag + 2.0 ** -24 * acc.abs())
 
 
+@pytest.mark.parametrize("R", [7, 12, 25])
+def test_product_of_shares_that_just_pass_24_bits(R):
+    """Four warps' shares add up to 2^24, the next ones are 1 and 1, which fp32 drops one after the other."""
+    K, N = 2048, 40
+    xq, wq = torch.zeros(R, K, dtype=torch.int8, device="cuda"), torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    for b in range(16):   # blocks of 128: warp b % 8's
+        at = slice(128 * b, 128 * b + (128 if b % 8 < 4 else 1))
+        v = -128 if b % 8 < 4 else 1 if b in (4, 5) else 0
+        xq[:, at], wq[:, at] = v, v
+    one = torch.ones(N, device="cuda")
+    acc = xq.double() @ wq.double().t()
+    assert torch.all(acc == 2 ** 24 + 2)
+    assert torch.equal(product(xq, one[:R], wq, one).double(), acc)
+
+
 def test_product_row_does_not_depend_on_its_batch():
     """The same bits alone, with a few rows and among many: past 24 bits on the kernel for few rows,
     below on both."""
