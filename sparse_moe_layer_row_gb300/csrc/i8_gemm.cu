@@ -7,7 +7,7 @@
 // accumulator's last bit, at every addition of 16 products and always towards zero:
 //   k_i8_rows   a warp's share of K is summed in pieces of 1024, none of which passes 2^24, and the
 //               pieces and shares in int32 (shares whose fp32 sum cannot pass 2^24: in fp32): the whole
-//               number for any K.  Costs 0.1 us of 4.5 (32 x 4096 x 2048).
+//               number for any K.  Costs 0.1 us of 4.7 (32 x 4096 x 2048).
 //   k_i8_tiles  parts of 8192 of K, added in fp32: off by (512 + parts) 2^-23 of the addends' magnitudes
 //               at most.  Codes of 100 to 127 at K = 7168: 1.2e-5; in one part K = 131056 had 7.6e-4.
 //               Parts of 1024, exact up to K = 2048, were 3 to 8% slower for every K above 1024
@@ -19,8 +19,8 @@
 // permuted inside a block, alike in both operands, so that a lane's are 16-byte loads and
 // four codes of a row make one MMA's operand.  The warps' sums are added through shared memory.
 // Bound by the round trip to memory (1 x 2048 x 2048 2.1 us, floor 0.6; 8 x 32768 x 2048 13.7 us,
-// 4.9 TB/s of W), with more rows by the conversions and mma.sync (32 x 4096 x 2048 4.5 us,
-// 77 x 1000 x 1104 4.6); mma.sync on int8 there took 911 us for 8192 x 4096 x 2048.
+// 4.9 TB/s of W), with more rows by the conversions and mma.sync (32 x 4096 x 2048 4.7 us,
+// 77 x 1000 x 1104 4.7); mma.sync on int8 there took 911 us for 8192 x 4096 x 2048.
 //
 // k_i8_tiles: tcgen05 kind::f16 (the bf16 rate).  A CTA pair (cta_group::2) takes 256 rows of A by up
 // to 256 of B, where B is the operand with fewer rows:

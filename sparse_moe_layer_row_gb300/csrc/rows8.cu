@@ -18,10 +18,14 @@
 // Between a row's loads and its stores lie the exchange and two passes of arithmetic, some
 // 2 us in which a CTA that comes and goes with its row asks memory for nothing: CTAs stay, and
 // load their next row before the exchange of this one.
-// 8192 x 2048, bf16 with a residual: y 22.5 us (6.0 TB/s, floor 20.2), e4m3 20.8 (5.7, 17.7), int8
-// 20.6; int8 quantising 9.9 (5.1 TB/s, floor 7.6); with an fp32 residual 31.3 (6.4 TB/s, floor 30.2).
-// Bound by the issue of some 13 instructions a value beside HBM (CTAs that come and go: 29.7 and
-// 12.3).  One row takes 1.7 us; 777 x 1000, fp16 with an fp32 residual and int8 codes, 3.4 (floor 1.3).
+// 8192 x 2048, bf16 with a residual: y 22.5 us (6.0 TB/s, floor 20.2), e4m3 20.9 (5.7, 17.7), int8
+// 20.6; int8 quantising 10.0 (5.0 TB/s, floor 7.6); with an fp32 residual 31.0 (6.5 TB/s, floor 30.2);
+// e4m3 without a residual 14.8 (floor 7.6).  CTAs that come and go: 29.7 (e4m3), 12.3 (quantising).
+// What binds codes is latency: 24 instructions a value (quantising: 11), issued in 57% (61%) of a
+// scheduler's cycles by a third of the warps that an SM holds, whose registers a row takes; HBM is
+// at 43% (34%) there.  One row takes 1.7 us; 777 x 1000, fp16 with an fp32 residual and int8 codes,
+// 3.3 (floor 1.3).  Rows off 16 bytes go value by value: 8192 x 1001 19 us (e4m3, floor 3.7) and 42
+// (y with a residual, floor 9.9).
 // Sums are fp32: 8 NV squares per thread, then a tree; rows read twice add up such pieces and keep
 // what each addition drops (without, constant rows of 2^22 values were off by 1.2e-5, of 2^28 by
 // 4e-4).  A row whose sum of squares overflows is read again and the squares of 2^-80 r are summed
@@ -705,7 +709,7 @@ cudaError_t launch_t(const RmsNormArgs& a, int num_sms, cudaStream_t st) {
     if (per_warp == 1) return launch_many<WHAT, T, 1, 4>(a, 1, num_sms, st);
     if (per_warp == 2) return launch_many<WHAT, T, 2, 3>(a, 1, num_sms, st);
     // (an fp32 residual of 16-bit rows takes HBM longer than the arithmetic anyway, and CTAs that
-    // stay were slower there: 8192 x 4096 73.6 us against 63.7)
+    // stay were slower there: 8192 x 4096 73.6 us against 63.7, which are 58.8 by now)
     if (WHAT != kQuantI8 && a.res_f32 && warps(2) <= 32) return launch_as<WHAT, T, true, 2, true, 1024, 1>(a, warps(2), st);
     // (8192 x 2048 with e4m3 codes: two vectors 20.8 us, four 22.4; int8 quantising 13.1 and 11.1)
     if (WHAT != kQuantI8 && warps(2) <= 8) return launch_many<WHAT, T, 2, 3>(a, warps(2), num_sms, st);

@@ -41,8 +41,9 @@
 // reach, and leaves.
 //
 // Measured (replayed in a graph; the calls for any number of rows, which end in the same y, beside):
-// one row 18.8 us (43.5), e4m3 15.0 (31.6), 4 rows 45 (62), e4m3 37 (46), 8 rows 69.5 (89; 366 MB,
-// 5.3 TB/s), e4m3 56 (61).  One row: logits 1.2 us, their way 1.4, top-k 0.8, list 0.8, gate/up 8.2
+// one row 19.0 us (43), e4m3 15.8 (32), 2 rows 28 (48), e4m3 23.6 (37), 4 rows 43 (62), e4m3 34 (44), 8
+// rows 68 (88; 366 MB, 5.3 TB/s), e4m3 53 (58); under a given routing one row 16.7 and 13.9, 8 rows
+// 64 and 48.5.  One row: logits 1.2 us, their way 1.4, top-k 0.8, list 0.8, gate/up 8.2
 // (37.7 MB), barrier 2.2 with what CTAs wait for one another, down 2.7.
 #include "route_common.cuh"
 #include "token.cuh"
